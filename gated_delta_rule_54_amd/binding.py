@@ -24,6 +24,9 @@ ALGOS = {"auto": GDR_ALGO_AUTO, "sequential": GDR_ALGO_SEQUENTIAL,
 # Every symbol include/gdr.h declares.
 SYMBOLS = ("gdr_keeps_chunks", "gdr_forward_workspace", "gdr_backward_workspace", "gdr_forward",
            "gdr_backward", "gdr_forward_noalloc", "gdr_forward_varlen", "gdr_backward_varlen",
+           "gdr_linear_forward_workspace", "gdr_linear_backward_workspace", "gdr_linear_forward",
+           "gdr_linear_backward", "gdr_linear_forward_varlen", "gdr_linear_backward_varlen",
+           "gdr_group_norm_forward", "gdr_group_norm_backward_workspace", "gdr_group_norm_backward",
            "gdr_profile_enable", "gdr_profile_read",
            "gdr_status_str", "gdr_last_hip_error", "gdr_abi_version")
 # Every symbol include/gdr_calib.h declares (device ceilings for the benchmark).
@@ -78,7 +81,19 @@ def lib():
                                           vp, vp, vp, fp, fp, fp, vp, sz, vp]
         L.gdr_calib_copy.argtypes = [vp, vp, sz, vp]
         L.gdr_calib_mfma.argtypes = [vp, ctypes.c_int64, ctypes.c_int64, ctypes.POINTER(ctypes.c_double), vp]
-        for name in ("gdr_keeps_chunks", "gdr_calib_copy", "gdr_calib_mfma",
+        for name in ("gdr_linear_forward_workspace", "gdr_linear_backward_workspace",
+                     "gdr_group_norm_backward_workspace"):
+            getattr(L, name).argtypes = [vp, ctypes.POINTER(sz)]
+        L.gdr_linear_forward.argtypes = [vp] * 9 + [sz, vp]
+        L.gdr_linear_forward_varlen.argtypes = [vp] * 10 + [sz, vp]
+        L.gdr_linear_backward.argtypes = [vp] * 14 + [sz, vp]
+        L.gdr_linear_backward_varlen.argtypes = [vp] * 15 + [sz, vp]
+        L.gdr_group_norm_forward.argtypes = [vp] * 7
+        L.gdr_group_norm_backward.argtypes = [vp] * 11 + [sz, vp]
+        for name in ("gdr_linear_forward_workspace", "gdr_linear_backward_workspace", "gdr_linear_forward",
+                     "gdr_linear_backward", "gdr_linear_forward_varlen", "gdr_linear_backward_varlen",
+                     "gdr_group_norm_forward", "gdr_group_norm_backward_workspace", "gdr_group_norm_backward",
+                     "gdr_keeps_chunks", "gdr_calib_copy", "gdr_calib_mfma",
                      "gdr_forward_workspace", "gdr_backward_workspace",
                      "gdr_forward", "gdr_backward", "gdr_forward_noalloc", "gdr_forward_varlen",
                      "gdr_backward_varlen"):

@@ -1,0 +1,246 @@
+// C entry points of the operators beside the gated delta rule (declared in
+// include/gdr.h): linear attention with a decay for each head, and the group
+// norm of the heads' outputs.  Argument validation, workspace sizes, algorithm
+// choice, launches.  Nothing here allocates, frees or synchronises.
+
+#include <gdr.h>
+
+#include "gdr_linear.h"
+#include "gdr_norm.h"
+
+namespace {
+
+using gdr::LinShape;
+
+bool misaligned(const void* p, uintptr_t a = 16) {
+  return p != nullptr && (reinterpret_cast<uintptr_t>(p) % a) != 0;
+}
+
+bool known(int32_t dtype) { return dtype == GDR_F32 || dtype == GDR_BF16; }
+
+// A row stride: 0 (dense), or at least the row, in whole 16-byte units and
+// small enough for 64-bit byte offsets.
+constexpr int64_t kMaxRow = int64_t(1) << 31;
+gdr_status check_row(int64_t stride, int64_t dense, int32_t dtype) {
+  if (stride == 0) return GDR_OK;
+  if (stride < dense) return GDR_ERR_BAD_SHAPE;
+  if (stride > kMaxRow) return GDR_ERR_UNSUPPORTED;
+  return stride % (dtype == GDR_BF16 ? 8 : 4) ? GDR_ERR_BAD_ALIGNMENT : GDR_OK;
+}
+
+gdr_status check(const gdr_linear_problem* p) {
+  if (!p) return GDR_ERR_NULL_ARG;
+  if (p->B < 0 || p->T < 0 || p->Hk <= 0 || p->Hv <= 0 || p->Dk <= 0 || p->Dv <= 0) return GDR_ERR_BAD_SHAPE;
+  if (p->Hv % p->Hk != 0) return GDR_ERR_BAD_SHAPE;
+  if (p->Dk % 16 || p->Dv % 16 || p->Dk > 256 || p->Dv > 256) return GDR_ERR_UNSUPPORTED;
+  if (!known(p->io_dtype) || !known(p->out_dtype)) return GDR_ERR_UNSUPPORTED;
+  if (p->flags & ~static_cast<uint32_t>(GDR_LINEAR_HEAD_DECAY)) return GDR_ERR_UNSUPPORTED;
+  if (p->algo < GDR_ALGO_AUTO || p->algo > GDR_ALGO_CHUNKED) return GDR_ERR_UNSUPPORTED;
+  const int64_t qk = static_cast<int64_t>(p->Hk) * p->Dk, v = static_cast<int64_t>(p->Hv) * p->Dv;
+  for (gdr_status st : {check_row(p->q_row, qk, p->io_dtype), check_row(p->k_row, qk, p->io_dtype),
+                        check_row(p->v_row, v, p->io_dtype)})
+    if (st != GDR_OK) return st;
+  // grid limits: workgroups are numbered by (segment, b, v-head, slice) in 31 bits
+  if (p->B > 65535 || p->Hv > 65535 || p->T > 0x7fffffffLL) return GDR_ERR_UNSUPPORTED;
+  if (p->B * p->Hv > (1 << 22) || p->B * p->T > 0x7fffffffLL || p->B * p->T * p->Hk > 0x7fffffffLL)
+    return GDR_ERR_UNSUPPORTED;
+  return GDR_OK;
+}
+
+LinShape shape_of(const gdr_linear_problem* p) {
+  LinShape s;
+  s.B = p->B, s.T = p->T, s.Hk = p->Hk, s.Hv = p->Hv, s.Dk = p->Dk, s.Dv = p->Dv;
+  s.io_bf16 = p->io_dtype == GDR_BF16;
+  s.out_bf16 = p->out_dtype == GDR_BF16;
+  s.head_decay = (p->flags & GDR_LINEAR_HEAD_DECAY) != 0;
+  s.q_row = p->q_row ? p->q_row : static_cast<int64_t>(p->Hk) * p->Dk;
+  s.k_row = p->k_row ? p->k_row : static_cast<int64_t>(p->Hk) * p->Dk;
+  s.v_row = p->v_row ? p->v_row : static_cast<int64_t>(p->Hv) * p->Dv;
+  return s;
+}
+
+gdr_status done(hipError_t e) { return e == hipSuccess ? GDR_OK : gdr::record_hip_error(e); }
+
+size_t forward_bytes(const LinShape&) { return 0; }
+size_t backward_bytes(const LinShape& s) {
+  gdr::LinBwdParts parts;
+  return gdr::lin_bwd_parts(s, 1, nullptr, &parts);
+}
+
+gdr_status check_ws(const void* ws, size_t have, size_t need) {
+  if (misaligned(ws, 256)) return GDR_ERR_BAD_ALIGNMENT;
+  if (need == 0) return GDR_OK;
+  if (!ws) return GDR_ERR_NULL_ARG;
+  return have < need ? GDR_ERR_WORKSPACE_TOO_SMALL : GDR_OK;
+}
+
+gdr_status linear_forward(const gdr_linear_problem* p, const int64_t* cu, bool ragged, const void* q, const void* k,
+                          const void* v, const float* g, const float* h0, void* o, float* ht, void* ws,
+                          size_t ws_bytes, void* hip_stream) {
+  gdr_status st = check(p);
+  if (st != GDR_OK) return st;
+  const LinShape s = shape_of(p);
+  const bool empty = s.B == 0 || s.T == 0;
+  if (!empty && (!q || !k || !v || !o)) return GDR_ERR_NULL_ARG;
+  if (ragged && !empty && !cu) return GDR_ERR_NULL_ARG;
+  for (const void* ptr : {q, k, v, static_cast<const void*>(h0), static_cast<const void*>(o),
+                          static_cast<const void*>(ht)})
+    if (misaligned(ptr)) return GDR_ERR_BAD_ALIGNMENT;
+  if (misaligned(g, 4) || misaligned(cu, 8)) return GDR_ERR_BAD_ALIGNMENT;
+  if ((st = check_ws(ws, ws_bytes, empty ? 0 : forward_bytes(s))) != GDR_OK) return st;
+  if (s.B == 0 || (s.T == 0 && (!ht || ht == h0))) return GDR_OK;
+  const gdr::LinFwdArgs a{q, k, v, g, h0, o, ht, cu};
+  return done(gdr::launch_lin_seq(s, gdr::lin_forward_chains(s, a), static_cast<hipStream_t>(hip_stream)));
+}
+
+gdr_status linear_backward(const gdr_linear_problem* p, const int64_t* cu, bool ragged, const void* q, const void* k,
+                           const void* v, const float* g, const float* h0, const void* dout, const float* dht,
+                           void* dq, void* dk, void* dv, float* dg, float* dh0, void* ws, size_t ws_bytes,
+                           void* hip_stream) {
+  gdr_status st = check(p);
+  if (st != GDR_OK) return st;
+  const LinShape s = shape_of(p);
+  const bool empty = s.B == 0 || s.T == 0;
+  if (!empty && (!q || !k || !v || !dout || !dq || !dk || !dv)) return GDR_ERR_NULL_ARG;
+  if (ragged && !empty && !cu) return GDR_ERR_NULL_ARG;
+  if (dg && !g) return GDR_ERR_NULL_ARG;
+  for (const void* ptr : {q, k, v, static_cast<const void*>(h0), dout, static_cast<const void*>(dht),
+                          static_cast<const void*>(dq), static_cast<const void*>(dk), static_cast<const void*>(dv),
+                          static_cast<const void*>(dh0)})
+    if (misaligned(ptr)) return GDR_ERR_BAD_ALIGNMENT;
+  if (misaligned(g, 4) || misaligned(dg, 4) || misaligned(cu, 8)) return GDR_ERR_BAD_ALIGNMENT;
+  if ((st = check_ws(ws, ws_bytes, empty ? 0 : backward_bytes(s))) != GDR_OK) return st;
+  const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+  const gdr::LinBwdArgs a{q, k, v, dout, g, h0, dht, dq, dk, dv, dg, dh0, cu};
+  gdr::LinBwdParts parts;
+  gdr::lin_bwd_parts(s, 1, static_cast<char*>(ws), &parts);
+  if (empty) {
+    if (s.B > 0 && dh0) {  // the state passes through
+      gdr::LinChains all = gdr::lin_backward_chains(s, a, parts), one = all;
+      one.c[0] = all.c[2], one.n = 1, one.T = 0;
+      if (hipError_t e = gdr::launch_lin_seq(s, one, stream); e != hipSuccess) return done(e);
+    }
+    return dg && s.head_decay ? done(gdr::launch_lin_zero(dg, s.Hv, stream)) : GDR_OK;
+  }
+  if (hipError_t e = gdr::launch_lin_seq(s, gdr::lin_backward_chains(s, a, parts), stream); e != hipSuccess)
+    return done(e);
+  return done(gdr::launch_lin_bwd_tail(s, a, parts, 1, s.T, stream));
+}
+
+gdr_status check(const gdr_norm_problem* p) {
+  if (!p) return GDR_ERR_NULL_ARG;
+  if (p->rows < 0 || p->groups <= 0 || p->channels <= 0) return GDR_ERR_BAD_SHAPE;
+  if (p->channels % 8 || p->channels > 512) return GDR_ERR_UNSUPPORTED;
+  if (!known(p->io_dtype) || !known(p->out_dtype)) return GDR_ERR_UNSUPPORTED;
+  if (p->flags & ~static_cast<uint32_t>(GDR_NORM_CENTER | GDR_NORM_SILU | GDR_NORM_SHARED_WEIGHT))
+    return GDR_ERR_UNSUPPORTED;
+  if (!(p->eps >= 0.f)) return GDR_ERR_BAD_SHAPE;
+  if (p->groups > 65535 || p->rows > (int64_t(1) << 40)) return GDR_ERR_UNSUPPORTED;
+  const int64_t row = static_cast<int64_t>(p->groups) * p->channels;
+  gdr_status st = check_row(p->x_row, row, p->io_dtype);
+  return st != GDR_OK ? st : check_row(p->z_row, row, p->io_dtype);
+}
+
+gdr::NormArgs norm_args(const gdr_norm_problem* p) {
+  gdr::NormArgs a{};
+  const int64_t row = static_cast<int64_t>(p->groups) * p->channels;
+  a.rows = p->rows, a.G = p->groups, a.D = p->channels, a.eps = p->eps;
+  a.x_row = p->x_row ? p->x_row : row;
+  a.z_row = p->z_row ? p->z_row : row;
+  a.io_bf16 = p->io_dtype == GDR_BF16, a.out_bf16 = p->out_dtype == GDR_BF16;
+  a.center = p->flags & GDR_NORM_CENTER, a.silu = p->flags & GDR_NORM_SILU;
+  a.shared = p->flags & GDR_NORM_SHARED_WEIGHT;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdr_status gdr_linear_forward_workspace(const gdr_linear_problem* p, size_t* bytes) {
+  const gdr_status st = check(p);
+  if (st != GDR_OK) return st;
+  if (!bytes) return GDR_ERR_NULL_ARG;
+  *bytes = p->B == 0 || p->T == 0 ? 0 : forward_bytes(shape_of(p));
+  return GDR_OK;
+}
+
+gdr_status gdr_linear_backward_workspace(const gdr_linear_problem* p, size_t* bytes) {
+  const gdr_status st = check(p);
+  if (st != GDR_OK) return st;
+  if (!bytes) return GDR_ERR_NULL_ARG;
+  *bytes = p->B == 0 || p->T == 0 ? 0 : backward_bytes(shape_of(p));
+  return GDR_OK;
+}
+
+gdr_status gdr_linear_forward(const gdr_linear_problem* p, const void* q, const void* k, const void* v,
+                              const float* g, const float* h0, void* o, float* ht, void* ws, size_t ws_bytes,
+                              void* hip_stream) {
+  return linear_forward(p, nullptr, false, q, k, v, g, h0, o, ht, ws, ws_bytes, hip_stream);
+}
+
+gdr_status gdr_linear_forward_varlen(const gdr_linear_problem* p, const int64_t* cu_seqlens, const void* q,
+                                     const void* k, const void* v, const float* g, const float* h0, void* o,
+                                     float* ht, void* ws, size_t ws_bytes, void* hip_stream) {
+  return linear_forward(p, cu_seqlens, true, q, k, v, g, h0, o, ht, ws, ws_bytes, hip_stream);
+}
+
+gdr_status gdr_linear_backward(const gdr_linear_problem* p, const void* q, const void* k, const void* v,
+                               const float* g, const float* h0, const void* dout, const float* dht, void* dq,
+                               void* dk, void* dv, float* dg, float* dh0, void* ws, size_t ws_bytes,
+                               void* hip_stream) {
+  return linear_backward(p, nullptr, false, q, k, v, g, h0, dout, dht, dq, dk, dv, dg, dh0, ws, ws_bytes,
+                         hip_stream);
+}
+
+gdr_status gdr_linear_backward_varlen(const gdr_linear_problem* p, const int64_t* cu_seqlens, const void* q,
+                                      const void* k, const void* v, const float* g, const float* h0,
+                                      const void* dout, const float* dht, void* dq, void* dk, void* dv, float* dg,
+                                      float* dh0, void* ws, size_t ws_bytes, void* hip_stream) {
+  return linear_backward(p, cu_seqlens, true, q, k, v, g, h0, dout, dht, dq, dk, dv, dg, dh0, ws, ws_bytes,
+                         hip_stream);
+}
+
+gdr_status gdr_group_norm_forward(const gdr_norm_problem* p, const void* x, const float* weight, const float* bias,
+                                  const void* z, void* y, void* hip_stream) {
+  const gdr_status st = check(p);
+  if (st != GDR_OK) return st;
+  if (z && (p->flags & GDR_NORM_SILU)) return GDR_ERR_UNSUPPORTED;
+  if (p->rows > 0 && (!x || !y)) return GDR_ERR_NULL_ARG;
+  for (const void* ptr : {x, z, static_cast<const void*>(y), static_cast<const void*>(weight),
+                          static_cast<const void*>(bias)})
+    if (misaligned(ptr)) return GDR_ERR_BAD_ALIGNMENT;
+  if (p->rows == 0) return GDR_OK;
+  gdr::NormArgs a = norm_args(p);
+  a.x = x, a.w = weight, a.b = bias, a.z = z, a.y = y;
+  return done(gdr::launch_norm_fwd(a, static_cast<hipStream_t>(hip_stream)));
+}
+
+gdr_status gdr_group_norm_backward_workspace(const gdr_norm_problem* p, size_t* bytes) {
+  const gdr_status st = check(p);
+  if (st != GDR_OK) return st;
+  if (!bytes) return GDR_ERR_NULL_ARG;
+  *bytes = gdr::norm_bwd_workspace(norm_args(p));
+  return GDR_OK;
+}
+
+gdr_status gdr_group_norm_backward(const gdr_norm_problem* p, const void* x, const float* weight, const float* bias,
+                                   const void* z, const void* dy, void* dx, void* dz, float* dweight, float* dbias,
+                                   void* ws, size_t ws_bytes, void* hip_stream) {
+  gdr_status st = check(p);
+  if (st != GDR_OK) return st;
+  if (z && (p->flags & GDR_NORM_SILU)) return GDR_ERR_UNSUPPORTED;
+  if (p->rows > 0 && (!x || !dy || !dx || (z && !dz))) return GDR_ERR_NULL_ARG;
+  for (const void* ptr : {x, z, dy, static_cast<const void*>(dx), static_cast<const void*>(dz),
+                          static_cast<const void*>(weight), static_cast<const void*>(bias),
+                          static_cast<const void*>(dweight), static_cast<const void*>(dbias)})
+    if (misaligned(ptr)) return GDR_ERR_BAD_ALIGNMENT;
+  if (p->rows == 0 && !dweight && !dbias) return GDR_OK;
+  gdr::NormArgs a = norm_args(p);
+  if ((st = check_ws(ws, ws_bytes, dweight || dbias ? gdr::norm_bwd_workspace(a) : 0)) != GDR_OK) return st;
+  a.x = x, a.w = weight, a.b = bias, a.z = z, a.dy = dy;
+  a.dx = dx, a.dz = dz, a.dw = dweight, a.db = dbias, a.part = static_cast<float*>(ws);
+  return done(gdr::launch_norm_bwd(a, static_cast<hipStream_t>(hip_stream)));
+}
+
+}  // extern "C"

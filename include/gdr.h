@@ -234,6 +234,113 @@ gdr_status gdr_backward_varlen(const gdr_problem* p, const int64_t* cu_seqlens,
                                float* dg, float* dbeta, float* dh0, void* ws,
                                size_t ws_bytes, void* hip_stream);
 
+/* ---------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the recurrence above without
+ * its prediction term,
+ *     S_t = alpha_t S_{t-1} + k_t v_t^T  (Dk x Dv),   o_t = S_t^T q_t,
+ * alpha_t = exp(g_t), and its VJP.  The layer that stands beside gated delta
+ * layers in a model: same heads (value head h reads k/q head h / (Hv/Hk)),
+ * same fp32 state [B, Hv, Dk, Dv], same ragged batches, no output scale, q
+ * and k used as given.
+ *
+ * g is [B, T, Hv], or [Hv] with GDR_LINEAR_HEAD_DECAY (one constant factor
+ * per head; dg is then [Hv], summed over all tokens), or NULL (alpha = 1).
+ * Any g, -Inf included (the state is dropped there), is allowed; growth past
+ * the fp32 range gives Inf or NaN.
+ *
+ * Dk and Dv are multiples of 16 up to 256, independent of each other; q_row,
+ * k_row, v_row are the elements between one token's row and the next of q, k
+ * and v (0: dense), so that the three may be column ranges of one projection:
+ * at least H * D, in whole 16-byte units.  Rows of a batch follow each other
+ * at the same distance.  All other tensors are dense, as above.
+ *
+ * Results: sums, the state and everything returned in fp32 (an fp32 o, dq,
+ * dk, dv, and ht, dg, dh0 always) carry fp32 accuracy also from bf16 inputs;
+ * bf16 outputs are rounded once from sums whose matrix-core operands hold 8
+ * bits or more.  Every row past a sequence's end, and rows that no sequence
+ * covers, are neither read nor written.  Inf and NaN inputs propagate; with
+ * GDR_ALGO_CHUNKED they may reach earlier tokens of their chunk of 64.
+ *
+ * GDR_ALGO_SEQUENTIAL runs token by token (decoding, with ht == h0 allowed);
+ * GDR_ALGO_CHUNKED groups tokens for the matrix cores; GDR_ALGO_AUTO picks by
+ * T.  Both take every supported problem. */
+enum { GDR_LINEAR_HEAD_DECAY = 1u };
+
+typedef struct gdr_linear_problem {
+  int64_t B, T;                /* batch (sequences), tokens (bound on them)   */
+  int32_t Hk, Hv;              /* k/q heads, v heads (Hv % Hk == 0)           */
+  int32_t Dk, Dv;              /* key and value head dims                     */
+  int32_t io_dtype;            /* gdr_dtype of q, k, v, dout                  */
+  int32_t out_dtype;           /* gdr_dtype of o, dq, dk, dv                  */
+  uint32_t flags;              /* GDR_LINEAR_HEAD_DECAY                       */
+  int32_t algo;                /* gdr_algo                                    */
+  int64_t q_row, k_row, v_row; /* elements between token rows; 0: dense       */
+} gdr_linear_problem;
+
+gdr_status gdr_linear_forward_workspace(const gdr_linear_problem* p, size_t* bytes);
+gdr_status gdr_linear_backward_workspace(const gdr_linear_problem* p, size_t* bytes);
+
+/* h0 may be NULL (zeros); ht may be NULL (not wanted) and may be h0. */
+gdr_status gdr_linear_forward(const gdr_linear_problem* p, const void* q, const void* k, const void* v,
+                              const float* g, const float* h0, void* o, float* ht, void* ws, size_t ws_bytes,
+                              void* hip_stream);
+
+/* VJP for the loss <dout, o> + <dht, ht>, from the forward's inputs alone.
+ * h0 and dht may be NULL (zeros); dg and dh0 may be NULL (not wanted; without
+ * dg less is computed; dg needs g).  dq and dk are summed over the value
+ * heads that share a key head.  Outputs must not alias inputs. */
+gdr_status gdr_linear_backward(const gdr_linear_problem* p, const void* q, const void* k, const void* v,
+                               const float* g, const float* h0, const void* dout, const float* dht, void* dq,
+                               void* dk, void* dv, float* dg, float* dh0, void* ws, size_t ws_bytes,
+                               void* hip_stream);
+
+/* Ragged batches: cu_seqlens as for gdr_forward_varlen. */
+gdr_status gdr_linear_forward_varlen(const gdr_linear_problem* p, const int64_t* cu_seqlens, const void* q,
+                                     const void* k, const void* v, const float* g, const float* h0, void* o,
+                                     float* ht, void* ws, size_t ws_bytes, void* hip_stream);
+gdr_status gdr_linear_backward_varlen(const gdr_linear_problem* p, const int64_t* cu_seqlens, const void* q,
+                                      const void* k, const void* v, const float* g, const float* h0,
+                                      const void* dout, const float* dht, void* dq, void* dk, void* dv, float* dg,
+                                      float* dh0, void* ws, size_t ws_bytes, void* hip_stream);
+
+/* ---------------------------------------------------------------------------
+ * Group norm of the heads' outputs, with an affine map and an activation:
+ * what a layer does with o of either recurrence.  x is [rows, groups,
+ * channels] (tokens, heads, Dv: channels last); per row and group
+ *     n = (x - mean) (mean (x - mean)^2 + eps)^(-1/2),   u = weight n + bias,
+ *     y = u silu(z)  (z given)  |  silu(u)  (GDR_NORM_SILU)  |  u,
+ * where mean is subtracted only with GDR_NORM_CENTER (without it: the root
+ * mean square).  A row's groups stand alone: a causal model shares no
+ * statistics between tokens.  weight and bias are fp32 [groups, channels], or
+ * [channels] for all groups with GDR_NORM_SHARED_WEIGHT, or NULL (ones,
+ * zeros).  channels is a multiple of 8 up to 512; x_row and z_row are the
+ * elements between rows of x and z (0: dense; in whole 16-byte units).
+ * All arithmetic is fp32, outputs are rounded once.  z together with
+ * GDR_NORM_SILU is GDR_ERR_UNSUPPORTED. */
+enum { GDR_NORM_CENTER = 1u, GDR_NORM_SILU = 2u, GDR_NORM_SHARED_WEIGHT = 4u };
+
+typedef struct gdr_norm_problem {
+  int64_t rows;
+  int32_t groups, channels;
+  int32_t io_dtype;            /* gdr_dtype of x, z, dy                       */
+  int32_t out_dtype;           /* gdr_dtype of y, dx, dz                      */
+  uint32_t flags;              /* GDR_NORM_*                                  */
+  float eps;                   /* >= 0                                        */
+  int64_t x_row, z_row;        /* elements between rows; 0: dense             */
+} gdr_norm_problem;
+
+gdr_status gdr_group_norm_forward(const gdr_norm_problem* p, const void* x, const float* weight, const float* bias,
+                                  const void* z, void* y, void* hip_stream);
+
+/* VJP from the forward's inputs: dx [rows, groups, channels]; dz likewise
+ * (required with z, ignored without); dweight, dbias in the parameters' shape,
+ * fp32, either may be NULL (not wanted; with neither no workspace is needed),
+ * and may be wanted where the parameter itself is NULL. */
+gdr_status gdr_group_norm_backward_workspace(const gdr_norm_problem* p, size_t* bytes);
+gdr_status gdr_group_norm_backward(const gdr_norm_problem* p, const void* x, const float* weight, const float* bias,
+                                   const void* z, const void* dy, void* dx, void* dz, float* dweight, float* dbias,
+                                   void* ws, size_t ws_bytes, void* hip_stream);
+
 /* Per-kernel timing for benchmarks (not for use under graph capture).
  * While enabled, every kernel that gdr_forward / gdr_backward launch from the
  * calling thread is bracketed by a pair of HIP events recorded on the call's
