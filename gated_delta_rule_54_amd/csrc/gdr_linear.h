@@ -45,9 +45,10 @@ struct LinBwdArgs {
   const int64_t* cu;
 };
 
-// Columns of the state that one workgroup of a chain owns.
+// Columns of the state that one workgroup of a chain owns: 64, or a launch's
+// own choice.
 constexpr int kLinSlice = 64;
-__host__ __device__ inline int lin_slices(int D2) { return (D2 + kLinSlice - 1) / kLinSlice; }
+__host__ __device__ inline int lin_slices(int D2, int width = kLinSlice) { return (D2 + width - 1) / width; }
 
 // One chain as its kernels see it.
 struct LinChain {
@@ -65,7 +66,12 @@ struct LinChain {
   int eg;
   float* e;             // [slices][B][Hv][T]
   const float* dot;     // gradient of the last state (element (d1, d2) as for s_in) or null
-  float* xdot;          // [B][Hv][slices]: <last state, dot>; null: not wanted
+  float* xdot;          // [segments][B][Hv][slices]: <last state, dot>; null: not wanted
+  // A sequence cut in segments (chunked): the state each segment starts its
+  // walk from, [B][Hv][segments][Dk * Dv] (elements as for s_in), which then
+  // holds instead of s_in; and the other direction's, which holds instead of dot.
+  const float *seg_in, *seg_dot;
+  int exact;            // chunked, bf16 inputs: the output's sums at fp32 accuracy
 };
 
 struct LinChains {
@@ -77,9 +83,18 @@ struct LinChains {
   int head_decay;       // g is [Hv]
   int out_bf16;
   const int64_t* cu;
+  int64_t segments, seg;  // chunked: segments per sequence and tokens in each
 };
 
 #ifdef __HIPCC__
+// Chain i of a launch, by selects: an indexed kernel argument would be copied
+// to scratch memory.
+__device__ __forceinline__ LinChain lin_chain(const LinChains& a, int i) {
+  LinChain c = a.c[0];
+  if (i == 1) c = a.c[1];
+  if (i == 2) c = a.c[2];
+  return c;
+}
 struct LinSpan {
   int64_t t0, len;
 };
@@ -104,12 +119,30 @@ size_t lin_bwd_parts(const LinShape& s, int64_t segments, char* base, LinBwdPart
 LinChains lin_backward_chains(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p);
 
 // dq, dk summed over the value heads of a key head; dg from e and xdot.
-// Sequences are cut in segments of seg tokens, each with its own xdot.
-hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p, int64_t segments,
-                               int64_t seg, hipStream_t st);
+// Sequences are cut in segments of seg tokens, each with its own xdot; slices
+// of the dq and dk chains.
+hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p, int slices,
+                               int64_t segments, int64_t seg, hipStream_t st);
 
 hipError_t launch_lin_zero(float* p, int n, hipStream_t st);  // p[0 .. n) = 0
 
 hipError_t launch_lin_seq(const LinShape& s, const LinChains& a, hipStream_t st);
+
+// Chunked algorithm.  How a problem is cut, and its workspace: the segments'
+// states (forward: one direction, backward: both) and factors.
+struct LinPlan {
+  int64_t segments, seg;
+  int wide;            // slices of 128 columns instead of 64
+  size_t states, bytes;  // bytes of one direction's segment states; of all
+};
+LinPlan lin_plan(const LinShape& s, bool backward);
+struct LinSegs {
+  float *fwd, *rev;    // [B][Hv][segments][Dk * Dv]
+  float* factor;       // [B][Hv][segments]
+};
+LinSegs lin_segs(const LinPlan& p, bool backward, char* base);
+hipError_t launch_lin_chunk_fwd(const LinShape& s, const LinPlan& p, const LinFwdArgs& a, char* ws, hipStream_t st);
+hipError_t launch_lin_chunk_bwd(const LinShape& s, const LinPlan& p, const LinBwdArgs& a, const LinBwdParts& parts,
+                                char* ws, hipStream_t st);
 
 }  // namespace gdr

@@ -61,10 +61,24 @@ LinShape shape_of(const gdr_linear_problem* p) {
 
 gdr_status done(hipError_t e) { return e == hipSuccess ? GDR_OK : gdr::record_hip_error(e); }
 
-size_t forward_bytes(const LinShape&) { return 0; }
-size_t backward_bytes(const LinShape& s) {
+// Shortest T at which AUTO takes the chunked kernels.
+constexpr int64_t kAutoForwardT = 16, kAutoBackwardT = 16;
+bool chunked(const gdr_linear_problem* p, bool backward) {
+  if (p->algo != GDR_ALGO_AUTO) return p->algo == GDR_ALGO_CHUNKED;
+  return p->T >= (backward ? kAutoBackwardT : kAutoForwardT);
+}
+
+// Workspace of a call: the parts of a backward, then the chunked algorithm's
+// segment states.
+size_t forward_bytes(const gdr_linear_problem* p) {
+  return chunked(p, false) ? gdr::lin_plan(shape_of(p), false).bytes : 0;
+}
+size_t backward_bytes(const gdr_linear_problem* p) {
+  const LinShape s = shape_of(p);
+  const gdr::LinPlan plan = gdr::lin_plan(s, true);
+  const bool chunk = chunked(p, true);
   gdr::LinBwdParts parts;
-  return gdr::lin_bwd_parts(s, 1, nullptr, &parts);
+  return gdr::lin_bwd_parts(s, chunk ? plan.segments : 1, nullptr, &parts) + (chunk ? plan.bytes : 0);
 }
 
 gdr_status check_ws(const void* ws, size_t have, size_t need) {
@@ -87,10 +101,13 @@ gdr_status linear_forward(const gdr_linear_problem* p, const int64_t* cu, bool r
                           static_cast<const void*>(ht)})
     if (misaligned(ptr)) return GDR_ERR_BAD_ALIGNMENT;
   if (misaligned(g, 4) || misaligned(cu, 8)) return GDR_ERR_BAD_ALIGNMENT;
-  if ((st = check_ws(ws, ws_bytes, empty ? 0 : forward_bytes(s))) != GDR_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, empty ? 0 : forward_bytes(p))) != GDR_OK) return st;
   if (s.B == 0 || (s.T == 0 && (!ht || ht == h0))) return GDR_OK;
   const gdr::LinFwdArgs a{q, k, v, g, h0, o, ht, cu};
-  return done(gdr::launch_lin_seq(s, gdr::lin_forward_chains(s, a), static_cast<hipStream_t>(hip_stream)));
+  const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+  if (s.T > 0 && chunked(p, false))
+    return done(gdr::launch_lin_chunk_fwd(s, gdr::lin_plan(s, false), a, static_cast<char*>(ws), stream));
+  return done(gdr::launch_lin_seq(s, gdr::lin_forward_chains(s, a), stream));
 }
 
 gdr_status linear_backward(const gdr_linear_problem* p, const int64_t* cu, bool ragged, const void* q, const void* k,
@@ -109,11 +126,15 @@ gdr_status linear_backward(const gdr_linear_problem* p, const int64_t* cu, bool 
                           static_cast<const void*>(dh0)})
     if (misaligned(ptr)) return GDR_ERR_BAD_ALIGNMENT;
   if (misaligned(g, 4) || misaligned(dg, 4) || misaligned(cu, 8)) return GDR_ERR_BAD_ALIGNMENT;
-  if ((st = check_ws(ws, ws_bytes, empty ? 0 : backward_bytes(s))) != GDR_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, empty ? 0 : backward_bytes(p))) != GDR_OK) return st;
   const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
   const gdr::LinBwdArgs a{q, k, v, dout, g, h0, dht, dq, dk, dv, dg, dh0, cu};
+  const bool chunk = !empty && chunked(p, true);
+  const gdr::LinPlan plan = chunk ? gdr::lin_plan(s, true) : gdr::LinPlan{1, s.T, 0, 0, 0};
   gdr::LinBwdParts parts;
-  gdr::lin_bwd_parts(s, 1, static_cast<char*>(ws), &parts);
+  const size_t used = gdr::lin_bwd_parts(s, plan.segments, static_cast<char*>(ws), &parts);
+  if (chunk)
+    return done(gdr::launch_lin_chunk_bwd(s, plan, a, parts, static_cast<char*>(ws) + used, stream));
   if (empty) {
     if (s.B > 0 && dh0) {  // the state passes through
       gdr::LinChains all = gdr::lin_backward_chains(s, a, parts), one = all;
@@ -124,7 +145,7 @@ gdr_status linear_backward(const gdr_linear_problem* p, const int64_t* cu, bool 
   }
   if (hipError_t e = gdr::launch_lin_seq(s, gdr::lin_backward_chains(s, a, parts), stream); e != hipSuccess)
     return done(e);
-  return done(gdr::launch_lin_bwd_tail(s, a, parts, 1, s.T, stream));
+  return done(gdr::launch_lin_bwd_tail(s, a, parts, gdr::lin_slices(s.Dk), 1, s.T, stream));
 }
 
 gdr_status check(const gdr_norm_problem* p) {
@@ -161,7 +182,7 @@ gdr_status gdr_linear_forward_workspace(const gdr_linear_problem* p, size_t* byt
   const gdr_status st = check(p);
   if (st != GDR_OK) return st;
   if (!bytes) return GDR_ERR_NULL_ARG;
-  *bytes = p->B == 0 || p->T == 0 ? 0 : forward_bytes(shape_of(p));
+  *bytes = p->B == 0 || p->T == 0 ? 0 : forward_bytes(p);
   return GDR_OK;
 }
 
@@ -169,7 +190,7 @@ gdr_status gdr_linear_backward_workspace(const gdr_linear_problem* p, size_t* by
   const gdr_status st = check(p);
   if (st != GDR_OK) return st;
   if (!bytes) return GDR_ERR_NULL_ARG;
-  *bytes = p->B == 0 || p->T == 0 ? 0 : backward_bytes(shape_of(p));
+  *bytes = p->B == 0 || p->T == 0 ? 0 : backward_bytes(p);
   return GDR_OK;
 }
 

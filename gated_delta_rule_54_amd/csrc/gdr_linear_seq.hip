@@ -54,8 +54,12 @@ __global__ __launch_bounds__(256) void lin_seq_kernel(LinChains a) {
   __shared__ float red[2][4][kLinSlice];
   int64_t blk = blockIdx.x;
   int ci = 0;
-  while (ci + 1 < a.n && blk >= a.B * a.Hv * lin_slices(a.c[ci].D2)) blk -= a.B * a.Hv * lin_slices(a.c[ci].D2), ++ci;
-  const LinChain& c = a.c[ci];
+  const int64_t heads = a.B * a.Hv;
+  if (a.n > 1 && blk >= heads * lin_slices(a.c[0].D2)) {
+    blk -= heads * lin_slices(a.c[0].D2), ci = 1;
+    if (blk >= heads * lin_slices(a.c[1].D2)) blk -= heads * lin_slices(a.c[1].D2), ci = 2;
+  }
+  const LinChain c = lin_chain(a, ci);
   const int nsl = lin_slices(c.D2), sl = static_cast<int>(blk % nsl);
   const int64_t bh = blk / nsl;
   const int h = static_cast<int>(bh % a.Hv);
@@ -268,7 +272,7 @@ hipError_t seq_launch(const LinChains& a, int rows, int64_t blocks, hipStream_t 
 LinChains lin_forward_chains(const LinShape& s, const LinFwdArgs& a) {
   LinChains L{};
   const int G = s.Hv / s.Hk;
-  L.n = 1;
+  L.n = 1, L.segments = 1, L.seg = s.T;
   L.B = s.B, L.T = s.T, L.Hv = s.Hv, L.g = a.g, L.head_decay = s.head_decay, L.out_bf16 = s.out_bf16, L.cu = a.cu;
   LinChain& c = L.c[0];
   c.x = a.q, c.xr = s.q_row, c.xg = G;
@@ -283,7 +287,7 @@ LinChains lin_forward_chains(const LinShape& s, const LinFwdArgs& a) {
 size_t lin_bwd_parts(const LinShape& s, int64_t segments, char* base, LinBwdParts* p) {
   size_t off = 0;
   auto take = [&](size_t bytes) {
-    char* at = base + off;
+    char* at = base ? base + off : nullptr;  // null: sizes only
     off += (bytes + 255) / 256 * 256;
     return at;
   };
@@ -302,7 +306,7 @@ LinChains lin_backward_chains(const LinShape& s, const LinBwdArgs& a, const LinB
   LinChains L{};
   const int G = s.Hv / s.Hk;
   const int64_t d_row = static_cast<int64_t>(s.Hv) * s.Dv;
-  L.n = 3;
+  L.n = 3, L.segments = 1, L.seg = s.T;
   L.B = s.B, L.T = s.T, L.Hv = s.Hv, L.g = a.g, L.head_decay = s.head_decay, L.out_bf16 = s.out_bf16, L.cu = a.cu;
   LinChain& q = L.c[0];  // dq
   q.x = a.dout, q.xr = d_row, q.xg = 1;
@@ -333,8 +337,8 @@ LinChains lin_backward_chains(const LinShape& s, const LinBwdArgs& a, const LinB
   return L;
 }
 
-hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p, int64_t segments,
-                               int64_t seg, hipStream_t st) {
+hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p, int slices,
+                               int64_t segments, int64_t seg, hipStream_t st) {
   if (s.Hv != s.Hk) {
     ProfScope prof("linear_group_sum", st);
     const int64_t n = s.B * s.T * s.Hk * (s.Dk / 4);
@@ -351,7 +355,7 @@ hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const Lin
   ProfScope prof("linear_dg", st);
   double* sums = s.head_decay ? p.dgsum : nullptr;
   lin_dg_kernel<<<static_cast<unsigned>(s.B * s.Hv * segments), 256, 0, st>>>(
-      p.eq, p.ek, p.xdot, lin_slices(s.Dk), a.dg, sums, s.B, s.T, s.Hv, segments, seg, a.cu);
+      p.eq, p.ek, p.xdot, slices, a.dg, sums, s.B, s.T, s.Hv, segments, seg, a.cu);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   if (sums) lin_dg_head_kernel<<<s.Hv, 64, 0, st>>>(sums, a.dg, s.B * segments, s.Hv);
   return hipGetLastError();
