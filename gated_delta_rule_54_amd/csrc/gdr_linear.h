@@ -45,10 +45,9 @@ struct LinBwdArgs {
   const int64_t* cu;
 };
 
-// Columns of the state that one workgroup of a chain owns: 64, or a launch's
-// own choice.
+// Columns of the state that one workgroup of a chain owns.
 constexpr int kLinSlice = 64;
-__host__ __device__ inline int lin_slices(int D2, int width = kLinSlice) { return (D2 + width - 1) / width; }
+__host__ __device__ inline int lin_slices(int D2) { return (D2 + kLinSlice - 1) / kLinSlice; }
 
 // One chain as its kernels see it.
 struct LinChain {
@@ -119,10 +118,9 @@ size_t lin_bwd_parts(const LinShape& s, int64_t segments, char* base, LinBwdPart
 LinChains lin_backward_chains(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p);
 
 // dq, dk summed over the value heads of a key head; dg from e and xdot.
-// Sequences are cut in segments of seg tokens, each with its own xdot; slices
-// of the dq and dk chains.
-hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p, int slices,
-                               int64_t segments, int64_t seg, hipStream_t st);
+// Sequences are cut in segments of seg tokens, each with its own xdot.
+hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p, int64_t segments,
+                               int64_t seg, hipStream_t st);
 
 hipError_t launch_lin_zero(float* p, int n, hipStream_t st);  // p[0 .. n) = 0
 
@@ -132,7 +130,6 @@ hipError_t launch_lin_seq(const LinShape& s, const LinChains& a, hipStream_t st)
 // states (forward: one direction, backward: both) and factors.
 struct LinPlan {
   int64_t segments, seg;
-  int wide;            // slices of 128 columns instead of 64
   size_t states, bytes;  // bytes of one direction's segment states; of all
 };
 LinPlan lin_plan(const LinShape& s, bool backward);

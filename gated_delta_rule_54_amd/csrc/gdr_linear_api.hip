@@ -18,10 +18,11 @@ bool misaligned(const void* p, uintptr_t a = 16) {
 
 bool known(int32_t dtype) { return dtype == GDR_F32 || dtype == GDR_BF16; }
 
-// A row stride: 0 (dense), or at least the row, in whole 16-byte units and
-// small enough for 64-bit byte offsets.
-constexpr int64_t kMaxRow = int64_t(1) << 31;
+// A row stride: 0 (dense), or at least the row, in whole 16-byte units; 64 rows
+// of it lie within 2^30 bytes, which 32-bit offsets reach.
+constexpr int64_t kMaxRow = int64_t(1) << 22;
 gdr_status check_row(int64_t stride, int64_t dense, int32_t dtype) {
+  if (dense > kMaxRow) return GDR_ERR_UNSUPPORTED;
   if (stride == 0) return GDR_OK;
   if (stride < dense) return GDR_ERR_BAD_SHAPE;
   if (stride > kMaxRow) return GDR_ERR_UNSUPPORTED;
@@ -38,7 +39,8 @@ gdr_status check(const gdr_linear_problem* p) {
   if (p->algo < GDR_ALGO_AUTO || p->algo > GDR_ALGO_CHUNKED) return GDR_ERR_UNSUPPORTED;
   const int64_t qk = static_cast<int64_t>(p->Hk) * p->Dk, v = static_cast<int64_t>(p->Hv) * p->Dv;
   for (gdr_status st : {check_row(p->q_row, qk, p->io_dtype), check_row(p->k_row, qk, p->io_dtype),
-                        check_row(p->v_row, v, p->io_dtype)})
+                        check_row(p->v_row, v, p->io_dtype),
+                        check_row(0, static_cast<int64_t>(p->Hv) * p->Dk, p->io_dtype)})
     if (st != GDR_OK) return st;
   // grid limits: workgroups are numbered by (segment, b, v-head, slice) in 31 bits
   if (p->B > 65535 || p->Hv > 65535 || p->T > 0x7fffffffLL) return GDR_ERR_UNSUPPORTED;
@@ -130,7 +132,7 @@ gdr_status linear_backward(const gdr_linear_problem* p, const int64_t* cu, bool 
   const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
   const gdr::LinBwdArgs a{q, k, v, dout, g, h0, dht, dq, dk, dv, dg, dh0, cu};
   const bool chunk = !empty && chunked(p, true);
-  const gdr::LinPlan plan = chunk ? gdr::lin_plan(s, true) : gdr::LinPlan{1, s.T, 0, 0, 0};
+  const gdr::LinPlan plan = chunk ? gdr::lin_plan(s, true) : gdr::LinPlan{1, s.T, 0, 0};
   gdr::LinBwdParts parts;
   const size_t used = gdr::lin_bwd_parts(s, plan.segments, static_cast<char*>(ws), &parts);
   if (chunk)
@@ -145,7 +147,7 @@ gdr_status linear_backward(const gdr_linear_problem* p, const int64_t* cu, bool 
   }
   if (hipError_t e = gdr::launch_lin_seq(s, gdr::lin_backward_chains(s, a, parts), stream); e != hipSuccess)
     return done(e);
-  return done(gdr::launch_lin_bwd_tail(s, a, parts, gdr::lin_slices(s.Dk), 1, s.T, stream));
+  return done(gdr::launch_lin_bwd_tail(s, a, parts, 1, s.T, stream));
 }
 
 gdr_status check(const gdr_norm_problem* p) {

@@ -68,23 +68,19 @@ __device__ __forceinline__ double log2_decay(float g) {
   return (g < -128.f ? -128.0 : static_cast<double>(g)) * 1.4426950408889634;
 }
 
-// Matrix-core operands: 8 consecutive steps of the summed index per lane, as
-// 4 + 4 of a 32-step block; C chunk rows, PAD elements between LDS rows.
+// Matrix-core operands: lane group g holds steps 8g .. 8g + 7 of a 32-step
+// block of the summed index.  C chunk rows, PAD elements between LDS rows.
 struct OpB {
   using E = uint16_t;
   static constexpr int C = 64, PAD = 8, PER = 8;  // PER: elements of a 16-byte unit
   typedef bf16x8 F;
-  // row r, columns c .. c+3 and c+16 .. c+19
-  static __device__ __forceinline__ F pair(const E* p) {
-    const bf16x4 a = *reinterpret_cast<const bf16x4*>(p), b = *reinterpret_cast<const bf16x4*>(p + 16);
-    return F{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-  }
   static __device__ __forceinline__ F run(const E* p) { return *reinterpret_cast<const F*>(p); }
-  // Rows k0 + 8g .. +7 of column n0 + lane % 16 of a row-major tile: one
-  // transposing read hands a group of 16 lanes 4 rows of 16 columns.
-  static __device__ __forceinline__ F col(const E* M, int ld, int k0, int n0) {
+  // Rows k0 + 8g .. +7 of column n0 + step (p / 4) + p % 4, p = lane % 16, of
+  // a row-major tile: one transposing read hands a group of 16 lanes 4 rows of
+  // four runs of 4 columns.
+  static __device__ __forceinline__ F col(const E* M, int ld, int k0, int n0, int step) {
     const int p = lane_id() & 15, g = lane_id() >> 4;
-    const E* at = M + (k0 + 8 * g + (p >> 2)) * ld + n0 + 4 * (p & 3);
+    const E* at = M + (k0 + 8 * g + (p >> 2)) * ld + n0 + step * (p & 3);
     const bf16x4 a = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at));
     const bf16x4 b = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 4 * ld)));
     return F{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
@@ -129,20 +125,15 @@ struct OpF {
   using E = float;
   static constexpr int C = 32, PAD = 4, PER = 4;
   struct F { float v[8]; };
-  static __device__ __forceinline__ F pair(const E* p) {
-    F f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f.v[i] = p[i], f.v[4 + i] = p[16 + i];
-    return f;
-  }
   static __device__ __forceinline__ F run(const E* p) {
     F f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) f.v[i] = p[i];
     return f;
   }
-  static __device__ __forceinline__ F col(const E* M, int ld, int k0, int n0) {
-    const E* at = M + (k0 + 8 * (lane_id() >> 4)) * ld + n0 + (lane_id() & 15);
+  static __device__ __forceinline__ F col(const E* M, int ld, int k0, int n0, int step) {
+    const int p = lane_id() & 15;
+    const E* at = M + (k0 + 8 * (lane_id() >> 4)) * ld + n0 + step * (p >> 2) + (p & 3);
     F f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) f.v[i] = at[i * ld];
@@ -169,40 +160,74 @@ struct OpF {
   }
 };
 
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ rsrc_t make_rsrc(const void* p, uint32_t nbytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(nbytes), 0x00020000);
+}
+
+// A chunk's rows of one tensor as a buffer that ends with them: row i of the
+// chunk lies i rows from its start, or, backward in time, n - 1 - i.  Reads
+// outside give zeros, writes are dropped: rows at or past n lie beyond the end
+// either way (backward as negative offsets, which wrap around), and kNone does.
+constexpr uint32_t kNone = 0xf0000000u;
+struct Rows {
+  const char* at;  // row 0 of the segment's walk
+  uint32_t rowb;   // bytes between tokens; a chunk's rows span less than 2^30 bytes
+  uint32_t width;  // bytes of a row that may be touched
+  bool rev;
+  __device__ __forceinline__ rsrc_t chunk(int64_t first, int n) const {
+    const char* lo = rev ? at - (first + n - 1) * rowb : at + first * rowb;
+    return make_rsrc(lo, (n - 1) * rowb + width);
+  }
+  // Offset of row i, from the chunk's n = C form.
+  __device__ __forceinline__ uint32_t row(int i, int C) const { return (rev ? C - 1 - i : i) * rowb; }
+  __device__ __forceinline__ uint32_t shift(int n, int C) const { return rev ? (C - n) * rowb : 0; }
+};
+
 // Rows of a chunk on their way from memory to LDS: 16-byte unit e of the
-// [C][W] tile is loaded by thread e % 256 in round e / 256.  Rows at or past n
-// and columns at or past `units` read as zeros (their loads go to the first
-// row and column instead).
+// [C][W] tile is loaded by thread e % 256 in round e / 256.
 template <typename OP, int W>
 struct Stage {
-  static constexpr int UPR = W / OP::PER, N = (OP::C * UPR + 255) / 256;
-  uint4 r[N];
-  __device__ __forceinline__ void load(const char* base, int64_t row_bytes, int n, int units) {
+  static constexpr int UPR = W / OP::PER, N = OP::C * UPR / 256, STEP = 256 / UPR;
+  static_assert(OP::C * UPR % 256 == 0, "whole rounds");
+  Rows rows;
+  uint32_t off;  // of round 0
+  bool on;       // the thread's columns exist
+  u32x4 r[N];
+  __device__ __forceinline__ void init(const Rows& t) {
+    rows = t;
+    on = 16 * (threadIdx.x % UPR) < t.width;
+    off = rows.row(threadIdx.x / UPR, OP::C) + 16 * (threadIdx.x % UPR);
+  }
+  __device__ __forceinline__ void load(int64_t first, int n) {
+    const rsrc_t b = rows.chunk(first, n);
+    const uint32_t o = off - rows.shift(n, OP::C), step = rows.rev ? -(STEP * rows.rowb) : STEP * rows.rowb;
 #pragma unroll
-    for (int u = 0; u < N; ++u) {
-      const int e = 256 * u + threadIdx.x, row = e / UPR, cu = e % UPR;
-      const bool ok = row < n && cu < units;
-      const uint4 x = *reinterpret_cast<const uint4*>(base + (ok ? row * row_bytes + 16 * cu : 0));
-      r[u] = ok ? x : make_uint4(0, 0, 0, 0);
-    }
+    for (int u = 0; u < N; ++u) r[u] = __builtin_amdgcn_raw_buffer_load_b128(b, on ? o + u * step : kNone, 0, 0);
   }
   __device__ __forceinline__ void store(typename OP::E* dst) const {
+    typename OP::E* p = dst + threadIdx.x / UPR * (W + OP::PAD) + OP::PER * (threadIdx.x % UPR);
 #pragma unroll
-    for (int u = 0; u < N; ++u) {
-      const int e = 256 * u + threadIdx.x, row = e / UPR, cu = e % UPR;
-      if (OP::C * UPR % 256 == 0 || row < OP::C)
-        *reinterpret_cast<uint4*>(dst + row * (W + OP::PAD) + OP::PER * cu) = r[u];
-    }
+    for (int u = 0; u < N; ++u) *reinterpret_cast<u32x4*>(p + u * STEP * (W + OP::PAD)) = r[u];
   }
 };
 
-// The tile (i, j) of index t in the order (0,0) (1,0) (1,1) (2,0) ...
-__device__ __forceinline__ int tri_row(int t) { return t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3; }
+constexpr int kW2 = kLinSlice;  // columns of a workgroup's slice: 16 for each of its four waves
 
-template <typename OP, int D1P, int NCT>
+template <typename OP, int D1P>
 struct Tiles {
-  static constexpr int C = OP::C, LD1 = D1P + OP::PAD, W2 = 64 * NCT, LDZ = W2 + OP::PAD, LDP = C + OP::PAD;
-  static constexpr int MAXNS = std::is_same_v<OP, OpB> ? 3 : 1;
+  static constexpr int C = OP::C, LD1 = D1P + OP::PAD, LDZ = kW2 + OP::PAD, LDP = C + OP::PAD;
+};
+
+// Decay factors of a chunk's rows.
+template <int C>
+struct Decay {
+  double A[C];             // log2, running
+  float fo[C], fz[C];      // 2^A_i, 2^(A_C - A_i)
+  float all;               // 2^A_C
 };
 
 // Where a workgroup works.
@@ -215,193 +240,221 @@ struct Walk {
 };
 
 // One walk over a segment.  NS: operands that P and H enter the output's
-// products as; STATE: only the state is wanted.
-template <typename OP, int D1P, int NCT, int NS, bool STATE>
-__device__ __forceinline__ void walk(const LinChains& a, const Walk& w, f32x4 (&H)[NCT][D1P / 16], double& total,
+// products as; STATE: only the state is wanted.  `total` (in the last wave):
+// the segment's log2 decay.
+//
+// Two barriers a chunk.  Between the first and the second the waves read X, Y,
+// Z and write P; behind the second they read P and write the next chunk's
+// X, Y, Z.  A wave forms the column block of P that has its index, from X
+// fragments that it needs for X H anyway.
+template <typename OP, int D1P, int NS, bool STATE>
+__device__ __forceinline__ void walk(const LinChains& a, const Walk& w, f32x4 (&H)[D1P / 16], double& total,
                                      typename OP::E* Xs, typename OP::E* Ys, typename OP::E* Zs, typename OP::E* Ps,
-                                     double* As, float* fo, float* fz, float* ftot, float (*Es)[OP::C]) {
-  using T = Tiles<OP, D1P, NCT>;
+                                     Decay<OP::C>* Ds, float (*Es)[OP::C]) {
+  using T = Tiles<OP, D1P>;
   using E = typename OP::E;
   using F = typename OP::F;
   constexpr int C = T::C, NI = C / 16, KB = D1P / 32, KS = C / 32, LD1 = T::LD1, LDZ = T::LDZ, LDP = T::LDP;
   constexpr int NU = std::is_same_v<OP, OpB> ? 3 : 1;  // operands the state's update enters as
-  constexpr int ES = static_cast<int>(sizeof(E));
+  constexpr uint32_t ES = sizeof(E);
   const LinChain& c = w.c;
   const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m = lane & 15, g4 = 4 * (lane >> 4);
-  const int wc = 16 * NCT * wave;  // the wave's first column in the slice
-  const int64_t dir = c.rev ? -1 : 1;
-  const int64_t start = w.row0 + (c.rev ? w.len - 1 : 0);
-  const char* xb = static_cast<const char*>(c.x) + (start * c.xr + static_cast<int64_t>(w.h / c.xg) * c.D1) * ES;
-  const char* yb = static_cast<const char*>(c.y) + (start * c.yr + static_cast<int64_t>(w.h / c.yg) * c.D1) * ES;
-  const char* zb =
-      static_cast<const char*>(c.z) + (start * c.zr + static_cast<int64_t>(w.h / c.zg) * c.D2 + w.col0) * ES;
-  const int64_t xrb = dir * c.xr * ES, yrb = dir * c.yr * ES, zrb = dir * c.zr * ES;
-  const int u1 = c.D1 / OP::PER, u2 = min(c.D2 - w.col0, T::W2) / OP::PER;
-  const float* gp = a.g ? a.g + w.h + (a.head_decay ? 0 : start * a.Hv) : nullptr;
-  const int64_t gstep = a.head_decay ? 0 : dir * a.Hv;
-
+  const int wc = 16 * wave;  // the wave's first column in the slice
+  const bool rev = c.rev;
+  const int64_t start = w.row0 + (rev ? w.len - 1 : 0);
+  const int w2 = min(c.D2 - w.col0, kW2);
+  auto rows = [&](const void* p, int64_t stride, int group, int D, int col, int width) {
+    const char* at = static_cast<const char*>(p) + (start * stride + static_cast<int64_t>(w.h / group) * D + col) * ES;
+    return Rows{at, static_cast<uint32_t>(stride) * ES, width * ES, rev};
+  };
   Stage<OP, D1P> sx, sy;
-  Stage<OP, T::W2> sz;
+  Stage<OP, kW2> sz;
+  if constexpr (!STATE) sx.init(rows(c.x, c.xr, c.xg, c.D1, 0, c.D1));
+  sy.init(rows(c.y, c.yr, c.yg, c.D1, 0, c.D1));
+  sz.init(rows(c.z, c.zr, c.zg, c.D2, w.col0, w2));
+  // output rows, and those of e's other factor
+  const bool wide = c.out_partial || !a.out_bf16, has = wc < w2;
+  const uint32_t os = wide ? 4 : 2;
+  Rows ro{}, re{};
+  uint32_t oo = 0, oe = 0;
+  if constexpr (!STATE) {
+    const int64_t orow = c.out_partial ? w.b * a.T + w.t0 + (rev ? w.len - 1 : 0) : start;
+    ro = Rows{static_cast<char*>(c.out) + ((orow * a.Hv + w.h) * c.D2 + w.col0) * os,
+              static_cast<uint32_t>(a.Hv) * c.D2 * os, w2 * os, rev};
+    oo = ro.row(m, C) + (wc + g4) * os;
+    if (c.ex) {
+      re = rows(c.ex, c.er, c.eg, c.D2, w.col0, w2);
+      oe = re.row(m, C) + (wc + g4) * ES;
+    }
+  }
+  const float* gp = a.g ? a.g + w.h + (a.head_decay ? 0 : start * a.Hv) : nullptr;
+  const int64_t gstep = a.head_decay ? 0 : rev ? -a.Hv : a.Hv;
+
   float gn = 0.f;
   auto fetch = [&](int64_t at) {
     const int n = static_cast<int>(min(w.len - at, static_cast<int64_t>(C)));
-    if constexpr (!STATE) sx.load(xb + at * xrb, xrb, n, u1);
-    sy.load(yb + at * yrb, yrb, n, u1);
-    sz.load(zb + at * zrb, zrb, n, u2);
-    if (wave == 0) gn = gp && lane < n ? gp[(at + lane) * gstep] : 0.f;
+    if constexpr (!STATE) sx.load(at, n);
+    sy.load(at, n);
+    sz.load(at, n);
+    if (wave == 3) gn = gp && lane < n ? gp[(at + lane) * gstep] : 0.f;
   };
-  fetch(0);
-  total = 0.0;
-
-  for (int64_t at = 0; at < w.len; at += C) {
-    const int n = static_cast<int>(min(w.len - at, static_cast<int64_t>(C)));
+  auto put = [&]() {
     if constexpr (!STATE) sx.store(Xs);
     sy.store(Ys);
     sz.store(Zs);
-    if (wave == 0) {
-      const double g2 = log2_decay(gn), inc = prefix64(g2), A = c.rev ? inc - g2 : inc;
-      const double all = __shfl(inc, 63, 64);
-      if (lane < C) {
-        As[lane] = A;
-        fo[lane] = __builtin_amdgcn_exp2f(static_cast<float>(A));
-        fz[lane] = __builtin_amdgcn_exp2f(static_cast<float>(all - A));
-      }
-      if (lane == 0) ftot[0] = __builtin_amdgcn_exp2f(static_cast<float>(all));
-      total += all;
+  };
+  auto decays = [&](Decay<C>& d) {  // by the last wave
+    const double g2 = log2_decay(gn), inc = prefix64(g2), A = rev ? inc - g2 : inc, all = __shfl(inc, 63, 64);
+    if (lane < C) {
+      d.A[lane] = A;
+      d.fo[lane] = __builtin_amdgcn_exp2f(static_cast<float>(A));
+      d.fz[lane] = __builtin_amdgcn_exp2f(static_cast<float>(all - A));
     }
-    __syncthreads();
-    if (at + C < w.len) fetch(at + C);
+    if (lane == 0) d.all = __builtin_amdgcn_exp2f(static_cast<float>(all));
+    total += all;
+  };
+  total = 0.0;
+  fetch(0);
+  put();
+  if (wave == 3) decays(Ds[0]);
+  __syncthreads();
 
-    f32x4 O[NCT][NI];
+  int buf = 0;
+  for (int64_t at = 0; at < w.len; at += C, buf ^= 1) {
+    const int n = static_cast<int>(min(w.len - at, static_cast<int64_t>(C)));
+    const bool more = at + C < w.len;
+    const Decay<C>& d = Ds[buf];
+    if (more) fetch(at + C);
+
+    f32x4 O[NI];
     if constexpr (!STATE) {
-      // P, transposed tiles: lane holds rows j = 16 jb + g4 + e of column i = 16 ib + m
-      for (int t = wave; t < NI * (NI + 1) / 2; t += 4) {
-        const int ib = tri_row(t), jb = t - ib * (ib + 1) / 2;
-        f32x4 s{0.f, 0.f, 0.f, 0.f};
+      // X H, and the wave's block of P; both transposed
+      f32x4 S[NI];
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-          s = OP::mma(OP::pair(Ys + (16 * jb + m) * LD1 + 32 * kb + g4),
-                      OP::pair(Xs + (16 * ib + m) * LD1 + 32 * kb + g4), s);
-        const int i = 16 * ib + m, j = 16 * jb + g4;
-        const double Ai = As[i];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          s[e] = j + e <= i ? s[e] * __builtin_amdgcn_exp2f(static_cast<float>(Ai - As[j + e])) : 0.f;
-        OP::template put4<NS>(Ps + i * LDP + j, C * LDP, s);
-      }
-      // e^{A_i} X H, transposed
-#pragma unroll
-      for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-        for (int ib = 0; ib < NI; ++ib) O[ct][ib] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int ib = 0; ib < NI; ++ib) O[ib] = S[ib] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
-        F hf[NCT][NS];
-#pragma unroll
-        for (int ct = 0; ct < NCT; ++ct) {
-          const f32x4 h0 = H[ct][2 * kb], h1 = H[ct][2 * kb + 1];
-          const float x[8] = {h0[0], h0[1], h0[2], h0[3], h1[0], h1[1], h1[2], h1[3]};
-          OP::template split<NS>(hf[ct], x);
-        }
+        F hf[NS];
+        const f32x4 h0 = H[2 * kb], h1 = H[2 * kb + 1];
+        const float x[8] = {h0[0], h0[1], h0[2], h0[3], h1[0], h1[1], h1[2], h1[3]};
+        OP::template split<NS>(hf, x);
+        const F yf = OP::run(Ys + (16 * (wave % NI) + m) * LD1 + 32 * kb + 2 * g4);
 #pragma unroll
         for (int ib = 0; ib < NI; ++ib) {
-          const F xf = OP::pair(Xs + (16 * ib + m) * LD1 + 32 * kb + g4);
+          const F xf = OP::run(Xs + (16 * ib + m) * LD1 + 32 * kb + 2 * g4);
+          if (ib >= wave) S[ib] = OP::mma(yf, xf, S[ib]);
 #pragma unroll
-          for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-            for (int s = NS - 1; s >= 0; --s) O[ct][ib] = OP::mma(hf[ct][s], xf, O[ct][ib]);
+          for (int s = NS - 1; s >= 0; --s) O[ib] = OP::mma(hf[s], xf, O[ib]);
         }
       }
+      // P = S o 2^(A_i - A_j): the lane holds rows j .. j + 3 of column i
+      if (wave < NI) {
+        const int j = 16 * wave + g4;
+        double Aj[4];
 #pragma unroll
-      for (int ib = 0; ib < NI; ++ib) {
-        const float f = fo[16 * ib + m];
+        for (int e = 0; e < 4; ++e) Aj[e] = d.A[j + e];
 #pragma unroll
-        for (int ct = 0; ct < NCT; ++ct)
+        for (int ib = 0; ib < NI; ++ib)
+          if (ib >= wave) {
+            const int i = 16 * ib + m;
+            const double Ai = d.A[i];
+            f32x4 p;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) O[ct][ib][e] *= f;
+            for (int e = 0; e < 4; ++e)
+              p[e] = j + e <= i ? S[ib][e] * __builtin_amdgcn_exp2f(static_cast<float>(Ai - Aj[e])) : 0.f;
+            OP::template put4<NS>(Ps + i * LDP + j, C * LDP, p);
+          }
       }
-      __syncthreads();
     }
 
     // Z as it is for the output, decayed to the chunk's end for the state
-    F zu[KS][NCT][NU];
+    F zf[KS], zu[KS][NU];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      float f[8];
+      zf[ks] = OP::col(Zs, LDZ, 32 * ks, wc, 4);
+      float x[8];
+      OP::widen(x, zf[ks]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = fz[32 * ks + 2 * g4 + i];
-#pragma unroll
-      for (int ct = 0; ct < NCT; ++ct) {
-        const F z = OP::col(Zs, LDZ, 32 * ks, wc + 16 * ct);
-        if constexpr (!STATE) {
-#pragma unroll
-          for (int ib = 2 * ks; ib < NI; ++ib)
-#pragma unroll
-            for (int s = NS - 1; s >= 0; --s)
-              O[ct][ib] = OP::mma(z, OP::run(Ps + s * C * LDP + (16 * ib + m) * LDP + 32 * ks + 2 * g4), O[ct][ib]);
-        }
-        float x[8];
-        OP::widen(x, z);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= f[i];
-        OP::template split<NU>(zu[ks][ct], x);
-      }
+      for (int i = 0; i < 8; ++i) x[i] *= d.fz[32 * ks + 2 * g4 + i];
+      OP::template split<NU>(zu[ks], x);
     }
-    const float ft = ftot[0];
+    const float ft = d.all;
 #pragma unroll
     for (int t = 0; t < D1P / 16; ++t) {
 #pragma unroll
-      for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) H[ct][t][e] *= ft;
+      for (int e = 0; e < 4; ++e) H[t][e] *= ft;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        const F yf = OP::col(Ys, LD1, 32 * ks, 16 * t);
+        // tile t holds rows 32 (t / 2) + 8 g + 4 (t % 2) + e, the order of X's operands
+        const F yf = OP::col(Ys, LD1, 32 * ks, 32 * (t / 2) + 4 * (t % 2), 8);
 #pragma unroll
-        for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-          for (int s = NU - 1; s >= 0; --s) H[ct][t] = OP::mma(yf, zu[ks][ct][s], H[ct][t]);
+        for (int s = NU - 1; s >= 0; --s) H[t] = OP::mma(yf, zu[ks][s], H[t]);
       }
     }
-
     if constexpr (!STATE) {
 #pragma unroll
       for (int ib = 0; ib < NI; ++ib) {
-        const int i = 16 * ib + m;
-        const int64_t row = start + dir * (at + i);
-        float e = 0.f;
+        const float f = d.fo[16 * ib + m];
 #pragma unroll
-        for (int ct = 0; ct < NCT; ++ct) {
-          const int col = w.col0 + wc + 16 * ct + g4;
-          if (i < n && col < c.D2) {
-            const float v[4] = {O[ct][ib][0], O[ct][ib][1], O[ct][ib][2], O[ct][ib][3]};
-            const int64_t orow = c.out_partial ? w.b * a.T + (row - w.row0 + w.t0) : row;
-            const int64_t o = (orow * a.Hv + w.h) * c.D2 + col;
-            if (c.out_partial || !a.out_bf16) {
-              *reinterpret_cast<f32x4*>(static_cast<float*>(c.out) + o) = O[ct][ib];
-            } else {
-              const bf16x4 q{static_cast<__bf16>(v[0]), static_cast<__bf16>(v[1]), static_cast<__bf16>(v[2]),
-                             static_cast<__bf16>(v[3])};
-              *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(c.out) + o) = q;
-            }
-            if (c.ex) {
-              float x[4];
-              ld4<E>(static_cast<const E*>(c.ex) + row * c.er + static_cast<int64_t>(w.h / c.eg) * c.D2 + col, x);
-              e += (x[0] * v[0] + x[1] * v[1]) + (x[2] * v[2] + x[3] * v[3]);
-            }
+        for (int e = 0; e < 4; ++e) O[ib][e] *= f;
+      }
+    }
+    if (more && wave == 3) decays(Ds[buf ^ 1]);
+    __syncthreads();
+    if (more) put();
+
+    if constexpr (!STATE) {
+      rsrc_t be;
+      if (c.ex) be = re.chunk(at, n);
+      float ex[NI][4];
+      if (c.ex) {
+        const uint32_t step = rev ? -(16 * re.rowb) : 16 * re.rowb, at0 = oe - re.shift(n, C);
+#pragma unroll
+        for (int ib = 0; ib < NI; ++ib) {
+          const uint32_t o = has ? at0 + ib * step : kNone;
+          if constexpr (ES == 2) {
+            const u32x2 u = __builtin_amdgcn_raw_buffer_load_b64(be, o, 0, 0);
+            ex[ib][0] = __uint_as_float(u[0] << 16), ex[ib][1] = __uint_as_float(u[0] & 0xffff0000u);
+            ex[ib][2] = __uint_as_float(u[1] << 16), ex[ib][3] = __uint_as_float(u[1] & 0xffff0000u);
+          } else {
+            const u32x4 u = __builtin_amdgcn_raw_buffer_load_b128(be, o, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ex[ib][e] = __uint_as_float(static_cast<unsigned>(u[e]));
           }
         }
+      }
+      // O += P Z
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int ib = 2 * ks; ib < NI; ++ib)
+#pragma unroll
+          for (int s = NS - 1; s >= 0; --s)
+            O[ib] = OP::mma(zf[ks], OP::run(Ps + s * C * LDP + (16 * ib + m) * LDP + 32 * ks + 2 * g4), O[ib]);
+      const rsrc_t bo = ro.chunk(at, n);
+      const uint32_t step = rev ? -(16 * ro.rowb) : 16 * ro.rowb, at0 = oo - ro.shift(n, C);
+#pragma unroll
+      for (int ib = 0; ib < NI; ++ib) {
+        const uint32_t o = has ? at0 + ib * step : kNone;
+        if (wide) {
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[ib]), bo, o, 0, 0);
+        } else {
+          const bf16x4 v{static_cast<__bf16>(O[ib][0]), static_cast<__bf16>(O[ib][1]), static_cast<__bf16>(O[ib][2]),
+                         static_cast<__bf16>(O[ib][3])};
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, v), bo, o, 0, 0);
+        }
         if (c.ex) {
-          e = rows4_sum(e);
-          if (lane < 16) Es[wave][i] = e;
+          const float e = rows4_sum((ex[ib][0] * O[ib][0] + ex[ib][1] * O[ib][1]) +
+                                    (ex[ib][2] * O[ib][2] + ex[ib][3] * O[ib][3]));
+          if (lane < 16) Es[wave][16 * ib + m] = e;
         }
       }
     }
     __syncthreads();
     if constexpr (!STATE) {
       if (c.ex && tid < n) {
-        const int64_t t = c.rev ? w.t0 + w.len - 1 - at - tid : w.t0 + at + tid;
+        const int64_t t = rev ? w.t0 + w.len - 1 - at - tid : w.t0 + at + tid;
         c.e[(w.sl * a.B * a.Hv + w.bh) * a.T + t] = (Es[0][tid] + Es[1][tid]) + (Es[2][tid] + Es[3][tid]);
       }
     }
@@ -417,10 +470,9 @@ __device__ __forceinline__ int64_t xcd_index() {
 
 // Finds the workgroup's place; false: nothing to do.  Slices are fastest (of
 // all chains of a head), then heads, then sequences, then segments.
-template <int W2>
 __device__ __forceinline__ bool find(const LinChains& a, Walk& w) {
-  const int n0 = lin_slices(a.c[0].D2, W2), n1 = a.n > 1 ? lin_slices(a.c[1].D2, W2) : 0,
-            n2 = a.n > 2 ? lin_slices(a.c[2].D2, W2) : 0, all = n0 + n1 + n2;
+  const int n0 = lin_slices(a.c[0].D2), n1 = a.n > 1 ? lin_slices(a.c[1].D2) : 0,
+            n2 = a.n > 2 ? lin_slices(a.c[2].D2) : 0, all = n0 + n1 + n2;
   const int64_t k = xcd_index();
   int s = static_cast<int>(k % all);
   const int64_t r = k / all;
@@ -429,7 +481,7 @@ __device__ __forceinline__ bool find(const LinChains& a, Walk& w) {
   s -= ci == 0 ? 0 : ci == 1 ? n0 : n0 + n1;
   w.c = lin_chain(a, ci);
   w.sl = s;
-  w.col0 = s * W2;
+  w.col0 = s * kW2;
   w.bh = r % (a.B * a.Hv);
   w.seg = r / (a.B * a.Hv);
   w.h = static_cast<int>(w.bh % a.Hv);
@@ -445,75 +497,68 @@ __device__ __forceinline__ bool find(const LinChains& a, Walk& w) {
   return true;
 }
 
-// Element (d1, d2) of a state for lane's accumulator element e of tile t.
-template <int D1P, int NCT, typename F>
+// Element (d1, d2) of a state for the lane's accumulator tile t (rows d1 ..
+// d1 + 3 are its elements).
+template <int D1P, typename F>
 __device__ __forceinline__ void each_state(const LinChain& c, int col0, F&& f) {
-  const int lane = lane_id(), wave = threadIdx.x >> 6, m = lane & 15, g4 = 4 * (lane >> 4);
+  const int lane = lane_id(), d2 = col0 + 16 * static_cast<int>(threadIdx.x >> 6) + (lane & 15);
 #pragma unroll
-  for (int ct = 0; ct < NCT; ++ct) {
-    const int d2 = col0 + 16 * (NCT * wave + ct) + m;
-#pragma unroll
-    for (int t = 0; t < D1P / 16; ++t) {
-      const int d1 = 16 * t + g4;
-      if (d2 < c.D2 && d1 < c.D1) f(ct, t, static_cast<int64_t>(d1) * c.s1 + static_cast<int64_t>(d2) * c.s2);
-    }
+  for (int t = 0; t < D1P / 16; ++t) {
+    const int d1 = 32 * (t / 2) + 8 * (lane >> 4) + 4 * (t % 2);
+    if (d2 < c.D2 && d1 < c.D1) f(t, static_cast<int64_t>(d1) * c.s1 + static_cast<int64_t>(d2) * c.s2);
   }
 }
 
-template <typename OP, int D1P, int NCT, int NS0, int NS1>
-__global__ __launch_bounds__(256) void lin_chunk_kernel(LinChains a) {
-  using T = Tiles<OP, D1P, NCT>;
+template <typename OP, int D1P, int NS0, int NS1>
+__global__ __launch_bounds__(256, D1P <= 128 ? 2 : 1) void lin_chunk_kernel(LinChains a) {
+  using T = Tiles<OP, D1P>;
   using E = typename OP::E;
   constexpr int C = T::C, NSM = NS0 > NS1 ? NS0 : NS1;
   __shared__ __align__(16) E Xs[C * T::LD1], Ys[C * T::LD1], Zs[C * T::LDZ], Ps[NSM * C * T::LDP];
-  __shared__ __align__(16) double As[C];
-  __shared__ __align__(16) float fo[C], fz[C], ftot[1], Es[4][C];
+  __shared__ __align__(16) Decay<C> Ds[2];
+  __shared__ __align__(16) float Es[4][C];
   Walk w;
-  if (!find<T::W2>(a, w)) return;
+  if (!find(a, w)) return;
   const LinChain& c = w.c;
   const int64_t one = static_cast<int64_t>(c.D1) * c.D2;
-  // the blocks of P above the diagonal that a 32-step product reads
+  // the blocks of P above the diagonal that a 32-step product reads stay zero
   for (int e = threadIdx.x; e < NSM * C * T::LDP; e += 256) Ps[e] = E(0);
 
-  f32x4 H[NCT][D1P / 16];
+  f32x4 H[D1P / 16];
 #pragma unroll
-  for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-    for (int t = 0; t < D1P / 16; ++t) H[ct][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < D1P / 16; ++t) H[t] = f32x4{0.f, 0.f, 0.f, 0.f};
   const float* in = c.seg_in ? c.seg_in + (w.bh * a.segments + w.seg) * one : c.s_in ? c.s_in + w.bh * one : nullptr;
   if (in)
-    each_state<D1P, NCT>(c, w.col0, [&](int ct, int t, int64_t at) {
+    each_state<D1P>(c, w.col0, [&](int t, int64_t at) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) H[ct][t][e] = in[at + static_cast<int64_t>(e) * c.s1];
+      for (int e = 0; e < 4; ++e) H[t][e] = in[at + static_cast<int64_t>(e) * c.s1];
     });
   double total;
   if (w.len > 0) {
-    if (NS0 == NS1 || c.exact)
-      walk<OP, D1P, NCT, NS0, false>(a, w, H, total, Xs, Ys, Zs, Ps, As, fo, fz, ftot, Es);
-    else
-      walk<OP, D1P, NCT, NS1, false>(a, w, H, total, Xs, Ys, Zs, Ps, As, fo, fz, ftot, Es);
+    if (NS0 == NS1 || c.exact) walk<OP, D1P, NS0, false>(a, w, H, total, Xs, Ys, Zs, Ps, Ds, Es);
+    else walk<OP, D1P, NS1, false>(a, w, H, total, Xs, Ys, Zs, Ps, Ds, Es);
   }
   if (c.xdot) {
     const float* dot = c.seg_dot ? c.seg_dot + (w.bh * a.segments + w.seg) * one : c.dot ? c.dot + w.bh * one : nullptr;
     float s = 0.f;
     if (dot)
-      each_state<D1P, NCT>(c, w.col0, [&](int ct, int t, int64_t at) {
+      each_state<D1P>(c, w.col0, [&](int t, int64_t at) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s += H[ct][t][e] * dot[at + static_cast<int64_t>(e) * c.s1];
+        for (int e = 0; e < 4; ++e) s += H[t][e] * dot[at + static_cast<int64_t>(e) * c.s1];
       });
     s = rows4_sum(row16_sum(s));
     __syncthreads();
     if (lane_id() == 0) Es[threadIdx.x >> 6][0] = s;
     __syncthreads();
     if (threadIdx.x == 0)
-      c.xdot[(w.seg * a.B * a.Hv + w.bh) * lin_slices(c.D2, T::W2) + w.sl] =
+      c.xdot[(w.seg * a.B * a.Hv + w.bh) * lin_slices(c.D2) + w.sl] =
           (Es[0][0] + Es[1][0]) + (Es[2][0] + Es[3][0]);
   }
   if (c.s_out && w.last) {
     float* out = c.s_out + w.bh * one;
-    each_state<D1P, NCT>(c, w.col0, [&](int ct, int t, int64_t at) {
+    each_state<D1P>(c, w.col0, [&](int t, int64_t at) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) out[at + static_cast<int64_t>(e) * c.s1] = H[ct][t][e];
+      for (int e = 0; e < 4; ++e) out[at + static_cast<int64_t>(e) * c.s1] = H[t][e];
     });
   }
 }
@@ -522,32 +567,29 @@ __global__ __launch_bounds__(256) void lin_chunk_kernel(LinChains a) {
 // direction), from zero.  The last segment's is not needed.  The chain forward
 // in time leaves the segments' factors, but the last one's, which only the
 // chain backward in time needs and leaves.
-template <typename OP, int D1P, int NCT>
-__global__ __launch_bounds__(256) void lin_segment_kernel(LinChains a, float* factor) {
-  using T = Tiles<OP, D1P, NCT>;
+template <typename OP, int D1P>
+__global__ __launch_bounds__(256, 2) void lin_segment_kernel(LinChains a, float* factor) {
+  using T = Tiles<OP, D1P>;
   using E = typename OP::E;
   constexpr int C = T::C;
   __shared__ __align__(16) E Ys[C * T::LD1], Zs[C * T::LDZ];
-  __shared__ __align__(16) double As[C];
-  __shared__ __align__(16) float fo[C], fz[C], ftot[1];
+  __shared__ __align__(16) Decay<C> Ds[2];
   Walk w;
-  if (!find<T::W2>(a, w) || w.last) return;
+  if (!find(a, w) || w.last) return;
   const LinChain& c = w.c;
   const int64_t one = static_cast<int64_t>(c.D1) * c.D2;
-  f32x4 H[NCT][D1P / 16];
+  f32x4 H[D1P / 16];
 #pragma unroll
-  for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-    for (int t = 0; t < D1P / 16; ++t) H[ct][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  double total = 0.0;
-  if (w.len > 0) walk<OP, D1P, NCT, 1, true>(a, w, H, total, nullptr, Ys, Zs, nullptr, As, fo, fz, ftot, nullptr);
+  for (int t = 0; t < D1P / 16; ++t) H[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  double total;
+  walk<OP, D1P, 1, true>(a, w, H, total, nullptr, Ys, Zs, nullptr, Ds, nullptr);
   const int64_t at0 = w.bh * a.segments + w.seg;
-  if ((!c.rev || w.first) && w.sl == 0 && threadIdx.x == 0)
+  if ((!c.rev || w.first) && w.sl == 0 && threadIdx.x == 192)
     factor[at0] = __builtin_amdgcn_exp2f(static_cast<float>(total));
   float* out = c.s_out + at0 * one;
-  each_state<D1P, NCT>(c, w.col0, [&](int ct, int t, int64_t at) {
+  each_state<D1P>(c, w.col0, [&](int t, int64_t at) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) out[at + static_cast<int64_t>(e) * c.s1] = H[ct][t][e];
+    for (int e = 0; e < 4; ++e) out[at + static_cast<int64_t>(e) * c.s1] = H[t][e];
   });
 }
 
@@ -577,14 +619,18 @@ __global__ __launch_bounds__(256) void lin_scan_kernel(float* fwd, float* rev, c
   }
 }
 
-// Cutting sequences: workgroups wanted in the launch, the shortest segment,
-// and whether slices of 128 columns are taken where that saves workgroups.
-constexpr int64_t kTargetGroups = 512, kMinSegment = 256;
-constexpr int kWide = 1;
+// Cutting sequences: workgroups wanted in the launch, the shortest segment.
+#ifndef TG
+#define TG 512
+#endif
+#ifndef MS
+#define MS 256
+#endif
+constexpr int64_t kTargetGroups = TG, kMinSegment = MS;
 
-int64_t chunk_blocks(const LinChains& a, int W2) {
+int64_t chunk_blocks(const LinChains& a) {
   int64_t all = 0;
-  for (int i = 0; i < a.n; ++i) all += lin_slices(a.c[i].D2, W2);
+  for (int i = 0; i < a.n; ++i) all += lin_slices(a.c[i].D2);
   return (all * a.B * a.Hv * a.segments + 7) / 8 * 8;
 }
 
@@ -594,37 +640,32 @@ int max_d1(const LinChains& a) {
   return d;
 }
 
-template <typename OP, int D1P, int NCT>
+template <typename OP, int D1P>
 hipError_t run_chunks(const LinChains& a, bool exact, bool mixed, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(chunk_blocks(a, 64 * NCT)));
+  const dim3 grid(static_cast<unsigned>(chunk_blocks(a)));
   if constexpr (std::is_same_v<OP, OpF>) {
-    lin_chunk_kernel<OP, D1P, NCT, 1, 1><<<grid, 256, 0, st>>>(a);
+    lin_chunk_kernel<OP, D1P, 1, 1><<<grid, 256, 0, st>>>(a);
   } else {
-    if (mixed) lin_chunk_kernel<OP, D1P, NCT, 3, 1><<<grid, 256, 0, st>>>(a);
-    else if (exact) lin_chunk_kernel<OP, D1P, NCT, 3, 3><<<grid, 256, 0, st>>>(a);
-    else lin_chunk_kernel<OP, D1P, NCT, 1, 1><<<grid, 256, 0, st>>>(a);
+    if (mixed) lin_chunk_kernel<OP, D1P, 3, 1><<<grid, 256, 0, st>>>(a);
+    else if (exact) lin_chunk_kernel<OP, D1P, 3, 3><<<grid, 256, 0, st>>>(a);
+    else lin_chunk_kernel<OP, D1P, 1, 1><<<grid, 256, 0, st>>>(a);
   }
   return hipGetLastError();
 }
 
-template <typename OP, int D1P, int NCT>
+template <typename OP, int D1P>
 hipError_t run_segments(const LinChains& a, float* factor, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(chunk_blocks(a, 64 * NCT)));
-  lin_segment_kernel<OP, D1P, NCT><<<grid, 256, 0, st>>>(a, factor);
+  lin_segment_kernel<OP, D1P><<<static_cast<unsigned>(chunk_blocks(a)), 256, 0, st>>>(a, factor);
   return hipGetLastError();
 }
 
-// Calls f with the kernel types for a launch's operands: integral constants
-// for the padded width and the column tiles per wave.
+// Calls f with the operand type and the padded width (an integral constant).
 template <typename F>
-hipError_t by_type(bool io_bf16, int d1, int wide, F&& f) {
+hipError_t by_type(bool io_bf16, int d1, F&& f) {
   auto width = [&](auto op) {
-    using OP = decltype(op);
-    if (d1 <= 64) return wide ? f(op, std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{})
-                              : f(op, std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
-    if (d1 <= 128) return wide ? f(op, std::integral_constant<int, 128>{}, std::integral_constant<int, 2>{})
-                               : f(op, std::integral_constant<int, 128>{}, std::integral_constant<int, 1>{});
-    return f(OP{}, std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
+    if (d1 <= 64) return f(op, std::integral_constant<int, 64>{});
+    if (d1 <= 128) return f(op, std::integral_constant<int, 128>{});
+    return f(op, std::integral_constant<int, 256>{});
   };
   return io_bf16 ? width(OpB{}) : width(OpF{});
 }
@@ -634,12 +675,9 @@ hipError_t by_type(bool io_bf16, int d1, int wide, F&& f) {
 // One direction's segment states, then their factors.
 LinPlan lin_plan(const LinShape& s, bool backward) {
   LinPlan p{};
-  const int wide_slices = backward ? 2 * lin_slices(s.Dk, 128) + lin_slices(s.Dv, 128) : lin_slices(s.Dv, 128);
   const int slices = backward ? 2 * lin_slices(s.Dk) + lin_slices(s.Dv) : lin_slices(s.Dv);
   const int64_t heads = std::max<int64_t>(1, s.B * s.Hv);
-  const bool can = std::max(s.Dk, s.Dv) <= 128 && wide_slices < slices;
-  p.wide = can ? kWide : 0;
-  const int64_t groups = heads * (p.wide ? wide_slices : slices);
+  const int64_t groups = heads * slices;
   const int64_t want = (kTargetGroups + groups - 1) / groups, most = (s.T + kMinSegment - 1) / kMinSegment;
   const int64_t n = std::max<int64_t>(1, std::min(want, most));
   p.seg = std::max<int64_t>(64, ((s.T + n - 1) / n + 63) / 64 * 64);
@@ -669,8 +707,8 @@ hipError_t segment_states(const LinShape& s, const LinPlan& p, const LinSegs& g,
   a.segments = p.segments, a.seg = p.seg;
   {
     ProfScope prof("linear_segments", st);
-    hipError_t e = by_type(s.io_bf16, max_d1(a), p.wide, [&](auto op, auto d1, auto nct) {
-      return run_segments<decltype(op), decltype(d1)::value, decltype(nct)::value>(a, g.factor, st);
+    hipError_t e = by_type(s.io_bf16, max_d1(a), [&](auto op, auto d1) {
+      return run_segments<decltype(op), decltype(d1)::value>(a, g.factor, st);
     });
     if (e != hipSuccess) return e;
   }
@@ -697,8 +735,8 @@ hipError_t launch_lin_chunk_fwd(const LinShape& s, const LinPlan& p, const LinFw
   }
   ProfScope prof("linear_chunks", st);
   a.c[0].exact = !s.out_bf16;
-  return by_type(s.io_bf16, s.Dk, p.wide, [&](auto op, auto d1, auto nct) {
-    return run_chunks<decltype(op), decltype(d1)::value, decltype(nct)::value>(a, !s.out_bf16, false, st);
+  return by_type(s.io_bf16, s.Dk, [&](auto op, auto d1) {
+    return run_chunks<decltype(op), decltype(d1)::value>(a, !s.out_bf16, false, st);
   });
 }
 
@@ -723,12 +761,12 @@ hipError_t launch_lin_chunk_bwd(const LinShape& s, const LinPlan& p, const LinBw
   a.c[2].exact = all;
   {
     ProfScope prof("linear_chunks_vjp", st);
-    const hipError_t e = by_type(s.io_bf16, max_d1(a), p.wide, [&](auto op, auto d1, auto nct) {
-      return run_chunks<decltype(op), decltype(d1)::value, decltype(nct)::value>(a, all, some && !all, st);
+    const hipError_t e = by_type(s.io_bf16, max_d1(a), [&](auto op, auto d1) {
+      return run_chunks<decltype(op), decltype(d1)::value>(a, all, some && !all, st);
     });
     if (e != hipSuccess) return e;
   }
-  return launch_lin_bwd_tail(s, args, parts, lin_slices(s.Dk, p.wide ? 128 : 64), p.segments, p.seg, st);
+  return launch_lin_bwd_tail(s, args, parts, p.segments, p.seg, st);
 }
 
 }  // namespace gdr

@@ -337,8 +337,8 @@ LinChains lin_backward_chains(const LinShape& s, const LinBwdArgs& a, const LinB
   return L;
 }
 
-hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p, int slices,
-                               int64_t segments, int64_t seg, hipStream_t st) {
+hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p, int64_t segments,
+                               int64_t seg, hipStream_t st) {
   if (s.Hv != s.Hk) {
     ProfScope prof("linear_group_sum", st);
     const int64_t n = s.B * s.T * s.Hk * (s.Dk / 4);
@@ -355,7 +355,7 @@ hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const Lin
   ProfScope prof("linear_dg", st);
   double* sums = s.head_decay ? p.dgsum : nullptr;
   lin_dg_kernel<<<static_cast<unsigned>(s.B * s.Hv * segments), 256, 0, st>>>(
-      p.eq, p.ek, p.xdot, slices, a.dg, sums, s.B, s.T, s.Hv, segments, seg, a.cu);
+      p.eq, p.ek, p.xdot, lin_slices(s.Dk), a.dg, sums, s.B, s.T, s.Hv, segments, seg, a.cu);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   if (sums) lin_dg_head_kernel<<<s.Hv, 64, 0, st>>>(sums, a.dg, s.B * segments, s.Hv);
   return hipGetLastError();

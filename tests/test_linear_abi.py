@@ -55,7 +55,7 @@ BAD = [
     (dict(Hv=3), 2), (dict(T=-1), 2), (dict(B=-2), 2), (dict(Hk=0), 2), (dict(Dk=0), 2), (dict(Dv=-16), 2),
     (dict(Dk=24), 3), (dict(Dv=272), 3), (dict(io_dtype=2), 3), (dict(out_dtype=-1), 3), (dict(flags=2), 3),
     (dict(algo=3), 3), (dict(algo=-1), 3), (dict(q_row=120), 2), (dict(k_row=-8), 2), (dict(v_row=504), 2),
-    (dict(q_row=132), 4), (dict(v_row=(1 << 31) + 8), 3), (dict(B=70000), 3), (dict(T=1 << 31), 3),
+    (dict(q_row=132), 4), (dict(v_row=(1 << 22) + 8), 3), (dict(B=70000), 3), (dict(T=1 << 31), 3),
     (dict(B=60000, T=60000), 3), (dict(B=60000, Hk=1000, Hv=1000, T=1), 3),
 ]
 
