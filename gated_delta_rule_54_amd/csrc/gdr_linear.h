@@ -65,19 +65,20 @@ struct LinChain {
   int eg;
   float* e;             // [slices][B][Hv][T]
   const float* dot;     // gradient of the last state (element (d1, d2) as for s_in) or null
-  float* xdot;          // [segments][B][Hv][slices]: <last state, dot>; null: not wanted
+  float* xdot;          // <last state, dot> in parts, [segments][B][Hv][slices] (sequential) or [..][slices][4]
+                        // (chunked); null: not wanted
   // A sequence cut in segments (chunked): the state each segment starts its
   // walk from, [B][Hv][segments][Dk * Dv] (elements as for s_in), which then
   // holds instead of s_in; and the other direction's, which holds instead of dot.
   const float *seg_in, *seg_dot;
-  int exact;            // chunked, bf16 inputs: the output's sums at fp32 accuracy
+  int key;              // chunked: a dq or dk chain of a VJP
 };
 
 struct LinChains {
   LinChain c[3];
   int n;                // chains in the launch
   int64_t B, T;
-  int Hv;
+  int Hv, group;        // value heads; those that share a key head
   const float* g;       // null: no decay
   int head_decay;       // g is [Hv]
   int out_bf16;
@@ -110,7 +111,7 @@ LinChains lin_forward_chains(const LinShape& s, const LinFwdArgs& a);
 // Carved parts of a backward workspace, common to both algorithms.
 struct LinBwdParts {
   float *eq, *ek;    // [slices(Dk)][B][Hv][T]
-  float* xdot;       // [segments][B][Hv][slices(Dk)]
+  float* xdot;       // [segments][B][Hv][slices(Dk)][4]
   float *pdq, *pdk;  // [B][T][Hv][Dk], only where value heads share a key head
   double* dgsum;     // [B][segments][Hv], only with a decay per head
 };
@@ -118,9 +119,10 @@ size_t lin_bwd_parts(const LinShape& s, int64_t segments, char* base, LinBwdPart
 LinChains lin_backward_chains(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p);
 
 // dq, dk summed over the value heads of a key head; dg from e and xdot.
-// Sequences are cut in segments of seg tokens, each with its own xdot.
-hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p, int64_t segments,
-                               int64_t seg, hipStream_t st);
+// Sequences are cut in segments of seg tokens, each with its own xdot in
+// `dots` parts.
+hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p, int dots,
+                               int64_t segments, int64_t seg, hipStream_t st);
 
 hipError_t launch_lin_zero(float* p, int n, hipStream_t st);  // p[0 .. n) = 0
 

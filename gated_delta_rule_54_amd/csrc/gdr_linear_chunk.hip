@@ -8,15 +8,16 @@
 // A chain backward in time is the same with the rows taken last to first and
 // A_i the sum over the rows before i (the tokens after it).
 //
-// One workgroup of four waves walks a segment of a sequence for one value
-// head and a slice of columns; a wave keeps its 16 NCT columns of H in
-// accumulators for the whole walk.  The accumulator layout of H (rows 4g + e
-// of a 16-row tile in lane group g) is at the same time the operand layout of
-// X H when X's columns are read in the matching order, so H never leaves the
-// registers; O is formed transposed, so that a lane stores 4 consecutive
-// columns of one token.  X, Y and Z pass through LDS (X and Y are shared by
-// the waves, Y and Z are read transposed); the next chunk is loaded into
-// registers while this one is worked on.
+// One workgroup walks a segment of a sequence for one value head and a slice
+// of 64 columns with eight waves.  Waves 4 .. 7 carry the state: each keeps 16
+// columns of H in accumulators for the whole walk and leaves H in LDS, as
+// operands, for the chunk that comes.  Waves 0 .. 3 form the output's 16
+// columns each from it.  So the two products that depend on each other along
+// the sequence (H, and what is read from it) run side by side, on one SIMD an
+// output wave beside a state wave.  The accumulator layout of H is the operand
+// layout of X H when tile t takes rows 32 (t / 2) + 8 g + 4 (t % 2) + e (lane
+// group g, element e), so a lane hands its own registers over.  O is formed
+// transposed, a lane storing 4 consecutive columns of one token.
 //
 // Precision.  bf16 inputs are matrix-core operands as they are.  What is
 // computed on the way (P, H, the decayed Z) is fp32: where a result is
@@ -38,6 +39,8 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 63; }
@@ -69,10 +72,12 @@ __device__ __forceinline__ double log2_decay(float g) {
 }
 
 // Matrix-core operands: lane group g holds steps 8g .. 8g + 7 of a 32-step
-// block of the summed index.  C chunk rows, PAD elements between LDS rows.
+// block of the summed index.  C chunk rows; PAD elements between LDS rows; PER
+// elements of a 16-byte unit; FULL operands hold an fp32 value.
+template <int CC>
 struct OpB {
   using E = uint16_t;
-  static constexpr int C = 64, PAD = 8, PER = 8;  // PER: elements of a 16-byte unit
+  static constexpr int C = CC, PAD = 8, PER = 8, FULL = 3;
   typedef bf16x8 F;
   static __device__ __forceinline__ F run(const E* p) { return *reinterpret_cast<const F*>(p); }
   // Rows k0 + 8g .. +7 of column n0 + step (p / 4) + p % 4, p = lane % 16, of
@@ -85,45 +90,53 @@ struct OpB {
     const bf16x4 b = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 4 * ld)));
     return F{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
   }
+  // columns j .. j + 7 of row i of P (place as p_at)
+  static __device__ __forceinline__ F prun(const E* P, int i, int j) { return run(P + i * C + ((j / 8) ^ (i & (C / 8 - 1))) * 8); }
   static __device__ __forceinline__ f32x4 mma(F a, F b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
   static __device__ __forceinline__ void widen(float (&x)[8], F f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = static_cast<float>(f[i]);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = __builtin_bit_cast(u32x4, f)[i];
+      x[2 * i] = __uint_as_float(w << 16), x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
+    }
+  }
+  // Two values as NS bf16 pairs: each pair rounds what the ones before leave.
+  template <int NS>
+  static __device__ __forceinline__ void split2(uint32_t (&w)[NS], float a, float b) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+      typedef float f2 __attribute__((ext_vector_type(2)));
+      w[s] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{a, b}), b2));
+      a -= __uint_as_float(w[s] << 16);
+      b -= __uint_as_float(w[s] & 0xffff0000u);
+    }
   }
   // x as a sum of NS operands
   template <int NS>
   static __device__ __forceinline__ void split(F (&f)[NS], const float (&x)[8]) {
+    uint32_t w[4][NS];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float r = x[i];
+    for (int i = 0; i < 4; ++i) split2<NS>(w[i], x[2 * i], x[2 * i + 1]);
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        f[s][i] = static_cast<__bf16>(r);
-        if (s + 1 < NS) r -= static_cast<float>(f[s][i]);
-      }
-    }
+    for (int s = 0; s < NS; ++s) f[s] = __builtin_bit_cast(F, (u32x4{w[0][s], w[1][s], w[2][s], w[3][s]}));
   }
   // x[0..3] into NS tiles, `step` elements apart, at p
   template <int NS>
   static __device__ __forceinline__ void put4(E* p, int step, f32x4 x) {
+    uint32_t w[2][NS];
+    split2<NS>(w[0], x[0], x[1]);
+    split2<NS>(w[1], x[2], x[3]);
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      bf16x4 v;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = static_cast<__bf16>(x[i]);
-        x[i] -= static_cast<float>(v[i]);
-      }
-      *reinterpret_cast<bf16x4*>(p + s * step) = v;
-    }
+    for (int s = 0; s < NS; ++s) *reinterpret_cast<u32x2*>(p + s * step) = u32x2{w[0][s], w[1][s]};
   }
 };
 
 struct OpF {
   using E = float;
-  static constexpr int C = 32, PAD = 4, PER = 4;
+  static constexpr int C = 32, PAD = 4, PER = 4, FULL = 1;
   struct F { float v[8]; };
   static __device__ __forceinline__ F run(const E* p) {
     F f;
@@ -137,6 +150,13 @@ struct OpF {
     F f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) f.v[i] = at[i * ld];
+    return f;
+  }
+  static __device__ __forceinline__ F prun(const E* P, int i, int j) {
+    const E *a = P + i * C + ((j / 4) ^ (i & 7)) * 4, *b = P + i * C + ((j / 4 + 1) ^ (i & 7)) * 4;
+    F f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f.v[k] = a[k], f.v[4 + k] = b[k];
     return f;
   }
   static __device__ __forceinline__ f32x4 mma(const F& a, const F& b, f32x4 c) {
@@ -161,8 +181,6 @@ struct OpF {
 };
 
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ rsrc_t make_rsrc(const void* p, uint32_t nbytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(nbytes), 0x00020000);
@@ -174,25 +192,30 @@ __device__ __forceinline__ rsrc_t make_rsrc(const void* p, uint32_t nbytes) {
 // either way (backward as negative offsets, which wrap around), and kNone does.
 constexpr uint32_t kNone = 0xf0000000u;
 struct Rows {
-  const char* at;  // row 0 of the segment's walk
-  uint32_t rowb;   // bytes between tokens; a chunk's rows span less than 2^30 bytes
-  uint32_t width;  // bytes of a row that may be touched
+  const char* top;  // row 0 of the chunk
+  uint32_t rowb;    // bytes between tokens; a chunk's rows span less than 2^30 bytes
+  uint32_t width;   // bytes of a row that may be touched
   bool rev;
-  __device__ __forceinline__ rsrc_t chunk(int64_t first, int n) const {
-    const char* lo = rev ? at - (first + n - 1) * rowb : at + first * rowb;
-    return make_rsrc(lo, (n - 1) * rowb + width);
+  __device__ __forceinline__ rsrc_t chunk(int n) const {
+    return make_rsrc(rev ? top - (n - 1) * rowb : top, (n - 1) * rowb + width);
+  }
+  __device__ __forceinline__ void next(int C) {
+    const int64_t d = static_cast<int64_t>(C * rowb);
+    top += rev ? -d : d;
   }
   // Offset of row i, from the chunk's n = C form.
   __device__ __forceinline__ uint32_t row(int i, int C) const { return (rev ? C - 1 - i : i) * rowb; }
   __device__ __forceinline__ uint32_t shift(int n, int C) const { return rev ? (C - n) * rowb : 0; }
+  __device__ __forceinline__ uint32_t step(int k) const { return rev ? -(k * rowb) : k * rowb; }
 };
 
-// Rows of a chunk on their way from memory to LDS: 16-byte unit e of the
-// [C][W] tile is loaded by thread e % 256 in round e / 256.
-template <typename OP, int W>
+// Rows of a chunk on their way from memory to LDS by NTH threads: 16-byte unit
+// e of the [C][W] tile is loaded by thread e % NTH in round e / NTH.
+template <typename OP, int W, int NTH>
 struct Stage {
-  static constexpr int UPR = W / OP::PER, N = OP::C * UPR / 256, STEP = 256 / UPR;
-  static_assert(OP::C * UPR % 256 == 0, "whole rounds");
+  static constexpr int UPR = W / OP::PER, UNITS = OP::C * UPR, N = (UNITS + NTH - 1) / NTH, STEP = NTH / UPR;
+  static constexpr int LD = W + OP::PAD;
+  static_assert(NTH % UPR == 0, "whole rows per round");
   Rows rows;
   uint32_t off;  // of round 0
   bool on;       // the thread's columns exist
@@ -202,31 +225,42 @@ struct Stage {
     on = 16 * (threadIdx.x % UPR) < t.width;
     off = rows.row(threadIdx.x / UPR, OP::C) + 16 * (threadIdx.x % UPR);
   }
-  __device__ __forceinline__ void load(int64_t first, int n) {
-    const rsrc_t b = rows.chunk(first, n);
-    const uint32_t o = off - rows.shift(n, OP::C), step = rows.rev ? -(STEP * rows.rowb) : STEP * rows.rowb;
+  // The next chunk's n rows (rows at or past C, where the threads are more
+  // than the units, lie past n).
+  __device__ __forceinline__ void load(int n) {
+    const rsrc_t b = rows.chunk(n);
+    const uint32_t o = off - rows.shift(n, OP::C), step = rows.step(STEP);
 #pragma unroll
     for (int u = 0; u < N; ++u) r[u] = __builtin_amdgcn_raw_buffer_load_b128(b, on ? o + u * step : kNone, 0, 0);
+    rows.next(OP::C);
   }
   __device__ __forceinline__ void store(typename OP::E* dst) const {
-    typename OP::E* p = dst + threadIdx.x / UPR * (W + OP::PAD) + OP::PER * (threadIdx.x % UPR);
+    typename OP::E* p = dst + threadIdx.x / UPR * LD + OP::PER * (threadIdx.x % UPR);
 #pragma unroll
-    for (int u = 0; u < N; ++u) *reinterpret_cast<u32x4*>(p + u * STEP * (W + OP::PAD)) = r[u];
+    for (int u = 0; u < N; ++u)
+      if (UNITS % NTH == 0 || u * NTH + static_cast<int>(threadIdx.x) < UNITS)
+        *reinterpret_cast<u32x4*>(p + u * STEP * LD) = r[u];
   }
 };
 
-constexpr int kW2 = kLinSlice;  // columns of a workgroup's slice: 16 for each of its four waves
+constexpr int kW2 = kLinSlice;
 
-template <typename OP, int D1P>
-struct Tiles {
-  static constexpr int C = OP::C, LD1 = D1P + OP::PAD, LDZ = kW2 + OP::PAD, LDP = C + OP::PAD;
-};
+// Place of P's element (i, j), j a multiple of 4: rows of C elements without
+// gaps, their 16-byte units exchanged by the row's number so that a column of
+// units spreads over the LDS banks.
+template <typename OP>
+__device__ __forceinline__ int p_at(int i, int j) {
+  constexpr int U = OP::PER;
+  return i * OP::C + ((j / U) ^ (i & (OP::C / U - 1))) * U + j % U;
+}
 
 // Decay factors of a chunk's rows.
 template <int C>
 struct Decay {
   double A[C];             // log2, running
   float fo[C], fz[C];      // 2^A_i, 2^(A_C - A_i)
+  float up[C], down[C];    // 2^(A_i - A_b), b the first row of i's block of 16; 2^(A_b' - A_i), b' that of the next block
+  float block[C / 16];     // 2^(A_b' - A_b)
   float all;               // 2^A_C
 };
 
@@ -239,223 +273,351 @@ struct Walk {
   bool first, last;          // of the sequence's segments, in the chain's direction
 };
 
-// One walk over a segment.  NS: operands that P and H enter the output's
-// products as; STATE: only the state is wanted.  `total` (in the last wave):
-// the segment's log2 decay.
-//
-// Two barriers a chunk.  Between the first and the second the waves read X, Y,
-// Z and write P; behind the second they read P and write the next chunk's
-// X, Y, Z.  A wave forms the column block of P that has its index, from X
-// fragments that it needs for X H anyway.
-template <typename OP, int D1P, int NS, bool STATE>
-__device__ __forceinline__ void walk(const LinChains& a, const Walk& w, f32x4 (&H)[D1P / 16], double& total,
-                                     typename OP::E* Xs, typename OP::E* Ys, typename OP::E* Zs, typename OP::E* Ps,
-                                     Decay<OP::C>* Ds, float (*Es)[OP::C]) {
-  using T = Tiles<OP, D1P>;
-  using E = typename OP::E;
-  using F = typename OP::F;
-  constexpr int C = T::C, NI = C / 16, KB = D1P / 32, KS = C / 32, LD1 = T::LD1, LDZ = T::LDZ, LDP = T::LDP;
-  constexpr int NU = std::is_same_v<OP, OpB> ? 3 : 1;  // operands the state's update enters as
-  constexpr uint32_t ES = sizeof(E);
-  const LinChain& c = w.c;
-  const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int m = lane & 15, g4 = 4 * (lane >> 4);
-  const int wc = 16 * wave;  // the wave's first column in the slice
-  const bool rev = c.rev;
-  const int64_t start = w.row0 + (rev ? w.len - 1 : 0);
-  const int w2 = min(c.D2 - w.col0, kW2);
-  auto rows = [&](const void* p, int64_t stride, int group, int D, int col, int width) {
-    const char* at = static_cast<const char*>(p) + (start * stride + static_cast<int64_t>(w.h / group) * D + col) * ES;
-    return Rows{at, static_cast<uint32_t>(stride) * ES, width * ES, rev};
-  };
-  Stage<OP, D1P> sx, sy;
-  Stage<OP, kW2> sz;
-  if constexpr (!STATE) sx.init(rows(c.x, c.xr, c.xg, c.D1, 0, c.D1));
-  sy.init(rows(c.y, c.yr, c.yg, c.D1, 0, c.D1));
-  sz.init(rows(c.z, c.zr, c.zg, c.D2, w.col0, w2));
-  // output rows, and those of e's other factor
-  const bool wide = c.out_partial || !a.out_bf16, has = wc < w2;
-  const uint32_t os = wide ? 4 : 2;
-  Rows ro{}, re{};
-  uint32_t oo = 0, oe = 0;
-  if constexpr (!STATE) {
-    const int64_t orow = c.out_partial ? w.b * a.T + w.t0 + (rev ? w.len - 1 : 0) : start;
-    ro = Rows{static_cast<char*>(c.out) + ((orow * a.Hv + w.h) * c.D2 + w.col0) * os,
-              static_cast<uint32_t>(a.Hv) * c.D2 * os, w2 * os, rev};
-    oo = ro.row(m, C) + (wc + g4) * os;
-    if (c.ex) {
-      re = rows(c.ex, c.er, c.eg, c.D2, w.col0, w2);
-      oe = re.row(m, C) + (wc + g4) * ES;
-    }
-  }
-  const float* gp = a.g ? a.g + w.h + (a.head_decay ? 0 : start * a.Hv) : nullptr;
-  const int64_t gstep = a.head_decay ? 0 : rev ? -a.Hv : a.Hv;
+// What a walk computes.  NS: operands that P and H enter the output's products
+// as; EX: the terms e too; WIDE: the output is stored in fp32.
+template <int NS_, bool EX_, bool WIDE_>
+struct Job {
+  static constexpr int NS = NS_;
+  static constexpr bool EX = EX_, WIDE = WIDE_;
+};
 
-  float gn = 0.f;
-  auto fetch = [&](int64_t at) {
-    const int n = static_cast<int>(min(w.len - at, static_cast<int64_t>(C)));
-    if constexpr (!STATE) sx.load(at, n);
-    sy.load(at, n);
-    sz.load(at, n);
-    if (wave == 3) gn = gp && lane < n ? gp[(at + lane) * gstep] : 0.f;
-  };
-  auto put = [&]() {
-    if constexpr (!STATE) sx.store(Xs);
-    sy.store(Ys);
-    sz.store(Zs);
-  };
-  auto decays = [&](Decay<C>& d) {  // by the last wave
-    const double g2 = log2_decay(gn), inc = prefix64(g2), A = rev ? inc - g2 : inc, all = __shfl(inc, 63, 64);
+template <typename OP, int D1P>
+struct Tiles {
+  static constexpr int C = OP::C, NI = C / 16, KB = D1P / 32, KS = C / 32, NT = D1P / 16;
+  static constexpr int LD1 = D1P + OP::PAD, LDZ = kW2 + OP::PAD;
+};
+
+// The rows of an operand of the walk, from the walk's first token on.
+template <typename E>
+__device__ __forceinline__ Rows walk_rows(const Walk& w, const void* p, int64_t stride, int group, int D, int col,
+                                          int width) {
+  const int64_t start = w.row0 + (w.c.rev ? w.len - 1 : 0);
+  const char* at = static_cast<const char*>(p) +
+                   (start * stride + static_cast<int64_t>(w.h / group) * D + col) * static_cast<int64_t>(sizeof(E));
+  return Rows{at, static_cast<uint32_t>(stride * sizeof(E)), static_cast<uint32_t>(width * sizeof(E)),
+              w.c.rev != 0};
+}
+
+// The decays of the walk's chunks, by one wave: lane i reads row i's gate.
+struct Gates {
+  const float* p;
+  int64_t step;
+  float g;
+  __device__ __forceinline__ void init(const LinChains& a, const Walk& w) {
+    const int64_t start = w.row0 + (w.c.rev ? w.len - 1 : 0);
+    p = a.g ? a.g + w.h + (a.head_decay ? 0 : start * a.Hv) : nullptr;
+    step = a.head_decay ? 0 : w.c.rev ? -a.Hv : a.Hv;
+  }
+  __device__ __forceinline__ void load(int64_t at, int n) {
+    g = p && lane_id() < n ? p[(at + lane_id()) * step] : 0.f;
+  }
+  // The chunk's factors into d; returns its log2 decay.
+  template <int C>
+  __device__ __forceinline__ double put(Decay<C>& d, bool rev) const {
+    const int lane = lane_id();
+    const double g2 = log2_decay(g), inc = prefix64(g2), A = rev ? inc - g2 : inc, all = __shfl(inc, 63, 64);
+    const double Ab = __shfl(A, lane & ~15, 64), next = __shfl(A, ((lane & ~15) + 16) & 63, 64);
+    const double An = lane < C - 16 ? next : A;
     if (lane < C) {
       d.A[lane] = A;
       d.fo[lane] = __builtin_amdgcn_exp2f(static_cast<float>(A));
       d.fz[lane] = __builtin_amdgcn_exp2f(static_cast<float>(all - A));
+      d.up[lane] = __builtin_amdgcn_exp2f(static_cast<float>(A - Ab));
+      d.down[lane] = __builtin_amdgcn_exp2f(static_cast<float>(An - A));
+      if (lane % 16 == 0) d.block[lane / 16] = __builtin_amdgcn_exp2f(static_cast<float>(An - A));
     }
     if (lane == 0) d.all = __builtin_amdgcn_exp2f(static_cast<float>(all));
-    total += all;
+    return all;
+  }
+};
+
+// One chunk's update of a state wave's columns: H <- 2^A_C H + Y^T (2^(A_C - A_j) Z).
+template <typename OP, int D1P>
+__device__ __forceinline__ void update(f32x4 (&H)[D1P / 16], const typename OP::E* Ys, const typename OP::E* Zs,
+                                       const Decay<OP::C>& d, int wc) {
+  using T = Tiles<OP, D1P>;
+  using F = typename OP::F;
+  constexpr int NU = OP::FULL, G = T::NT < 8 ? T::NT : 4, STEPS = T::NT / G;
+  const int g8 = 8 * (lane_id() >> 4);
+  // fragments of Y are read a step ahead of the products that take them, and
+  // a step's tiles are independent: the products of one tile wait on each other
+  F yt[2][G];
+  auto read = [&](int step) {
+#pragma unroll
+    for (int t = 0; t < G; ++t) {
+      const int tile = step % STEPS * G + t;
+      yt[step % 2][t] = OP::col(Ys, T::LD1, 32 * (step / STEPS), 32 * (tile / 2) + 4 * (tile % 2), 8);
+    }
   };
-  total = 0.0;
+  read(0);
+  F zu[NU];
+  const float ft = d.all;
+#pragma unroll
+  for (int step = 0; step < T::KS * STEPS; ++step) {
+    const int ks = step / STEPS, t0 = step % STEPS * G;
+    if (step + 1 < T::KS * STEPS) read(step + 1);
+    if (t0 == 0) {
+      float x[8];
+      OP::widen(x, OP::col(Zs, T::LDZ, 32 * ks, wc, 4));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] *= d.fz[32 * ks + g8 + i];
+      OP::template split<NU>(zu, x);
+    }
+    if (ks == 0)
+#pragma unroll
+      for (int t = 0; t < G; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) H[t0 + t][e] *= ft;
+#pragma unroll
+    for (int s = NU - 1; s >= 0; --s)
+#pragma unroll
+      for (int t = 0; t < G; ++t) H[t0 + t] = OP::mma(yt[step % 2][t], zu[s], H[t0 + t]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// LDS of a walk.
+template <typename OP, int D1P, int NS, bool EX>
+struct Shared {
+  using T = Tiles<OP, D1P>;
+  using E = typename OP::E;
+  alignas(16) E X[T::C * T::LD1], Y[T::C * T::LD1], Z[T::C * T::LDZ], P[NS * T::C * T::C];
+  typename OP::F H[4][T::KB][NS][64];  // [wave's columns][32 rows][operand][lane]
+  Decay<T::C> d;
+  float e[EX ? 4 : 1][T::C];
+  float x[4];
+};
+
+// H for the output waves, as NS operands.
+template <typename OP, int D1P, int NS, typename S>
+__device__ __forceinline__ void hand_over(const f32x4 (&H)[D1P / 16], S& s, int cg) {
+#pragma unroll
+  for (int kb = 0; kb < D1P / 32; ++kb) {
+    const f32x4 h0 = H[2 * kb], h1 = H[2 * kb + 1];
+    const float x[8] = {h0[0], h0[1], h0[2], h0[3], h1[0], h1[1], h1[2], h1[3]};
+    typename OP::F f[NS];
+    OP::template split<NS>(f, x);
+#pragma unroll
+    for (int k = 0; k < NS; ++k) s.H[cg][kb][k][lane_id()] = f[k];
+  }
+}
+
+// One walk over a segment of at least one token; H: the state waves' columns.
+//
+// Two barriers a chunk.  Up to the first, the output waves form X H and P and
+// the state waves update H; behind it, the output waves add P Z, the state
+// waves hand H over, and all write the next chunk's X, Y, Z.
+template <typename OP, int D1P, typename J, typename S>
+__device__ __forceinline__ void walk(const LinChains& a, const Walk& w, f32x4 (&H)[D1P / 16], S& s) {
+  using T = Tiles<OP, D1P>;
+  using E = typename OP::E;
+  using F = typename OP::F;
+  constexpr int C = T::C, NI = T::NI, KB = T::KB, KS = T::KS, NS = J::NS;
+  constexpr bool EX = J::EX, WIDE = J::WIDE;
+  constexpr uint32_t ES = sizeof(E);
+  const LinChain& c = w.c;
+  const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6), cg = wave & 3;
+  const int m = lane & 15, g4 = 4 * (lane >> 4);
+  const int wc = 16 * cg;  // the wave's first column in the slice
+  const bool rev = c.rev, state = wave >= 4;
+  const int w2 = min(c.D2 - w.col0, kW2);
+
+  Stage<OP, D1P, 512> sx, sy;
+  Stage<OP, kW2, 512> sz;
+  sx.init(walk_rows<E>(w, c.x, c.xr, c.xg, c.D1, 0, c.D1));
+  sy.init(walk_rows<E>(w, c.y, c.yr, c.yg, c.D1, 0, c.D1));
+  sz.init(walk_rows<E>(w, c.z, c.zr, c.zg, c.D2, w.col0, w2));
+  auto rows_at = [&](int64_t at) { return static_cast<int>(min(w.len - at, static_cast<int64_t>(C))); };
+  auto fetch = [&](int64_t at) {
+    const int n = rows_at(at);
+    sx.load(n);
+    sy.load(n);
+    sz.load(n);
+  };
+  auto put = [&]() {
+    sx.store(s.X);
+    sy.store(s.Y);
+    sz.store(s.Z);
+  };
   fetch(0);
+
+  if (state) {
+    Gates gates;
+    const bool mine = wave == 7;
+    if (mine) {
+      gates.init(a, w);
+      gates.load(0, rows_at(0));
+      gates.put(s.d, rev);
+    }
+    hand_over<OP, D1P, NS>(H, s, cg);
+    put();
+    __syncthreads();
+    for (int64_t at = 0; at < w.len; at += C) {
+      const bool more = at + C < w.len;
+      if (more) {
+        fetch(at + C);
+        if (mine) gates.load(at + C, rows_at(at + C));
+      }
+      update<OP, D1P>(H, s.Y, s.Z, s.d, wc);
+      __syncthreads();
+      if (more) {
+        hand_over<OP, D1P, NS>(H, s, cg);
+        put();
+        if (mine) gates.put(s.d, rev);
+      }
+      __syncthreads();
+    }
+    return;
+  }
+
+  // output rows, and those of e's other factor
+  constexpr uint32_t os = WIDE ? 4 : 2;
+  const int64_t first = w.len - 1;
+  const int64_t orow = c.out_partial ? w.b * a.T + w.t0 + (rev ? first : 0) : w.row0 + (rev ? first : 0);
+  Rows ro{static_cast<char*>(c.out) + ((orow * a.Hv + w.h) * c.D2 + w.col0) * os,
+          static_cast<uint32_t>(a.Hv) * c.D2 * os, w2 * os, rev};
+  Rows re{};
+  const uint32_t oo = ro.row(m, C) + (wc + g4) * os;
+  uint32_t oe = 0;
+  if constexpr (EX) {
+    re = walk_rows<E>(w, c.ex, c.er, c.eg, c.D2, w.col0, w2);
+    oe = re.row(m, C) + (wc + g4) * ES;
+  }
+  const bool has = wc < w2;
+  // the wave's column block of P, and the row blocks in the order it takes them
+  const int jb = wave % NI;
+  int blk[NI];
+#pragma unroll
+  for (int k = 0; k < NI; ++k) blk[k] = (jb + k) % NI;
   put();
-  if (wave == 3) decays(Ds[0]);
   __syncthreads();
 
-  int buf = 0;
-  for (int64_t at = 0; at < w.len; at += C, buf ^= 1) {
-    const int n = static_cast<int>(min(w.len - at, static_cast<int64_t>(C)));
+  for (int64_t at = 0; at < w.len; at += C) {
+    const int n = rows_at(at);
     const bool more = at + C < w.len;
-    const Decay<C>& d = Ds[buf];
     if (more) fetch(at + C);
 
-    f32x4 O[NI];
-    if constexpr (!STATE) {
-      // X H, and the wave's block of P; both transposed
-      f32x4 S[NI];
+    // X H, and the wave's block of P; both transposed.  Fragments are read a
+    // step ahead of the products that take them.
+    f32x4 O[NI], S4[NI];
 #pragma unroll
-      for (int ib = 0; ib < NI; ++ib) O[ib] = S[ib] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < NI; ++k) O[k] = S4[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+    F xf[2][NI], yf[2], hf[2][NS];
+    auto read = [&](int kb) {
+      yf[kb % 2] = OP::run(s.Y + (16 * jb + m) * T::LD1 + 32 * kb + 2 * g4);
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        F hf[NS];
-        const f32x4 h0 = H[2 * kb], h1 = H[2 * kb + 1];
-        const float x[8] = {h0[0], h0[1], h0[2], h0[3], h1[0], h1[1], h1[2], h1[3]};
-        OP::template split<NS>(hf, x);
-        const F yf = OP::run(Ys + (16 * (wave % NI) + m) * LD1 + 32 * kb + 2 * g4);
+      for (int k = 0; k < NS; ++k) hf[kb % 2][k] = s.H[cg][kb][k][lane];
 #pragma unroll
-        for (int ib = 0; ib < NI; ++ib) {
-          const F xf = OP::run(Xs + (16 * ib + m) * LD1 + 32 * kb + 2 * g4);
-          if (ib >= wave) S[ib] = OP::mma(yf, xf, S[ib]);
+      for (int k = 0; k < NI; ++k) xf[kb % 2][k] = OP::run(s.X + (16 * blk[k] + m) * T::LD1 + 32 * kb + 2 * g4);
+    };
+    read(0);
 #pragma unroll
-          for (int s = NS - 1; s >= 0; --s) O[ib] = OP::mma(hf[s], xf, O[ib]);
-        }
-      }
-      // P = S o 2^(A_i - A_j): the lane holds rows j .. j + 3 of column i
-      if (wave < NI) {
-        const int j = 16 * wave + g4;
-        double Aj[4];
+    for (int kb = 0; kb < KB; ++kb) {
+      if (kb + 1 < KB) read(kb + 1);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) Aj[e] = d.A[j + e];
+      for (int k = 0; k < NI; ++k) S4[k] = OP::mma(yf[kb % 2], xf[kb % 2][k], S4[k]);
 #pragma unroll
-        for (int ib = 0; ib < NI; ++ib)
-          if (ib >= wave) {
-            const int i = 16 * ib + m;
-            const double Ai = d.A[i];
-            f32x4 p;
+      for (int q = NS - 1; q >= 0; --q)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              p[e] = j + e <= i ? S[ib][e] * __builtin_amdgcn_exp2f(static_cast<float>(Ai - Aj[e])) : 0.f;
-            OP::template put4<NS>(Ps + i * LDP + j, C * LDP, p);
+        for (int k = 0; k < NI; ++k) O[k] = OP::mma(hf[kb % 2][q], xf[kb % 2][k], O[k]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // P = S o 2^(A_i - A_j): the lane holds rows j .. j + 3 of column i.  On
+    // the diagonal block (k = 0) each factor is formed from its difference;
+    // below, it is 2^(A_i - A_b) 2^(A_b - A_j), b the first row of i's block,
+    // whose second part takes one more block's factor from block to block.
+    if (NI == 4 || wave < NI) {
+      const int j = 16 * jb + g4;
+      float f[4];
+#pragma unroll
+      for (int k = 0; k < NI; ++k) {
+        const int i = 16 * blk[k] + m;
+        f32x4 p;
+        if (k == 0) {
+          const double Ai = s.d.A[i];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[e] = j + e <= i ? S4[k][e] * __builtin_amdgcn_exp2f(static_cast<float>(Ai - s.d.A[j + e])) : 0.f;
+            f[e] = s.d.down[j + e];
           }
-      }
-    }
-
-    // Z as it is for the output, decayed to the chunk's end for the state
-    F zf[KS], zu[KS][NU];
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      zf[ks] = OP::col(Zs, LDZ, 32 * ks, wc, 4);
-      float x[8];
-      OP::widen(x, zf[ks]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] *= d.fz[32 * ks + 2 * g4 + i];
-      OP::template split<NU>(zu[ks], x);
-    }
-    const float ft = d.all;
-#pragma unroll
-    for (int t = 0; t < D1P / 16; ++t) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) H[t][e] *= ft;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        // tile t holds rows 32 (t / 2) + 8 g + 4 (t % 2) + e, the order of X's operands
-        const F yf = OP::col(Ys, LD1, 32 * ks, 32 * (t / 2) + 4 * (t % 2), 8);
-#pragma unroll
-        for (int s = NU - 1; s >= 0; --s) H[t] = OP::mma(yf, zu[ks][s], H[t]);
-      }
-    }
-    if constexpr (!STATE) {
-#pragma unroll
-      for (int ib = 0; ib < NI; ++ib) {
-        const float f = d.fo[16 * ib + m];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) O[ib][e] *= f;
-      }
-    }
-    if (more && wave == 3) decays(Ds[buf ^ 1]);
-    __syncthreads();
-    if (more) put();
-
-    if constexpr (!STATE) {
-      rsrc_t be;
-      if (c.ex) be = re.chunk(at, n);
-      float ex[NI][4];
-      if (c.ex) {
-        const uint32_t step = rev ? -(16 * re.rowb) : 16 * re.rowb, at0 = oe - re.shift(n, C);
-#pragma unroll
-        for (int ib = 0; ib < NI; ++ib) {
-          const uint32_t o = has ? at0 + ib * step : kNone;
-          if constexpr (ES == 2) {
-            const u32x2 u = __builtin_amdgcn_raw_buffer_load_b64(be, o, 0, 0);
-            ex[ib][0] = __uint_as_float(u[0] << 16), ex[ib][1] = __uint_as_float(u[0] & 0xffff0000u);
-            ex[ib][2] = __uint_as_float(u[1] << 16), ex[ib][3] = __uint_as_float(u[1] & 0xffff0000u);
-          } else {
-            const u32x4 u = __builtin_amdgcn_raw_buffer_load_b128(be, o, 0, 0);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) ex[ib][e] = __uint_as_float(static_cast<unsigned>(u[e]));
-          }
-        }
-      }
-      // O += P Z
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int ib = 2 * ks; ib < NI; ++ib)
-#pragma unroll
-          for (int s = NS - 1; s >= 0; --s)
-            O[ib] = OP::mma(zf[ks], OP::run(Ps + s * C * LDP + (16 * ib + m) * LDP + 32 * ks + 2 * g4), O[ib]);
-      const rsrc_t bo = ro.chunk(at, n);
-      const uint32_t step = rev ? -(16 * ro.rowb) : 16 * ro.rowb, at0 = oo - ro.shift(n, C);
-#pragma unroll
-      for (int ib = 0; ib < NI; ++ib) {
-        const uint32_t o = has ? at0 + ib * step : kNone;
-        if (wide) {
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, O[ib]), bo, o, 0, 0);
         } else {
-          const bf16x4 v{static_cast<__bf16>(O[ib][0]), static_cast<__bf16>(O[ib][1]), static_cast<__bf16>(O[ib][2]),
-                         static_cast<__bf16>(O[ib][3])};
-          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, v), bo, o, 0, 0);
+          const float u = s.d.up[i], bl = s.d.block[blk[k]];
+          const bool below = jb + k < NI;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[e] = below ? S4[k][e] * (u * f[e]) : 0.f;
+            f[e] *= bl;
+          }
         }
-        if (c.ex) {
-          const float e = rows4_sum((ex[ib][0] * O[ib][0] + ex[ib][1] * O[ib][1]) +
-                                    (ex[ib][2] * O[ib][2] + ex[ib][3] * O[ib][3]));
-          if (lane < 16) Es[wave][16 * ib + m] = e;
+        OP::template put4<NS>(s.P + p_at<OP>(i, j), C * C, p);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < NI; ++k) {
+      const float f = s.d.fo[16 * blk[k] + m];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) O[k][e] *= f;
+    }
+    F zf[KS];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) zf[ks] = OP::col(s.Z, T::LDZ, 32 * ks, wc, 4);
+    float ex[NI][4];
+    if constexpr (EX) {
+      const rsrc_t be = re.chunk(n);
+      const uint32_t step = re.step(16), at0 = oe - re.shift(n, C);
+      re.next(C);
+#pragma unroll
+      for (int k = 0; k < NI; ++k) {
+        const uint32_t o = has ? at0 + blk[k] * step : kNone;
+        if constexpr (ES == 2) {
+          const u32x2 u = __builtin_amdgcn_raw_buffer_load_b64(be, o, 0, 0);
+          ex[k][0] = __uint_as_float(u[0] << 16), ex[k][1] = __uint_as_float(u[0] & 0xffff0000u);
+          ex[k][2] = __uint_as_float(u[1] << 16), ex[k][3] = __uint_as_float(u[1] & 0xffff0000u);
+        } else {
+          const u32x4 u = __builtin_amdgcn_raw_buffer_load_b128(be, o, 0, 0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ex[k][e] = __uint_as_float(static_cast<unsigned>(u[e]));
         }
       }
     }
     __syncthreads();
-    if constexpr (!STATE) {
-      if (c.ex && tid < n) {
+
+    // O += P Z; the blocks of P above the diagonal are zeros
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int q = NS - 1; q >= 0; --q) {
+        F pf[NI];
+#pragma unroll
+        for (int k = 0; k < NI; ++k) pf[k] = OP::prun(s.P + q * C * C, 16 * blk[k] + m, 32 * ks + 2 * g4);
+#pragma unroll
+        for (int k = 0; k < NI; ++k) O[k] = OP::mma(zf[ks], pf[k], O[k]);
+      }
+    if (more) put();
+    const rsrc_t bo = ro.chunk(n);
+    const uint32_t step = ro.step(16), at0 = oo - ro.shift(n, C);
+    ro.next(C);
+#pragma unroll
+    for (int k = 0; k < NI; ++k) {
+      const f32x4 v = O[k];
+      const uint32_t o = has ? at0 + blk[k] * step : kNone;
+      if constexpr (WIDE) {
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), bo, o, 0, 0);
+      } else {
+        const bf16x4 q{static_cast<__bf16>(v[0]), static_cast<__bf16>(v[1]), static_cast<__bf16>(v[2]),
+                       static_cast<__bf16>(v[3])};
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, q), bo, o, 0, 0);
+      }
+      if constexpr (EX) {
+        const float e = rows4_sum((ex[k][0] * v[0] + ex[k][1] * v[1]) + (ex[k][2] * v[2] + ex[k][3] * v[3]));
+        if (lane < 16) s.e[wave][16 * blk[k] + m] = e;
+      }
+    }
+    __syncthreads();
+    if constexpr (EX) {
+      if (tid < n) {
         const int64_t t = rev ? w.t0 + w.len - 1 - at - tid : w.t0 + at + tid;
-        c.e[(w.sl * a.B * a.Hv + w.bh) * a.T + t] = (Es[0][tid] + Es[1][tid]) + (Es[2][tid] + Es[3][tid]);
+        c.e[(w.sl * a.B * a.Hv + w.bh) * a.T + t] = (s.e[0][tid] + s.e[1][tid]) + (s.e[2][tid] + s.e[3][tid]);
       }
     }
   }
@@ -469,7 +631,9 @@ __device__ __forceinline__ int64_t xcd_index() {
 }
 
 // Finds the workgroup's place; false: nothing to do.  Slices are fastest (of
-// all chains of a head), then heads, then sequences, then segments.
+// all chains of a head), then the value heads that share a key head, then
+// sequences, then segments, then key heads: an XCD's share is a range of key
+// heads, the same for sequences of any lengths.
 __device__ __forceinline__ bool find(const LinChains& a, Walk& w) {
   const int n0 = lin_slices(a.c[0].D2), n1 = a.n > 1 ? lin_slices(a.c[1].D2) : 0,
             n2 = a.n > 2 ? lin_slices(a.c[2].D2) : 0, all = n0 + n1 + n2;
@@ -482,10 +646,11 @@ __device__ __forceinline__ bool find(const LinChains& a, Walk& w) {
   w.c = lin_chain(a, ci);
   w.sl = s;
   w.col0 = s * kW2;
-  w.bh = r % (a.B * a.Hv);
-  w.seg = r / (a.B * a.Hv);
-  w.h = static_cast<int>(w.bh % a.Hv);
-  w.b = w.bh / a.Hv;
+  const int64_t per = a.group * a.B;
+  w.b = r % per / a.group;
+  w.seg = r / per % a.segments;
+  w.h = static_cast<int>(r / (per * a.segments)) * a.group + static_cast<int>(r % a.group);
+  w.bh = w.b * a.Hv + w.h;
   const LinSpan sp = lin_span(a.cu, w.b, a.T);
   w.t0 = w.seg * a.seg;
   if (w.t0 >= sp.len && w.seg > 0) return false;
@@ -497,11 +662,11 @@ __device__ __forceinline__ bool find(const LinChains& a, Walk& w) {
   return true;
 }
 
-// Element (d1, d2) of a state for the lane's accumulator tile t (rows d1 ..
-// d1 + 3 are its elements).
+// The state's elements that a state wave's lane holds: tile t's are rows d1 ..
+// d1 + 3 of one column.
 template <int D1P, typename F>
 __device__ __forceinline__ void each_state(const LinChain& c, int col0, F&& f) {
-  const int lane = lane_id(), d2 = col0 + 16 * static_cast<int>(threadIdx.x >> 6) + (lane & 15);
+  const int lane = lane_id(), d2 = col0 + 16 * static_cast<int>(threadIdx.x >> 6 & 3) + (lane & 15);
 #pragma unroll
   for (int t = 0; t < D1P / 16; ++t) {
     const int d1 = 32 * (t / 2) + 8 * (lane >> 4) + 4 * (t % 2);
@@ -509,50 +674,42 @@ __device__ __forceinline__ void each_state(const LinChain& c, int col0, F&& f) {
   }
 }
 
-template <typename OP, int D1P, int NS0, int NS1>
-__global__ __launch_bounds__(256, D1P <= 128 ? 2 : 1) void lin_chunk_kernel(LinChains a) {
-  using T = Tiles<OP, D1P>;
-  using E = typename OP::E;
-  constexpr int C = T::C, NSM = NS0 > NS1 ? NS0 : NS1;
-  __shared__ __align__(16) E Xs[C * T::LD1], Ys[C * T::LD1], Zs[C * T::LDZ], Ps[NSM * C * T::LDP];
-  __shared__ __align__(16) Decay<C> Ds[2];
-  __shared__ __align__(16) float Es[4][C];
+// JA: the job of the dq and dk chains, JB: that of the others.
+template <typename OP, int D1P, typename JA, typename JB>
+__global__ __launch_bounds__(512) void lin_chunk_kernel(LinChains a) {
+  constexpr int NS = JA::NS > JB::NS ? JA::NS : JB::NS;
+  __shared__ Shared<OP, D1P, NS, JA::EX> s;
   Walk w;
   if (!find(a, w)) return;
   const LinChain& c = w.c;
   const int64_t one = static_cast<int64_t>(c.D1) * c.D2;
-  // the blocks of P above the diagonal that a 32-step product reads stay zero
-  for (int e = threadIdx.x; e < NSM * C * T::LDP; e += 256) Ps[e] = E(0);
+  const bool state = threadIdx.x >= 256;
 
   f32x4 H[D1P / 16];
 #pragma unroll
   for (int t = 0; t < D1P / 16; ++t) H[t] = f32x4{0.f, 0.f, 0.f, 0.f};
   const float* in = c.seg_in ? c.seg_in + (w.bh * a.segments + w.seg) * one : c.s_in ? c.s_in + w.bh * one : nullptr;
-  if (in)
+  if (state && in)
     each_state<D1P>(c, w.col0, [&](int t, int64_t at) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) H[t][e] = in[at + static_cast<int64_t>(e) * c.s1];
     });
-  double total;
   if (w.len > 0) {
-    if (NS0 == NS1 || c.exact) walk<OP, D1P, NS0, false>(a, w, H, total, Xs, Ys, Zs, Ps, Ds, Es);
-    else walk<OP, D1P, NS1, false>(a, w, H, total, Xs, Ys, Zs, Ps, Ds, Es);
+    if (!std::is_same_v<JA, JB> && c.key) walk<OP, D1P, JA>(a, w, H, s);
+    else walk<OP, D1P, JB>(a, w, H, s);
   }
+  if (!state) return;
   if (c.xdot) {
     const float* dot = c.seg_dot ? c.seg_dot + (w.bh * a.segments + w.seg) * one : c.dot ? c.dot + w.bh * one : nullptr;
-    float s = 0.f;
+    float x = 0.f;
     if (dot)
       each_state<D1P>(c, w.col0, [&](int t, int64_t at) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s += H[t][e] * dot[at + static_cast<int64_t>(e) * c.s1];
+        for (int e = 0; e < 4; ++e) x += H[t][e] * dot[at + static_cast<int64_t>(e) * c.s1];
       });
-    s = rows4_sum(row16_sum(s));
-    __syncthreads();
-    if (lane_id() == 0) Es[threadIdx.x >> 6][0] = s;
-    __syncthreads();
-    if (threadIdx.x == 0)
-      c.xdot[(w.seg * a.B * a.Hv + w.bh) * lin_slices(c.D2) + w.sl] =
-          (Es[0][0] + Es[1][0]) + (Es[2][0] + Es[3][0]);
+    x = rows4_sum(row16_sum(x));
+    if (lane_id() == 0)
+      c.xdot[((w.seg * a.B * a.Hv + w.bh) * lin_slices(c.D2) + w.sl) * 4 + (threadIdx.x >> 6 & 3)] = x;
   }
   if (c.s_out && w.last) {
     float* out = c.s_out + w.bh * one;
@@ -564,26 +721,47 @@ __global__ __launch_bounds__(256, D1P <= 128 ? 2 : 1) void lin_chunk_kernel(LinC
 }
 
 // Every segment's own contribution to the state at its end (in the chain's
-// direction), from zero.  The last segment's is not needed.  The chain forward
-// in time leaves the segments' factors, but the last one's, which only the
-// chain backward in time needs and leaves.
+// direction), from zero, by four state waves.  The last segment's is not
+// needed.  The chain forward in time leaves the segments' factors, but the
+// last one's, which only the chain backward in time needs and leaves.
 template <typename OP, int D1P>
-__global__ __launch_bounds__(256, 2) void lin_segment_kernel(LinChains a, float* factor) {
+__global__ __launch_bounds__(256) void lin_segment_kernel(LinChains a, float* factor) {
   using T = Tiles<OP, D1P>;
   using E = typename OP::E;
   constexpr int C = T::C;
   __shared__ __align__(16) E Ys[C * T::LD1], Zs[C * T::LDZ];
-  __shared__ __align__(16) Decay<C> Ds[2];
+  __shared__ __align__(16) Decay<C> d;
   Walk w;
   if (!find(a, w) || w.last) return;
   const LinChain& c = w.c;
-  const int64_t one = static_cast<int64_t>(c.D1) * c.D2;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w2 = min(c.D2 - w.col0, kW2);
   f32x4 H[D1P / 16];
 #pragma unroll
   for (int t = 0; t < D1P / 16; ++t) H[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  double total;
-  walk<OP, D1P, 1, true>(a, w, H, total, nullptr, Ys, Zs, nullptr, Ds, nullptr);
-  const int64_t at0 = w.bh * a.segments + w.seg;
+  Stage<OP, D1P, 256> sy;
+  Stage<OP, kW2, 256> sz;
+  sy.init(walk_rows<E>(w, c.y, c.yr, c.yg, c.D1, 0, c.D1));
+  sz.init(walk_rows<E>(w, c.z, c.zr, c.zg, c.D2, w.col0, w2));
+  Gates gates;
+  gates.init(a, w);
+  double total = 0.0;
+  auto fetch = [&](int64_t at) {
+    const int n = static_cast<int>(min(w.len - at, static_cast<int64_t>(C)));
+    sy.load(n);
+    sz.load(n);
+    if (wave == 3) gates.load(at, n);
+  };
+  fetch(0);
+  for (int64_t at = 0; at < w.len; at += C) {
+    sy.store(Ys);
+    sz.store(Zs);
+    if (wave == 3) total += gates.put(d, c.rev);
+    __syncthreads();
+    if (at + C < w.len) fetch(at + C);
+    update<OP, D1P>(H, Ys, Zs, d, 16 * wave);
+    __syncthreads();
+  }
+  const int64_t at0 = w.bh * a.segments + w.seg, one = static_cast<int64_t>(c.D1) * c.D2;
   if ((!c.rev || w.first) && w.sl == 0 && threadIdx.x == 192)
     factor[at0] = __builtin_amdgcn_exp2f(static_cast<float>(total));
   float* out = c.s_out + at0 * one;
@@ -621,17 +799,17 @@ __global__ __launch_bounds__(256) void lin_scan_kernel(float* fwd, float* rev, c
 
 // Cutting sequences: workgroups wanted in the launch, the shortest segment.
 #ifndef TG
-#define TG 512
+#define TG 256
 #endif
 #ifndef MS
 #define MS 256
 #endif
 constexpr int64_t kTargetGroups = TG, kMinSegment = MS;
 
-int64_t chunk_blocks(const LinChains& a) {
+unsigned chunk_blocks(const LinChains& a) {
   int64_t all = 0;
   for (int i = 0; i < a.n; ++i) all += lin_slices(a.c[i].D2);
-  return (all * a.B * a.Hv * a.segments + 7) / 8 * 8;
+  return static_cast<unsigned>((all * a.B * a.Hv * a.segments + 7) / 8 * 8);
 }
 
 int max_d1(const LinChains& a) {
@@ -640,34 +818,40 @@ int max_d1(const LinChains& a) {
   return d;
 }
 
-template <typename OP, int D1P>
-hipError_t run_chunks(const LinChains& a, bool exact, bool mixed, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(chunk_blocks(a)));
-  if constexpr (std::is_same_v<OP, OpF>) {
-    lin_chunk_kernel<OP, D1P, 1, 1><<<grid, 256, 0, st>>>(a);
-  } else {
-    if (mixed) lin_chunk_kernel<OP, D1P, 3, 1><<<grid, 256, 0, st>>>(a);
-    else if (exact) lin_chunk_kernel<OP, D1P, 3, 3><<<grid, 256, 0, st>>>(a);
-    else lin_chunk_kernel<OP, D1P, 1, 1><<<grid, 256, 0, st>>>(a);
-  }
+template <typename OP, int D1P, typename JA, typename JB = JA>
+hipError_t run_chunks(const LinChains& a, hipStream_t st) {
+  lin_chunk_kernel<OP, D1P, JA, JB><<<chunk_blocks(a), 512, 0, st>>>(a);
   return hipGetLastError();
 }
 
 template <typename OP, int D1P>
 hipError_t run_segments(const LinChains& a, float* factor, hipStream_t st) {
-  lin_segment_kernel<OP, D1P><<<static_cast<unsigned>(chunk_blocks(a)), 256, 0, st>>>(a, factor);
+  lin_segment_kernel<OP, D1P><<<chunk_blocks(a), 256, 0, st>>>(a, factor);
   return hipGetLastError();
 }
 
+// The kernel of a VJP: whether e is wanted, dq and dk go to fp32 parts, and
+// dv is returned in fp32 (then dq and dk are stored in fp32 in any case).
+template <typename OP, int D1P>
+hipError_t run_vjp(const LinChains& a, bool ex, bool part, bool wide, hipStream_t st) {
+  constexpr int N = OP::FULL;
+  if (wide) return ex ? run_chunks<OP, D1P, Job<N, true, true>, Job<N, false, true>>(a, st)
+                      : run_chunks<OP, D1P, Job<N, false, true>>(a, st);
+  if (ex) return part ? run_chunks<OP, D1P, Job<N, true, true>, Job<1, false, false>>(a, st)
+                      : run_chunks<OP, D1P, Job<N, true, false>, Job<1, false, false>>(a, st);
+  return part ? run_chunks<OP, D1P, Job<1, false, true>, Job<1, false, false>>(a, st)
+              : run_chunks<OP, D1P, Job<1, false, false>>(a, st);
+}
+
 // Calls f with the operand type and the padded width (an integral constant).
+// 256 rows of state leave LDS for chunks of 32 rows only.
 template <typename F>
 hipError_t by_type(bool io_bf16, int d1, F&& f) {
-  auto width = [&](auto op) {
-    if (d1 <= 64) return f(op, std::integral_constant<int, 64>{});
-    if (d1 <= 128) return f(op, std::integral_constant<int, 128>{});
-    return f(op, std::integral_constant<int, 256>{});
-  };
-  return io_bf16 ? width(OpB{}) : width(OpF{});
+  constexpr std::integral_constant<int, 64> w64{};
+  constexpr std::integral_constant<int, 128> w128{};
+  constexpr std::integral_constant<int, 256> w256{};
+  if (!io_bf16) return d1 <= 64 ? f(OpF{}, w64) : d1 <= 128 ? f(OpF{}, w128) : f(OpF{}, w256);
+  return d1 <= 64 ? f(OpB<64>{}, w64) : d1 <= 128 ? f(OpB<64>{}, w128) : f(OpB<32>{}, w256);
 }
 
 }  // namespace
@@ -676,8 +860,7 @@ hipError_t by_type(bool io_bf16, int d1, F&& f) {
 LinPlan lin_plan(const LinShape& s, bool backward) {
   LinPlan p{};
   const int slices = backward ? 2 * lin_slices(s.Dk) + lin_slices(s.Dv) : lin_slices(s.Dv);
-  const int64_t heads = std::max<int64_t>(1, s.B * s.Hv);
-  const int64_t groups = heads * slices;
+  const int64_t groups = std::max<int64_t>(1, s.B * s.Hv) * slices;
   const int64_t want = (kTargetGroups + groups - 1) / groups, most = (s.T + kMinSegment - 1) / kMinSegment;
   const int64_t n = std::max<int64_t>(1, std::min(want, most));
   p.seg = std::max<int64_t>(64, ((s.T + n - 1) / n + 63) / 64 * 64);
@@ -734,9 +917,11 @@ hipError_t launch_lin_chunk_fwd(const LinShape& s, const LinPlan& p, const LinFw
     a.c[0].seg_in = g.fwd;
   }
   ProfScope prof("linear_chunks", st);
-  a.c[0].exact = !s.out_bf16;
   return by_type(s.io_bf16, s.Dk, [&](auto op, auto d1) {
-    return run_chunks<decltype(op), decltype(d1)::value>(a, !s.out_bf16, false, st);
+    using OP = decltype(op);
+    constexpr int D1P = decltype(d1)::value;
+    return s.out_bf16 ? run_chunks<OP, D1P, Job<1, false, false>>(a, st)
+                      : run_chunks<OP, D1P, Job<OP::FULL, false, true>>(a, st);
   });
 }
 
@@ -756,17 +941,15 @@ hipError_t launch_lin_chunk_bwd(const LinShape& s, const LinPlan& p, const LinBw
     a.c[0].seg_in = g.fwd, a.c[0].seg_dot = g.rev;
     a.c[1].seg_in = a.c[2].seg_in = g.rev;
   }
-  const bool all = !s.out_bf16, some = args.dg != nullptr;
-  a.c[0].exact = a.c[1].exact = all || some;
-  a.c[2].exact = all;
+  a.c[0].key = a.c[1].key = 1;
   {
     ProfScope prof("linear_chunks_vjp", st);
     const hipError_t e = by_type(s.io_bf16, max_d1(a), [&](auto op, auto d1) {
-      return run_chunks<decltype(op), decltype(d1)::value>(a, all, some && !all, st);
+      return run_vjp<decltype(op), decltype(d1)::value>(a, args.dg != nullptr, s.Hv != s.Hk, !s.out_bf16, st);
     });
     if (e != hipSuccess) return e;
   }
-  return launch_lin_bwd_tail(s, args, parts, p.segments, p.seg, st);
+  return launch_lin_bwd_tail(s, args, parts, 4 * lin_slices(s.Dk), p.segments, p.seg, st);
 }
 
 }  // namespace gdr

@@ -193,7 +193,7 @@ __global__ __launch_bounds__(256) void lin_group_sum_kernel(const float* pdq, co
 // their terms cancel.  One workgroup walks its segment from the end, 256
 // tokens at a time.
 __global__ __launch_bounds__(256) void lin_dg_kernel(const float* eq, const float* ek, const float* xdot, int nsl,
-                                                     float* dg, double* dgsum, int64_t B, int64_t T, int Hv,
+                                                     int dots, float* dg, double* dgsum, int64_t B, int64_t T, int Hv,
                                                      int64_t segments, int64_t seg, const int64_t* cu) {
   __shared__ double wsum[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -202,7 +202,7 @@ __global__ __launch_bounds__(256) void lin_dg_kernel(const float* eq, const floa
   const LinSpan sp = lin_span(cu, b, T);
   const int64_t t0 = s * seg, t1 = sp.len < t0 + seg ? sp.len : t0 + seg;
   double carry = 0.0, total = 0.0;
-  for (int j = 0; j < nsl; ++j) carry += xdot[(s * B * Hv + bh) * nsl + j];
+  for (int j = 0; j < dots; ++j) carry += xdot[(s * B * Hv + bh) * dots + j];
   for (int64_t end = t1; end > t0; end -= 256) {
     const int64_t t = end - 1 - tid;
     double v = 0.0;
@@ -273,7 +273,7 @@ LinChains lin_forward_chains(const LinShape& s, const LinFwdArgs& a) {
   LinChains L{};
   const int G = s.Hv / s.Hk;
   L.n = 1, L.segments = 1, L.seg = s.T;
-  L.B = s.B, L.T = s.T, L.Hv = s.Hv, L.g = a.g, L.head_decay = s.head_decay, L.out_bf16 = s.out_bf16, L.cu = a.cu;
+  L.B = s.B, L.T = s.T, L.Hv = s.Hv, L.group = G, L.g = a.g, L.head_decay = s.head_decay, L.out_bf16 = s.out_bf16, L.cu = a.cu;
   LinChain& c = L.c[0];
   c.x = a.q, c.xr = s.q_row, c.xg = G;
   c.y = a.k, c.yr = s.k_row, c.yg = G;
@@ -294,7 +294,7 @@ size_t lin_bwd_parts(const LinShape& s, int64_t segments, char* base, LinBwdPart
   const size_t bh = static_cast<size_t>(s.B) * s.Hv, n = bh * s.T, nsl = lin_slices(s.Dk);
   p->eq = reinterpret_cast<float*>(take(nsl * n * 4));
   p->ek = reinterpret_cast<float*>(take(nsl * n * 4));
-  p->xdot = reinterpret_cast<float*>(take(segments * bh * nsl * 4));
+  p->xdot = reinterpret_cast<float*>(take(segments * bh * nsl * 4 * 4));
   const bool shared = s.Hv != s.Hk;
   p->pdq = reinterpret_cast<float*>(take(shared ? n * s.Dk * 4 : 0));
   p->pdk = reinterpret_cast<float*>(take(shared ? n * s.Dk * 4 : 0));
@@ -307,7 +307,7 @@ LinChains lin_backward_chains(const LinShape& s, const LinBwdArgs& a, const LinB
   const int G = s.Hv / s.Hk;
   const int64_t d_row = static_cast<int64_t>(s.Hv) * s.Dv;
   L.n = 3, L.segments = 1, L.seg = s.T;
-  L.B = s.B, L.T = s.T, L.Hv = s.Hv, L.g = a.g, L.head_decay = s.head_decay, L.out_bf16 = s.out_bf16, L.cu = a.cu;
+  L.B = s.B, L.T = s.T, L.Hv = s.Hv, L.group = G, L.g = a.g, L.head_decay = s.head_decay, L.out_bf16 = s.out_bf16, L.cu = a.cu;
   LinChain& q = L.c[0];  // dq
   q.x = a.dout, q.xr = d_row, q.xg = 1;
   q.y = a.v, q.yr = s.v_row, q.yg = 1;
@@ -337,8 +337,8 @@ LinChains lin_backward_chains(const LinShape& s, const LinBwdArgs& a, const LinB
   return L;
 }
 
-hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p, int64_t segments,
-                               int64_t seg, hipStream_t st) {
+hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p, int dots,
+                               int64_t segments, int64_t seg, hipStream_t st) {
   if (s.Hv != s.Hk) {
     ProfScope prof("linear_group_sum", st);
     const int64_t n = s.B * s.T * s.Hk * (s.Dk / 4);
@@ -355,7 +355,7 @@ hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const Lin
   ProfScope prof("linear_dg", st);
   double* sums = s.head_decay ? p.dgsum : nullptr;
   lin_dg_kernel<<<static_cast<unsigned>(s.B * s.Hv * segments), 256, 0, st>>>(
-      p.eq, p.ek, p.xdot, lin_slices(s.Dk), a.dg, sums, s.B, s.T, s.Hv, segments, seg, a.cu);
+      p.eq, p.ek, p.xdot, lin_slices(s.Dk), dots, a.dg, sums, s.B, s.T, s.Hv, segments, seg, a.cu);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   if (sums) lin_dg_head_kernel<<<s.Hv, 64, 0, st>>>(sums, a.dg, s.B * segments, s.Hv);
   return hipGetLastError();
