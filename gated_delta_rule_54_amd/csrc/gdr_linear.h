@@ -16,6 +16,7 @@
 
 #include <gdr.h>
 #include <hip/hip_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "gdr_internal.h"
@@ -63,7 +64,7 @@ struct LinChain {
   const void* ex;       // e_t = ex_t . out_t, ex [.., Hv / eg heads, D2], rows er elements apart; null: not wanted
   int64_t er;
   int eg;
-  float* e;             // [slices][B][Hv][T]
+  float* e;             // in parts, [slices][B][Hv][T] (sequential) or [slices][1 or 2][..] (chunked)
   const float* dot;     // gradient of the last state (element (d1, d2) as for s_in) or null
   float* xdot;          // <last state, dot> in parts, [segments][B][Hv][slices] (sequential) or [..][slices][4]
                         // (chunked); null: not wanted
@@ -87,13 +88,20 @@ struct LinChains {
 };
 
 #ifdef __HIPCC__
-// Chain i of a launch, by selects: an indexed kernel argument would be copied
-// to scratch memory.
-__device__ __forceinline__ LinChain lin_chain(const LinChains& a, int i) {
-  LinChain c = a.c[0];
-  if (i == 1) c = a.c[1];
-  if (i == 2) c = a.c[2];
-  return c;
+// Chain i of a launch whose kernel takes LinChains as its first argument, read
+// from the argument segment by scalar loads.  Indexed as a C++ array, the
+// argument would be copied to scratch memory; picked by selects, all three
+// chains would fill the scalar registers.
+__device__ __forceinline__ LinChain lin_chain(int i) {
+  static_assert(offsetof(LinChains, c) == 0 && sizeof(LinChain) % 4 == 0, "chains come first, in whole words");
+  typedef const __attribute__((address_space(4))) uint32_t* words;
+  const words p = (words)__builtin_amdgcn_kernarg_segment_ptr() + i * (sizeof(LinChain) / 4);
+  struct {
+    uint32_t w[sizeof(LinChain) / 4];
+  } u;
+#pragma unroll
+  for (unsigned k = 0; k < sizeof(LinChain) / 4; ++k) u.w[k] = p[k];
+  return __builtin_bit_cast(LinChain, u);
 }
 struct LinSpan {
   int64_t t0, len;
@@ -110,7 +118,7 @@ LinChains lin_forward_chains(const LinShape& s, const LinFwdArgs& a);
 
 // Carved parts of a backward workspace, common to both algorithms.
 struct LinBwdParts {
-  float *eq, *ek;    // [slices(Dk)][B][Hv][T]
+  float *eq, *ek;    // [slices(Dk)][up to 2][B][Hv][T]
   float* xdot;       // [segments][B][Hv][slices(Dk)][4]
   float *pdq, *pdk;  // [B][T][Hv][Dk], only where value heads share a key head
   double* dgsum;     // [B][segments][Hv], only with a decay per head
@@ -120,8 +128,8 @@ LinChains lin_backward_chains(const LinShape& s, const LinBwdArgs& a, const LinB
 
 // dq, dk summed over the value heads of a key head; dg from e and xdot.
 // Sequences are cut in segments of seg tokens, each with its own xdot in
-// `dots` parts.
-hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p, int dots,
+// `dots` parts; e is in `es` parts.
+hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p, int es, int dots,
                                int64_t segments, int64_t seg, hipStream_t st);
 
 hipError_t launch_lin_zero(float* p, int n, hipStream_t st);  // p[0 .. n) = 0

@@ -147,7 +147,7 @@ gdr_status linear_backward(const gdr_linear_problem* p, const int64_t* cu, bool 
   }
   if (hipError_t e = gdr::launch_lin_seq(s, gdr::lin_backward_chains(s, a, parts), stream); e != hipSuccess)
     return done(e);
-  return done(gdr::launch_lin_bwd_tail(s, a, parts, gdr::lin_slices(s.Dk), 1, s.T, stream));
+  return done(gdr::launch_lin_bwd_tail(s, a, parts, gdr::lin_slices(s.Dk), gdr::lin_slices(s.Dk), 1, s.T, stream));
 }
 
 gdr_status check(const gdr_norm_problem* p) {

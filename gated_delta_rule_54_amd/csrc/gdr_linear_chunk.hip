@@ -11,13 +11,14 @@
 // One workgroup walks a segment of a sequence for one value head and a slice
 // of 64 columns with eight waves.  Waves 4 .. 7 carry the state: each keeps 16
 // columns of H in accumulators for the whole walk and leaves H in LDS, as
-// operands, for the chunk that comes.  Waves 0 .. 3 form the output's 16
-// columns each from it.  So the two products that depend on each other along
-// the sequence (H, and what is read from it) run side by side, on one SIMD an
-// output wave beside a state wave.  The accumulator layout of H is the operand
-// layout of X H when tile t takes rows 32 (t / 2) + 8 g + 4 (t % 2) + e (lane
-// group g, element e), so a lane hands its own registers over.  O is formed
-// transposed, a lane storing 4 consecutive columns of one token.
+// operands, for the chunk that comes.  Waves 0 .. 3 form the output from it.
+// So the two products that depend on each other along the sequence (H, and
+// what is read from it) run side by side, on one SIMD an output wave beside a
+// state wave.  Accumulators are operands without a move: H's tile t takes rows
+// 32 (t / 2) + 8 g + 4 (t % 2) + e (lane group g, element e), which is the
+// order of X's operands.  O is formed transposed, a lane storing 4 consecutive
+// columns of one token.  Output waves share the work by rows (out_by_rows)
+// where H is one operand, by columns (out_by_columns) where it is three.
 //
 // Precision.  bf16 inputs are matrix-core operands as they are.  What is
 // computed on the way (P, H, the decayed Z) is fp32: where a result is
@@ -65,6 +66,20 @@ __device__ __forceinline__ double prefix64(double x) {
   return dpp_step<0x143, 0xc>(x);
 }
 
+// The value of the first lane of each row of 16, of the wave's last lane.
+__device__ __forceinline__ double row_first(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), 0x150, 0xf, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), 0x150, 0xf, 0xf, false);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+__device__ __forceinline__ double last_lane(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(u), 63);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(u >> 32), 63);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
 // log2 of a token's decay factor.  A factor below 2^-185 is zero in every
 // product; the bound keeps -Inf out of the differences of sums.
 __device__ __forceinline__ double log2_decay(float g) {
@@ -91,7 +106,17 @@ struct OpB {
     return F{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
   }
   // columns j .. j + 7 of row i of P (place as p_at)
-  static __device__ __forceinline__ F prun(const E* P, int i, int j) { return run(P + i * C + ((j / 8) ^ (i & (C / 8 - 1))) * 8); }
+  static __device__ __forceinline__ F prun(const E* P, int i, int j) {
+    return run(P + i * C + ((j / 8) ^ (i & (C / 8 - 1))) * 8);
+  }
+  // Rows k0 + 4g .. +3 and k0 + 16 + 4g .. +3 of column n0 + lane % 16.
+  static __device__ __forceinline__ F pair(const E* M, int ld, int k0, int n0) {
+    const int p = lane_id() & 15, g = lane_id() >> 4;
+    const E* at = M + (k0 + 4 * g + (p >> 2)) * ld + n0 + 4 * (p & 3);
+    const bf16x4 a = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at));
+    const bf16x4 b = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 16 * ld)));
+    return F{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  }
   static __device__ __forceinline__ f32x4 mma(F a, F b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
@@ -152,11 +177,11 @@ struct OpF {
     for (int i = 0; i < 8; ++i) f.v[i] = at[i * ld];
     return f;
   }
-  static __device__ __forceinline__ F prun(const E* P, int i, int j) {
-    const E *a = P + i * C + ((j / 4) ^ (i & 7)) * 4, *b = P + i * C + ((j / 4 + 1) ^ (i & 7)) * 4;
+  static __device__ __forceinline__ F pair(const E* M, int ld, int k0, int n0) {
+    const E* at = M + (k0 + 4 * (lane_id() >> 4)) * ld + n0 + (lane_id() & 15);
     F f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) f.v[k] = a[k], f.v[4 + k] = b[k];
+    for (int i = 0; i < 4; ++i) f.v[i] = at[i * ld], f.v[4 + i] = at[(16 + i) * ld];
     return f;
   }
   static __device__ __forceinline__ f32x4 mma(const F& a, const F& b, f32x4 c) {
@@ -173,10 +198,6 @@ struct OpF {
     static_assert(NS == 1, "fp32 operands are exact");
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[0].v[i] = x[i];
-  }
-  template <int NS>
-  static __device__ __forceinline__ void put4(E* p, int, f32x4 x) {
-    *reinterpret_cast<f32x4*>(p) = x;
   }
 };
 
@@ -256,10 +277,11 @@ __device__ __forceinline__ int p_at(int i, int j) {
 
 // Decay factors of a chunk's rows.
 template <int C>
-struct Decay {
+struct alignas(16) Decay {
   double A[C];             // log2, running
   float fo[C], fz[C];      // 2^A_i, 2^(A_C - A_i)
-  float up[C], down[C];    // 2^(A_i - A_b), b the first row of i's block of 16; 2^(A_b' - A_i), b' that of the next block
+  float up[C];             // 2^(A_i - A_b), b the first row of i's block of 16
+  float down[C];           // 2^(A_b' - A_i), b' the first row of the next block
   float block[C / 16];     // 2^(A_b' - A_b)
   float all;               // 2^A_C
 };
@@ -315,16 +337,17 @@ struct Gates {
   template <int C>
   __device__ __forceinline__ double put(Decay<C>& d, bool rev) const {
     const int lane = lane_id();
-    const double g2 = log2_decay(g), inc = prefix64(g2), A = rev ? inc - g2 : inc, all = __shfl(inc, 63, 64);
-    const double Ab = __shfl(A, lane & ~15, 64), next = __shfl(A, ((lane & ~15) + 16) & 63, 64);
+    const double g2 = log2_decay(g), inc = prefix64(g2), A = rev ? inc - g2 : inc, all = last_lane(inc);
+    const double Ab = row_first(A), next = __shfl(A, ((lane & ~15) + 16) & 63, 64);
     const double An = lane < C - 16 ? next : A;
     if (lane < C) {
       d.A[lane] = A;
       d.fo[lane] = __builtin_amdgcn_exp2f(static_cast<float>(A));
       d.fz[lane] = __builtin_amdgcn_exp2f(static_cast<float>(all - A));
       d.up[lane] = __builtin_amdgcn_exp2f(static_cast<float>(A - Ab));
-      d.down[lane] = __builtin_amdgcn_exp2f(static_cast<float>(An - A));
-      if (lane % 16 == 0) d.block[lane / 16] = __builtin_amdgcn_exp2f(static_cast<float>(An - A));
+      const float down = __builtin_amdgcn_exp2f(static_cast<float>(An - A));
+      d.down[lane] = down;
+      if (lane % 16 == 0) d.block[lane / 16] = down;
     }
     if (lane == 0) d.all = __builtin_amdgcn_exp2f(static_cast<float>(all));
     return all;
@@ -376,16 +399,32 @@ __device__ __forceinline__ void update(f32x4 (&H)[D1P / 16], const typename OP::
   }
 }
 
-// LDS of a walk.
-template <typename OP, int D1P, int NS, bool EX>
-struct Shared {
+// LDS of a walk: XB buffers of the chunk's rows and HB of H, two of each where
+// they fit, so that one chunk's readers do not hold up the next one's writers;
+// P and the waves' parts of e where the output waves work by columns.
+template <typename OP, int D1P, int NS>
+struct Room {
   using T = Tiles<OP, D1P>;
   using E = typename OP::E;
-  alignas(16) E X[T::C * T::LD1], Y[T::C * T::LD1], Z[T::C * T::LDZ], P[NS * T::C * T::C];
-  typename OP::F H[4][T::KB][NS][64];  // [wave's columns][32 rows][operand][lane]
-  Decay<T::C> d;
-  float e[EX ? 4 : 1][T::C];
-  float x[4];
+  struct Chunk {
+    alignas(16) E X[T::C * T::LD1], Y[T::C * T::LD1], Z[T::C * T::LDZ];
+  };
+  struct State {
+    typename OP::F f[4][T::KB][NS][64];  // [16 columns][32 rows][operand][lane]
+  };
+  static constexpr bool COLS = NS > 1;
+  struct Rest {
+    Decay<T::C> d[COLS ? 1 : 2];
+    alignas(16) E P[COLS ? NS * T::C * T::C : 8];
+    float e[COLS ? 4 : 1][T::C];
+  };
+  static constexpr size_t kMax = 160 * 1024 - sizeof(Rest);
+  static constexpr int XB = 2 * sizeof(Chunk) + sizeof(State) <= kMax ? 2 : 1;
+  static constexpr int HB = XB == 2 && 2 * sizeof(Chunk) + 2 * sizeof(State) <= kMax && !COLS ? 2 : 1;
+  struct Buffers : Rest {
+    Chunk x[XB];
+    State h[HB];
+  };
 };
 
 // H for the output waves, as NS operands.
@@ -398,17 +437,107 @@ __device__ __forceinline__ void hand_over(const f32x4 (&H)[D1P / 16], S& s, int 
     typename OP::F f[NS];
     OP::template split<NS>(f, x);
 #pragma unroll
-    for (int k = 0; k < NS; ++k) s.H[cg][kb][k][lane_id()] = f[k];
+    for (int k = 0; k < NS; ++k) s.f[cg][kb][k][lane_id()] = f[k];
   }
 }
 
-// One walk over a segment of at least one token; H: the state waves' columns.
-//
-// Two barriers a chunk.  Up to the first, the output waves form X H and P and
-// the state waves update H; behind it, the output waves add P Z, the state
-// waves hand H over, and all write the next chunk's X, Y, Z.
-template <typename OP, int D1P, typename J, typename S>
-__device__ __forceinline__ void walk(const LinChains& a, const Walk& w, f32x4 (&H)[D1P / 16], S& s) {
+// The rows of a walk's chunks on their way through registers to LDS (by all
+// eight waves), and the gates (by one).
+template <typename OP, int D1P, typename R>
+struct Feed {
+  using E = typename OP::E;
+  static constexpr int C = OP::C;
+  Stage<OP, D1P, 512> x, y;
+  Stage<OP, kW2, 512> z;
+  Gates g;
+  int64_t len;
+  bool mine, rev;
+  __device__ __forceinline__ void init(const LinChains& a, const Walk& w, int wave) {
+    const LinChain& c = w.c;
+    x.init(walk_rows<E>(w, c.x, c.xr, c.xg, c.D1, 0, c.D1));
+    y.init(walk_rows<E>(w, c.y, c.yr, c.yg, c.D1, 0, c.D1));
+    z.init(walk_rows<E>(w, c.z, c.zr, c.zg, c.D2, w.col0, min(c.D2 - w.col0, kW2)));
+    g.init(a, w);
+    len = w.len, rev = c.rev;
+    mine = wave == (R::COLS ? 7 : 1);  // by rows, 16 .. 31 are little work
+  }
+  __device__ __forceinline__ int rows(int64_t at) const { return static_cast<int>(min(len - at, static_cast<int64_t>(C))); }
+  // Loads the chunk at `at`, if there is one.
+  __device__ __forceinline__ void fetch(int64_t at) {
+    if (at >= len) return;
+    const int n = rows(at);
+    x.load(n);
+    y.load(n);
+    z.load(n);
+  }
+  __device__ __forceinline__ void put(typename R::Chunk& to) const {
+    x.store(to.X);
+    y.store(to.Y);
+    z.store(to.Z);
+  }
+  // The decays of the chunk whose gates are loaded, and loads the next one's.
+  __device__ __forceinline__ void decays(Decay<C>& d, int64_t next) {
+    if (!mine) return;
+    g.put(d, rev);
+    if (next < len) g.load(next, rows(next));
+  }
+};
+
+// What a walk does around each chunk's work.  With two buffers of both kinds a
+// chunk takes one barrier: its readers work while the next chunk's rows are
+// written (loaded a chunk before) and the state waves hand the next H over.
+// With one buffer of H the state waves hand it over between two barriers,
+// behind its last reader; with one buffer of the rows these are loaded as the
+// chunk's work starts and written between the barriers too.
+template <typename OP, int D1P, typename R>
+__device__ __forceinline__ void walk_start(Feed<OP, D1P, R>& f, typename R::Buffers& s) {
+  f.fetch(0);
+  if (f.mine) f.g.load(0, f.rows(0));
+  f.decays(s.d[0], OP::C);
+  f.put(s.x[0]);
+  if constexpr (R::XB == 2) f.fetch(OP::C);
+}
+template <typename OP, int D1P, typename R>
+__device__ __forceinline__ void chunk_start(Feed<OP, D1P, R>& f, typename R::Buffers& s, int64_t at, int b) {
+  if (at + OP::C >= f.len) return;
+  if constexpr (R::XB == 2) {
+    f.put(s.x[b ^ 1]);
+    f.fetch(at + 2 * OP::C);
+  } else {
+    f.fetch(at + OP::C);
+  }
+  if constexpr (!R::COLS) f.decays(s.d[b ^ 1], at + 2 * OP::C);
+}
+template <typename OP, int D1P, typename R>
+__device__ __forceinline__ void chunk_end(Feed<OP, D1P, R>& f, typename R::Buffers& s, int64_t at) {
+  if (at + OP::C >= f.len) return;
+  if constexpr (R::XB == 1) f.put(s.x[0]);
+  if constexpr (R::COLS) f.decays(s.d[0], at + 2 * OP::C);
+}
+
+// The state waves' part of a walk.
+template <typename OP, int D1P, typename R, int NS>
+__device__ __forceinline__ void carry_state(f32x4 (&H)[D1P / 16], Feed<OP, D1P, R>& f, typename R::Buffers& s, int cg) {
+  constexpr int C = OP::C;
+  hand_over<OP, D1P, NS>(H, s.h[0], cg);
+  __syncthreads();
+  int b = 0;
+  for (int64_t at = 0; at < f.len; at += C, b ^= 1) {
+    chunk_start(f, s, at, b);
+    const auto& x = s.x[R::XB == 2 ? b : 0];
+    update<OP, D1P>(H, x.Y, x.Z, s.d[R::COLS ? 0 : b], 16 * cg);
+    if constexpr (R::HB == 1) __syncthreads();
+    chunk_end(f, s, at);
+    if (at + C < f.len) hand_over<OP, D1P, NS>(H, s.h[R::HB == 2 ? b ^ 1 : 0], cg);
+    __syncthreads();
+  }
+}
+
+// The output waves' part, a wave forming 16 rows of a chunk: X H and P of its
+// rows, and P Z from registers, without a barrier between.
+template <typename OP, int D1P, typename R, typename J>
+__device__ __forceinline__ void out_by_rows(const LinChains& a, const Walk& w, Feed<OP, D1P, R>& f,
+                                            typename R::Buffers& s, int wave) {
   using T = Tiles<OP, D1P>;
   using E = typename OP::E;
   using F = typename OP::F;
@@ -416,60 +545,174 @@ __device__ __forceinline__ void walk(const LinChains& a, const Walk& w, f32x4 (&
   constexpr bool EX = J::EX, WIDE = J::WIDE;
   constexpr uint32_t ES = sizeof(E);
   const LinChain& c = w.c;
-  const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6), cg = wave & 3;
-  const int m = lane & 15, g4 = 4 * (lane >> 4);
-  const int wc = 16 * cg;  // the wave's first column in the slice
-  const bool rev = c.rev, state = wave >= 4;
-  const int w2 = min(c.D2 - w.col0, kW2);
-
-  Stage<OP, D1P, 512> sx, sy;
-  Stage<OP, kW2, 512> sz;
-  sx.init(walk_rows<E>(w, c.x, c.xr, c.xg, c.D1, 0, c.D1));
-  sy.init(walk_rows<E>(w, c.y, c.yr, c.yg, c.D1, 0, c.D1));
-  sz.init(walk_rows<E>(w, c.z, c.zr, c.zg, c.D2, w.col0, w2));
-  auto rows_at = [&](int64_t at) { return static_cast<int>(min(w.len - at, static_cast<int64_t>(C))); };
-  auto fetch = [&](int64_t at) {
-    const int n = rows_at(at);
-    sx.load(n);
-    sy.load(n);
-    sz.load(n);
-  };
-  auto put = [&]() {
-    sx.store(s.X);
-    sy.store(s.Y);
-    sz.store(s.Z);
-  };
-  fetch(0);
-
-  if (state) {
-    Gates gates;
-    const bool mine = wave == 7;
-    if (mine) {
-      gates.init(a, w);
-      gates.load(0, rows_at(0));
-      gates.put(s.d, rev);
-    }
-    hand_over<OP, D1P, NS>(H, s, cg);
-    put();
-    __syncthreads();
-    for (int64_t at = 0; at < w.len; at += C) {
-      const bool more = at + C < w.len;
-      if (more) {
-        fetch(at + C);
-        if (mine) gates.load(at + C, rows_at(at + C));
-      }
-      update<OP, D1P>(H, s.Y, s.Z, s.d, wc);
-      __syncthreads();
-      if (more) {
-        hand_over<OP, D1P, NS>(H, s, cg);
-        put();
-        if (mine) gates.put(s.d, rev);
-      }
-      __syncthreads();
-    }
-    return;
+  const int lane = lane_id(), m = lane & 15, g4 = 4 * (lane >> 4), w2 = min(c.D2 - w.col0, kW2);
+  const bool rev = c.rev;
+  // The wave's 16 rows of a chunk and its NI tiles of 16 columns.
+  const int ib = wave % NI, ct0 = wave / NI * NI, i = 16 * ib + m;
+  constexpr uint32_t os = WIDE ? 4 : 2;
+  const int64_t first = rev ? w.len - 1 : 0;
+  const int64_t orow = (c.out_partial ? w.b * a.T + w.t0 : w.row0) + first;
+  Rows ro{static_cast<char*>(c.out) + ((orow * a.Hv + w.h) * c.D2 + w.col0) * os,
+          static_cast<uint32_t>(a.Hv) * c.D2 * os, w2 * os, rev};
+  const uint32_t oo = ro.row(i, C) + g4 * os;
+  Rows re{};
+  uint32_t oe = 0;
+  if constexpr (EX) {
+    re = walk_rows<E>(w, c.ex, c.er, c.eg, c.D2, w.col0, w2);
+    oe = re.row(i, C) + g4 * ES;
   }
+  // e in parts: a wave sums its NI tiles of columns
+  float* const ep = EX ? c.e + ((w.sl * (4 / NI) + wave / NI) * a.B * a.Hv + w.bh) * a.T + w.t0 : nullptr;
+  __syncthreads();
 
+  int b = 0;
+  for (int64_t at = 0; at < w.len; at += C, b ^= 1) {
+    const int n = f.rows(at);
+    chunk_start(f, s, at, b);
+    const auto& x = s.x[R::XB == 2 ? b : 0];
+    const auto& h = s.h[R::HB == 2 ? b : 0];
+    const auto& d = s.d[R::COLS ? 0 : b];
+    float ex[NI][4];
+    if constexpr (EX) {
+      const rsrc_t be = re.chunk(n);
+      const uint32_t at0 = oe - re.shift(n, C);
+      re.next(C);
+#pragma unroll
+      for (int t = 0; t < NI; ++t) {
+        const int col = 16 * (ct0 + t);
+        const uint32_t o = col < w2 ? at0 + col * ES : kNone;
+        if constexpr (ES == 2) {
+          const u32x2 u = __builtin_amdgcn_raw_buffer_load_b64(be, o, 0, 0);
+          ex[t][0] = __uint_as_float(u[0] << 16), ex[t][1] = __uint_as_float(u[0] & 0xffff0000u);
+          ex[t][2] = __uint_as_float(u[1] << 16), ex[t][3] = __uint_as_float(u[1] & 0xffff0000u);
+        } else {
+          const u32x4 u = __builtin_amdgcn_raw_buffer_load_b128(be, o, 0, 0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ex[t][e] = __uint_as_float(static_cast<unsigned>(u[e]));
+        }
+      }
+    }
+
+    // X H of the wave's rows, transposed; fragments are read a step ahead of
+    // the products that take them
+    f32x4 O[NI];
+#pragma unroll
+    for (int t = 0; t < NI; ++t) O[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    F xf[KB], hf[2][NI][NS];
+    auto read = [&](int kb) {
+      xf[kb] = OP::run(x.X + i * T::LD1 + 32 * kb + 2 * g4);
+#pragma unroll
+      for (int t = 0; t < NI; ++t)
+#pragma unroll
+        for (int q = 0; q < NS; ++q) hf[kb % 2][t][q] = h.f[ct0 + t][kb][q][lane];
+    };
+    read(0);
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      if (kb + 1 < KB) read(kb + 1);
+#pragma unroll
+      for (int q = NS - 1; q >= 0; --q)
+#pragma unroll
+        for (int t = 0; t < NI; ++t) O[t] = OP::mma(hf[kb % 2][t][q], xf[kb], O[t]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    const float fo = d.fo[i], up = d.up[i];
+    const double Ai = d.A[i];
+#pragma unroll
+    for (int t = 0; t < NI; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) O[t][e] *= fo;
+
+    // 32 columns of P at a time, transposed (the lane holds columns j .. j + 3
+    // of row i in each of two tiles), and O += P Z from them.  On the diagonal
+    // tile each factor 2^(A_i - A_j) is formed from its difference; below, it
+    // is 2^(A_i - A_b) 2^(A_b - A_b') 2^(A_b' - A_j), b the wave's first row and
+    // b' that of the block after j's.
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+      if (2 * ks <= ib) {
+        f32x4 S2[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            S2[t] = OP::mma(OP::run(x.Y + (32 * ks + 16 * t + m) * T::LD1 + 32 * kb + 2 * g4), xf[kb], S2[t]);
+        F zf[NI];
+#pragma unroll
+        for (int t = 0; t < NI; ++t) zf[t] = OP::pair(x.Z, T::LDZ, 32 * ks, 16 * (ct0 + t));
+        float p[8];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int jb = 2 * ks + t, j = 16 * jb + g4;
+          if (jb < ib) {
+            const f32x4 df = *reinterpret_cast<const f32x4*>(&d.down[j]);
+            float u = up;
+            for (int k = jb + 1; k < ib; ++k) u *= d.block[k];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[4 * t + e] = S2[t][e] * (u * df[e]);
+          } else if (jb == ib) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              p[4 * t + e] =
+                  j + e <= i ? S2[t][e] * __builtin_amdgcn_exp2f(static_cast<float>(Ai - d.A[j + e])) : 0.f;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[4 * t + e] = 0.f;
+          }
+        }
+        F pf[NS];
+        OP::template split<NS>(pf, p);
+#pragma unroll
+        for (int q = NS - 1; q >= 0; --q)
+#pragma unroll
+          for (int t = 0; t < NI; ++t) O[t] = OP::mma(zf[t], pf[q], O[t]);
+      }
+
+    const rsrc_t bo = ro.chunk(n);
+    const uint32_t at0 = oo - ro.shift(n, C);
+    ro.next(C);
+    float e = 0.f;
+#pragma unroll
+    for (int t = 0; t < NI; ++t) {
+      const f32x4 v = O[t];
+      const int col = 16 * (ct0 + t);
+      const uint32_t o = col < w2 ? at0 + col * os : kNone;
+      if constexpr (WIDE) {
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), bo, o, 0, 0);
+      } else {
+        const bf16x4 q{static_cast<__bf16>(v[0]), static_cast<__bf16>(v[1]), static_cast<__bf16>(v[2]),
+                       static_cast<__bf16>(v[3])};
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, q), bo, o, 0, 0);
+      }
+      if constexpr (EX) e += (ex[t][0] * v[0] + ex[t][1] * v[1]) + (ex[t][2] * v[2] + ex[t][3] * v[3]);
+    }
+    if constexpr (EX) {
+      e = rows4_sum(e);
+      const int64_t row = rev ? w.len - 1 - at - i : at + i;
+      if (lane < 16 && i < n) ep[row] = e;
+    }
+    if constexpr (R::HB == 1) __syncthreads();
+    chunk_end(f, s, at);
+    __syncthreads();
+  }
+}
+
+// The output waves' part, a wave forming 16 columns: it reads the operands of
+// its columns of H alone, which matters where H is three operands; the waves'
+// column blocks of P pass through LDS.
+template <typename OP, int D1P, typename R, typename J>
+__device__ __forceinline__ void out_by_columns(const LinChains& a, const Walk& w, Feed<OP, D1P, R>& f,
+                                               typename R::Buffers& s, int wave) {
+  using T = Tiles<OP, D1P>;
+  using E = typename OP::E;
+  using F = typename OP::F;
+  constexpr int C = T::C, NI = T::NI, KB = T::KB, KS = T::KS, NS = J::NS;
+  constexpr bool EX = J::EX, WIDE = J::WIDE;
+  constexpr uint32_t ES = sizeof(E);
+  const LinChain& c = w.c;
+  const int tid = threadIdx.x, lane = lane_id(), m = lane & 15, g4 = 4 * (lane >> 4), w2 = min(c.D2 - w.col0, kW2);
+  const bool rev = c.rev;
+  const int wc = 16 * wave;  // the wave's first column in the slice
   // output rows, and those of e's other factor
   constexpr uint32_t os = WIDE ? 4 : 2;
   const int64_t first = w.len - 1;
@@ -489,14 +732,15 @@ __device__ __forceinline__ void walk(const LinChains& a, const Walk& w, f32x4 (&
   int blk[NI];
 #pragma unroll
   for (int k = 0; k < NI; ++k) blk[k] = (jb + k) % NI;
-  put();
   __syncthreads();
 
-  for (int64_t at = 0; at < w.len; at += C) {
-    const int n = rows_at(at);
-    const bool more = at + C < w.len;
-    if (more) fetch(at + C);
-
+  int b = 0;
+  for (int64_t at = 0; at < w.len; at += C, b ^= 1) {
+    const int n = f.rows(at);
+    chunk_start(f, s, at, b);
+    const auto& x = s.x[R::XB == 2 ? b : 0];
+    const auto& h = s.h[0];
+    const auto& d = s.d[R::COLS ? 0 : b];
     // X H, and the wave's block of P; both transposed.  Fragments are read a
     // step ahead of the products that take them.
     f32x4 O[NI], S4[NI];
@@ -504,11 +748,11 @@ __device__ __forceinline__ void walk(const LinChains& a, const Walk& w, f32x4 (&
     for (int k = 0; k < NI; ++k) O[k] = S4[k] = f32x4{0.f, 0.f, 0.f, 0.f};
     F xf[2][NI], yf[2], hf[2][NS];
     auto read = [&](int kb) {
-      yf[kb % 2] = OP::run(s.Y + (16 * jb + m) * T::LD1 + 32 * kb + 2 * g4);
+      yf[kb % 2] = OP::run(x.Y + (16 * jb + m) * T::LD1 + 32 * kb + 2 * g4);
 #pragma unroll
-      for (int k = 0; k < NS; ++k) hf[kb % 2][k] = s.H[cg][kb][k][lane];
+      for (int k = 0; k < NS; ++k) hf[kb % 2][k] = h.f[wave][kb][k][lane];
 #pragma unroll
-      for (int k = 0; k < NI; ++k) xf[kb % 2][k] = OP::run(s.X + (16 * blk[k] + m) * T::LD1 + 32 * kb + 2 * g4);
+      for (int k = 0; k < NI; ++k) xf[kb % 2][k] = OP::run(x.X + (16 * blk[k] + m) * T::LD1 + 32 * kb + 2 * g4);
     };
     read(0);
 #pragma unroll
@@ -522,31 +766,27 @@ __device__ __forceinline__ void walk(const LinChains& a, const Walk& w, f32x4 (&
         for (int k = 0; k < NI; ++k) O[k] = OP::mma(hf[kb % 2][q], xf[kb % 2][k], O[k]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    // P = S o 2^(A_i - A_j): the lane holds rows j .. j + 3 of column i.  On
-    // the diagonal block (k = 0) each factor is formed from its difference;
-    // below, it is 2^(A_i - A_b) 2^(A_b - A_j), b the first row of i's block,
-    // whose second part takes one more block's factor from block to block.
+    // P = S o 2^(A_i - A_j): the lane holds rows j .. j + 3 of column i; the
+    // factors as in out_by_rows
     if (NI == 4 || wave < NI) {
       const int j = 16 * jb + g4;
-      float f[4];
+      f32x4 df = *reinterpret_cast<const f32x4*>(&d.down[j]);
 #pragma unroll
       for (int k = 0; k < NI; ++k) {
         const int i = 16 * blk[k] + m;
         f32x4 p;
         if (k == 0) {
-          const double Ai = s.d.A[i];
+          const double Ai = d.A[i];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            p[e] = j + e <= i ? S4[k][e] * __builtin_amdgcn_exp2f(static_cast<float>(Ai - s.d.A[j + e])) : 0.f;
-            f[e] = s.d.down[j + e];
-          }
+          for (int e = 0; e < 4; ++e)
+            p[e] = j + e <= i ? S4[k][e] * __builtin_amdgcn_exp2f(static_cast<float>(Ai - d.A[j + e])) : 0.f;
         } else {
-          const float u = s.d.up[i], bl = s.d.block[blk[k]];
           const bool below = jb + k < NI;
+          const float u = d.up[i], bl = d.block[blk[k]];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            p[e] = below ? S4[k][e] * (u * f[e]) : 0.f;
-            f[e] *= bl;
+            p[e] = below ? S4[k][e] * (u * df[e]) : 0.f;
+            df[e] *= bl;
           }
         }
         OP::template put4<NS>(s.P + p_at<OP>(i, j), C * C, p);
@@ -554,13 +794,13 @@ __device__ __forceinline__ void walk(const LinChains& a, const Walk& w, f32x4 (&
     }
 #pragma unroll
     for (int k = 0; k < NI; ++k) {
-      const float f = s.d.fo[16 * blk[k] + m];
+      const float fo = d.fo[16 * blk[k] + m];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) O[k][e] *= f;
+      for (int e = 0; e < 4; ++e) O[k][e] *= fo;
     }
     F zf[KS];
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) zf[ks] = OP::col(s.Z, T::LDZ, 32 * ks, wc, 4);
+    for (int ks = 0; ks < KS; ++ks) zf[ks] = OP::col(x.Z, T::LDZ, 32 * ks, wc, 4);
     float ex[NI][4];
     if constexpr (EX) {
       const rsrc_t be = re.chunk(n);
@@ -593,7 +833,7 @@ __device__ __forceinline__ void walk(const LinChains& a, const Walk& w, f32x4 (&
 #pragma unroll
         for (int k = 0; k < NI; ++k) O[k] = OP::mma(zf[ks], pf[k], O[k]);
       }
-    if (more) put();
+    chunk_end(f, s, at);
     const rsrc_t bo = ro.chunk(n);
     const uint32_t step = ro.step(16), at0 = oo - ro.shift(n, C);
     ro.next(C);
@@ -623,6 +863,18 @@ __device__ __forceinline__ void walk(const LinChains& a, const Walk& w, f32x4 (&
   }
 }
 
+// One walk over a segment of at least one token; H: the state waves' columns.
+template <typename OP, int D1P, typename R, typename J>
+__device__ __forceinline__ void walk(const LinChains& a, const Walk& w, f32x4 (&H)[D1P / 16], typename R::Buffers& s) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Feed<OP, D1P, R> f;
+  f.init(a, w, wave);
+  walk_start(f, s);
+  if (wave >= 4) carry_state<OP, D1P, R, J::NS>(H, f, s, wave & 3);
+  else if constexpr (R::COLS) out_by_columns<OP, D1P, R, J>(a, w, f, s, wave);
+  else out_by_rows<OP, D1P, R, J>(a, w, f, s, wave);
+}
+
 // Logical index of this workgroup: each of the 8 XCDs takes a contiguous
 // range, so that the workgroups that read the same rows share an L2.
 __device__ __forceinline__ int64_t xcd_index() {
@@ -634,16 +886,15 @@ __device__ __forceinline__ int64_t xcd_index() {
 // all chains of a head), then the value heads that share a key head, then
 // sequences, then segments, then key heads: an XCD's share is a range of key
 // heads, the same for sequences of any lengths.
-__device__ __forceinline__ bool find(const LinChains& a, Walk& w) {
+__device__ __forceinline__ bool find(const LinChains& a, int64_t k, Walk& w) {
   const int n0 = lin_slices(a.c[0].D2), n1 = a.n > 1 ? lin_slices(a.c[1].D2) : 0,
             n2 = a.n > 2 ? lin_slices(a.c[2].D2) : 0, all = n0 + n1 + n2;
-  const int64_t k = xcd_index();
   int s = static_cast<int>(k % all);
   const int64_t r = k / all;
   if (r >= a.B * a.Hv * a.segments) return false;
   const int ci = s < n0 ? 0 : s < n0 + n1 ? 1 : 2;
   s -= ci == 0 ? 0 : ci == 1 ? n0 : n0 + n1;
-  w.c = lin_chain(a, ci);
+  w.c = lin_chain(ci);
   w.sl = s;
   w.col0 = s * kW2;
   const int64_t per = a.group * a.B;
@@ -678,16 +929,18 @@ __device__ __forceinline__ void each_state(const LinChain& c, int col0, F&& f) {
 template <typename OP, int D1P, typename JA, typename JB>
 __global__ __launch_bounds__(512) void lin_chunk_kernel(LinChains a) {
   constexpr int NS = JA::NS > JB::NS ? JA::NS : JB::NS;
-  __shared__ Shared<OP, D1P, NS, JA::EX> s;
-  Walk w;
-  if (!find(a, w)) return;
-  const LinChain& c = w.c;
-  const int64_t one = static_cast<int64_t>(c.D1) * c.D2;
+  using R = Room<OP, D1P, NS>;
+  __shared__ typename R::Buffers s;
   const bool state = threadIdx.x >= 256;
-
+  int64_t index = xcd_index();
   f32x4 H[D1P / 16];
 #pragma unroll
   for (int t = 0; t < D1P / 16; ++t) H[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  {
+    Walk w;
+    if (!find(a, index, w)) return;
+  const LinChain& c = w.c;
+  const int64_t one = static_cast<int64_t>(c.D1) * c.D2;
   const float* in = c.seg_in ? c.seg_in + (w.bh * a.segments + w.seg) * one : c.s_in ? c.s_in + w.bh * one : nullptr;
   if (state && in)
     each_state<D1P>(c, w.col0, [&](int t, int64_t at) {
@@ -695,10 +948,18 @@ __global__ __launch_bounds__(512) void lin_chunk_kernel(LinChains a) {
       for (int e = 0; e < 4; ++e) H[t][e] = in[at + static_cast<int64_t>(e) * c.s1];
     });
   if (w.len > 0) {
-    if (!std::is_same_v<JA, JB> && c.key) walk<OP, D1P, JA>(a, w, H, s);
-    else walk<OP, D1P, JB>(a, w, H, s);
+    if (!std::is_same_v<JA, JB> && c.key) walk<OP, D1P, R, JA>(a, w, H, s);
+    else walk<OP, D1P, R, JB>(a, w, H, s);
+  }
   }
   if (!state) return;
+  // the place is found again: kept over the walk, it would crowd the walk's
+  // own scalars out of their registers
+  asm volatile("" : "+s"(index));
+  Walk w;
+  find(a, index, w);
+  const LinChain& c = w.c;
+  const int64_t one = static_cast<int64_t>(c.D1) * c.D2;
   if (c.xdot) {
     const float* dot = c.seg_dot ? c.seg_dot + (w.bh * a.segments + w.seg) * one : c.dot ? c.dot + w.bh * one : nullptr;
     float x = 0.f;
@@ -732,7 +993,7 @@ __global__ __launch_bounds__(256) void lin_segment_kernel(LinChains a, float* fa
   __shared__ __align__(16) E Ys[C * T::LD1], Zs[C * T::LDZ];
   __shared__ __align__(16) Decay<C> d;
   Walk w;
-  if (!find(a, w) || w.last) return;
+  if (!find(a, xcd_index(), w) || w.last) return;
   const LinChain& c = w.c;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w2 = min(c.D2 - w.col0, kW2);
   f32x4 H[D1P / 16];
@@ -949,7 +1210,9 @@ hipError_t launch_lin_chunk_bwd(const LinShape& s, const LinPlan& p, const LinBw
     });
     if (e != hipSuccess) return e;
   }
-  return launch_lin_bwd_tail(s, args, parts, 4 * lin_slices(s.Dk), p.segments, p.seg, st);
+  // by rows, chunks of 32 tokens leave e in two parts
+  const bool cols = s.io_bf16 && (!s.out_bf16 || args.dg), short_chunk = !s.io_bf16 || max_d1(a) > 128;
+  return launch_lin_bwd_tail(s, args, parts, lin_slices(s.Dk) * (short_chunk && !cols ? 2 : 1), 4 * lin_slices(s.Dk), p.segments, p.seg, st);
 }
 
 }  // namespace gdr

@@ -59,7 +59,7 @@ __global__ __launch_bounds__(256) void lin_seq_kernel(LinChains a) {
     blk -= heads * lin_slices(a.c[0].D2), ci = 1;
     if (blk >= heads * lin_slices(a.c[1].D2)) blk -= heads * lin_slices(a.c[1].D2), ci = 2;
   }
-  const LinChain c = lin_chain(a, ci);
+  const LinChain c = lin_chain(ci);
   const int nsl = lin_slices(c.D2), sl = static_cast<int>(blk % nsl);
   const int64_t bh = blk / nsl;
   const int h = static_cast<int>(bh % a.Hv);
@@ -292,8 +292,8 @@ size_t lin_bwd_parts(const LinShape& s, int64_t segments, char* base, LinBwdPart
     return at;
   };
   const size_t bh = static_cast<size_t>(s.B) * s.Hv, n = bh * s.T, nsl = lin_slices(s.Dk);
-  p->eq = reinterpret_cast<float*>(take(nsl * n * 4));
-  p->ek = reinterpret_cast<float*>(take(nsl * n * 4));
+  p->eq = reinterpret_cast<float*>(take(2 * nsl * n * 4));
+  p->ek = reinterpret_cast<float*>(take(2 * nsl * n * 4));
   p->xdot = reinterpret_cast<float*>(take(segments * bh * nsl * 4 * 4));
   const bool shared = s.Hv != s.Hk;
   p->pdq = reinterpret_cast<float*>(take(shared ? n * s.Dk * 4 : 0));
@@ -337,7 +337,7 @@ LinChains lin_backward_chains(const LinShape& s, const LinBwdArgs& a, const LinB
   return L;
 }
 
-hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p, int dots,
+hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p, int es, int dots,
                                int64_t segments, int64_t seg, hipStream_t st) {
   if (s.Hv != s.Hk) {
     ProfScope prof("linear_group_sum", st);
@@ -355,7 +355,7 @@ hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const Lin
   ProfScope prof("linear_dg", st);
   double* sums = s.head_decay ? p.dgsum : nullptr;
   lin_dg_kernel<<<static_cast<unsigned>(s.B * s.Hv * segments), 256, 0, st>>>(
-      p.eq, p.ek, p.xdot, lin_slices(s.Dk), dots, a.dg, sums, s.B, s.T, s.Hv, segments, seg, a.cu);
+      p.eq, p.ek, p.xdot, es, dots, a.dg, sums, s.B, s.T, s.Hv, segments, seg, a.cu);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   if (sums) lin_dg_head_kernel<<<s.Hv, 64, 0, st>>>(sums, a.dg, s.B * segments, s.Hv);
   return hipGetLastError();
