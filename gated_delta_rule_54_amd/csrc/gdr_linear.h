@@ -60,6 +60,7 @@ struct LinChain {
   float* s_out;         // null: not wanted
   int s1, s2;
   void* out;            // null: only the state is wanted
+  float* sum;           // chunked, summed over heads: fp32 [B][T][Hk][D2]
   int out_partial;      // 0: out type, rows of the batch; 1: fp32, [B][T] rows (a ragged batch has T rows per sequence)
   const void* ex;       // e_t = ex_t . out_t, ex [.., Hv / eg heads, D2], rows er elements apart; null: not wanted
   int64_t er;
@@ -85,6 +86,7 @@ struct LinChains {
   int out_bf16;
   const int64_t* cu;
   int64_t segments, seg;  // chunked: segments per sequence and tokens in each
+  int sum, head;          // chunked: dq and dk sum over heads, and this launch adds that of each key head
 };
 
 #ifdef __HIPCC__
@@ -120,17 +122,17 @@ LinChains lin_forward_chains(const LinShape& s, const LinFwdArgs& a);
 struct LinBwdParts {
   float *eq, *ek;    // [slices(Dk)][up to 2][B][Hv][T]
   float* xdot;       // [segments][B][Hv][slices(Dk)][4]
-  float *pdq, *pdk;  // [B][T][Hv][Dk], only where value heads share a key head
+  float *pdq, *pdk;  // only where value heads share a key head: [B][T][Hv][Dk], or sums [B][T][Hk][Dk]
   double* dgsum;     // [B][segments][Hv], only with a decay per head
 };
-size_t lin_bwd_parts(const LinShape& s, int64_t segments, char* base, LinBwdParts* p);  // returns its bytes
+size_t lin_bwd_parts(const LinShape& s, int64_t segments, bool summed, char* base, LinBwdParts* p);  // their bytes
 LinChains lin_backward_chains(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p);
 
 // dq, dk summed over the value heads of a key head; dg from e and xdot.
-// Sequences are cut in segments of seg tokens, each with its own xdot in
-// `dots` parts; e is in `es` parts.
-hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p, int es, int dots,
-                               int64_t segments, int64_t seg, hipStream_t st);
+// `summed`: dq and dk are complete.  Sequences are cut in segments of seg
+// tokens, each with its own xdot in `dots` parts; e is in `es` parts.
+hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p, bool summed, int es,
+                               int dots, int64_t segments, int64_t seg, hipStream_t st);
 
 hipError_t launch_lin_zero(float* p, int n, hipStream_t st);  // p[0 .. n) = 0
 
@@ -140,6 +142,7 @@ hipError_t launch_lin_seq(const LinShape& s, const LinChains& a, hipStream_t st)
 // states (forward: one direction, backward: both) and factors.
 struct LinPlan {
   int64_t segments, seg;
+  bool sum;              // backward: dq and dk are summed over a key head's value heads launch by launch
   size_t states, bytes;  // bytes of one direction's segment states; of all
 };
 LinPlan lin_plan(const LinShape& s, bool backward);

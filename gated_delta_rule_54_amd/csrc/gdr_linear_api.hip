@@ -63,8 +63,13 @@ LinShape shape_of(const gdr_linear_problem* p) {
 
 gdr_status done(hipError_t e) { return e == hipSuccess ? GDR_OK : gdr::record_hip_error(e); }
 
-// Shortest T at which AUTO takes the chunked kernels.
-constexpr int64_t kAutoForwardT = 16, kAutoBackwardT = 16;
+// Shortest T at which AUTO takes the chunked kernels, which take as long for a
+// few tokens as for a chunk.  Token by token against chunked, us, MI355X, 32
+// heads of 128 x 128, bf16: forward, 1 sequence 6.9 : 8.2 at T = 2 and 13.8 :
+// 8.2 at 8; 8 sequences 13.4 : 17.5 at 4, 18.6 : 16.9 at 8; 64 sequences 85 :
+// 122 at 4, 130 : 126 at 8.  VJP, 8 sequences 47 : 70 at 8, 71 : 71 at 16; 64
+// sequences 333 : 531 at 8, 546 : 535 at 16; 1 sequence 22 : 19 at 8.
+constexpr int64_t kAutoForwardT = 8, kAutoBackwardT = 16;
 bool chunked(const gdr_linear_problem* p, bool backward) {
   if (p->algo != GDR_ALGO_AUTO) return p->algo == GDR_ALGO_CHUNKED;
   return p->T >= (backward ? kAutoBackwardT : kAutoForwardT);
@@ -80,7 +85,7 @@ size_t backward_bytes(const gdr_linear_problem* p) {
   const gdr::LinPlan plan = gdr::lin_plan(s, true);
   const bool chunk = chunked(p, true);
   gdr::LinBwdParts parts;
-  return gdr::lin_bwd_parts(s, chunk ? plan.segments : 1, nullptr, &parts) + (chunk ? plan.bytes : 0);
+  return gdr::lin_bwd_parts(s, chunk ? plan.segments : 1, chunk && plan.sum, nullptr, &parts) + (chunk ? plan.bytes : 0);
 }
 
 gdr_status check_ws(const void* ws, size_t have, size_t need) {
@@ -132,9 +137,9 @@ gdr_status linear_backward(const gdr_linear_problem* p, const int64_t* cu, bool 
   const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
   const gdr::LinBwdArgs a{q, k, v, dout, g, h0, dht, dq, dk, dv, dg, dh0, cu};
   const bool chunk = !empty && chunked(p, true);
-  const gdr::LinPlan plan = chunk ? gdr::lin_plan(s, true) : gdr::LinPlan{1, s.T, 0, 0};
+  const gdr::LinPlan plan = chunk ? gdr::lin_plan(s, true) : gdr::LinPlan{1, s.T, false, 0, 0};
   gdr::LinBwdParts parts;
-  const size_t used = gdr::lin_bwd_parts(s, plan.segments, static_cast<char*>(ws), &parts);
+  const size_t used = gdr::lin_bwd_parts(s, plan.segments, plan.sum, static_cast<char*>(ws), &parts);
   if (chunk)
     return done(gdr::launch_lin_chunk_bwd(s, plan, a, parts, static_cast<char*>(ws) + used, stream));
   if (empty) {
@@ -147,7 +152,8 @@ gdr_status linear_backward(const gdr_linear_problem* p, const int64_t* cu, bool 
   }
   if (hipError_t e = gdr::launch_lin_seq(s, gdr::lin_backward_chains(s, a, parts), stream); e != hipSuccess)
     return done(e);
-  return done(gdr::launch_lin_bwd_tail(s, a, parts, gdr::lin_slices(s.Dk), gdr::lin_slices(s.Dk), 1, s.T, stream));
+  const int parted = gdr::lin_slices(s.Dk);
+  return done(gdr::launch_lin_bwd_tail(s, a, parts, false, parted, parted, 1, s.T, stream));
 }
 
 gdr_status check(const gdr_norm_problem* p) {

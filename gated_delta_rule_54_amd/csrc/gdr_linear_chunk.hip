@@ -28,6 +28,7 @@
 // fp32 inputs use fp32 operands.
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "gdr_device.h"
@@ -293,14 +294,17 @@ struct Walk {
   int64_t t0, len;           // the segment's first token in its sequence, its length
   int h, col0, sl;
   bool first, last;          // of the sequence's segments, in the chain's direction
+  bool more_heads, add;      // of a sum over heads: one follows; some went before
 };
 
 // What a walk computes.  NS: operands that P and H enter the output's products
-// as; EX: the terms e too; WIDE: the output is stored in fp32.
-template <int NS_, bool EX_, bool WIDE_>
+// as; EX: the terms e too; WIDE: the output is stored in fp32; SUM: the output
+// is summed over the value heads of a key head, one launch for each, in fp32
+// rows of the workspace until the last.
+template <int NS_, bool EX_, bool WIDE_, bool SUM_ = false>
 struct Job {
   static constexpr int NS = NS_;
-  static constexpr bool EX = EX_, WIDE = WIDE_;
+  static constexpr bool EX = EX_, WIDE = WIDE_, SUM = SUM_;
 };
 
 template <typename OP, int D1P>
@@ -351,6 +355,52 @@ struct Gates {
     }
     if (lane == 0) d.all = __builtin_amdgcn_exp2f(static_cast<float>(all));
     return all;
+  }
+};
+
+// Where an output wave stores: 4 columns of a row at a time.  Offsets are those
+// of the output's type; the sum's rows are fp32.
+template <typename J>
+struct Out {
+  static constexpr uint32_t SIZE = J::WIDE ? 4 : 2;
+  Rows o, p;
+  __device__ __forceinline__ void init(const LinChains& a, const Walk& w, int w2) {
+    const LinChain& c = w.c;
+    const bool rev = c.rev != 0;
+    const int64_t first = rev ? w.len - 1 : 0, bt = w.b * a.T + w.t0 + first;
+    const int heads = J::SUM ? a.Hv / a.group : a.Hv, h = J::SUM ? w.h / a.group : w.h;
+    const int64_t row = c.out_partial ? bt : w.row0 + first;
+    const uint32_t wide = static_cast<uint32_t>(heads) * c.D2;
+    o = Rows{static_cast<char*>(c.out) + ((row * heads + h) * c.D2 + w.col0) * SIZE, wide * SIZE, w2 * SIZE, rev};
+    if constexpr (J::SUM)
+      p = Rows{reinterpret_cast<char*>(c.sum) + ((bt * heads + h) * c.D2 + w.col0) * 4, wide * 4,
+               static_cast<uint32_t>(w2) * 4, rev};
+  }
+  // The sum so far at row i, column col (kNone: outside).
+  __device__ __forceinline__ f32x4 before(const Walk& w, int n, int C, int i, int col, bool on) const {
+    if (!w.add) return f32x4{0.f, 0.f, 0.f, 0.f};
+    const uint32_t at = p.row(i, C) + col * 4 - p.shift(n, C);
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(p.chunk(n), on ? at : kNone, 0, 0));
+  }
+  __device__ __forceinline__ void put(const Walk& w, int n, int C, int i, int col, bool on, f32x4 v) const {
+    if constexpr (J::SUM)
+      if (w.more_heads) {
+        const uint32_t at = p.row(i, C) + col * 4 - p.shift(n, C);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), p.chunk(n), on ? at : kNone, 0, 0);
+        return;
+      }
+    const uint32_t at = on ? o.row(i, C) + col * SIZE - o.shift(n, C) : kNone;
+    if constexpr (J::WIDE) {
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), o.chunk(n), at, 0, 0);
+    } else {
+      const bf16x4 q{static_cast<__bf16>(v[0]), static_cast<__bf16>(v[1]), static_cast<__bf16>(v[2]),
+                     static_cast<__bf16>(v[3])};
+      __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, q), o.chunk(n), at, 0, 0);
+    }
+  }
+  __device__ __forceinline__ void next(int C) {
+    o.next(C);
+    if constexpr (J::SUM) p.next(C);
   }
 };
 
@@ -542,19 +592,15 @@ __device__ __forceinline__ void out_by_rows(const LinChains& a, const Walk& w, F
   using E = typename OP::E;
   using F = typename OP::F;
   constexpr int C = T::C, NI = T::NI, KB = T::KB, KS = T::KS, NS = J::NS;
-  constexpr bool EX = J::EX, WIDE = J::WIDE;
+  constexpr bool EX = J::EX;
   constexpr uint32_t ES = sizeof(E);
   const LinChain& c = w.c;
   const int lane = lane_id(), m = lane & 15, g4 = 4 * (lane >> 4), w2 = min(c.D2 - w.col0, kW2);
   const bool rev = c.rev;
   // The wave's 16 rows of a chunk and its NI tiles of 16 columns.
   const int ib = wave % NI, ct0 = wave / NI * NI, i = 16 * ib + m;
-  constexpr uint32_t os = WIDE ? 4 : 2;
-  const int64_t first = rev ? w.len - 1 : 0;
-  const int64_t orow = (c.out_partial ? w.b * a.T + w.t0 : w.row0) + first;
-  Rows ro{static_cast<char*>(c.out) + ((orow * a.Hv + w.h) * c.D2 + w.col0) * os,
-          static_cast<uint32_t>(a.Hv) * c.D2 * os, w2 * os, rev};
-  const uint32_t oo = ro.row(i, C) + g4 * os;
+  Out<J> out;
+  out.init(a, w, w2);
   Rows re{};
   uint32_t oe = 0;
   if constexpr (EX) {
@@ -592,6 +638,11 @@ __device__ __forceinline__ void out_by_rows(const LinChains& a, const Walk& w, F
         }
       }
     }
+
+    f32x4 pv[NI];
+    if constexpr (J::SUM)
+#pragma unroll
+      for (int t = 0; t < NI; ++t) pv[t] = out.before(w, n, C, i, 16 * (ct0 + t) + g4, 16 * (ct0 + t) < w2);
 
     // X H of the wave's rows, transposed; fragments are read a step ahead of
     // the products that take them
@@ -668,24 +719,16 @@ __device__ __forceinline__ void out_by_rows(const LinChains& a, const Walk& w, F
           for (int t = 0; t < NI; ++t) O[t] = OP::mma(zf[t], pf[q], O[t]);
       }
 
-    const rsrc_t bo = ro.chunk(n);
-    const uint32_t at0 = oo - ro.shift(n, C);
-    ro.next(C);
     float e = 0.f;
 #pragma unroll
     for (int t = 0; t < NI; ++t) {
       const f32x4 v = O[t];
       const int col = 16 * (ct0 + t);
-      const uint32_t o = col < w2 ? at0 + col * os : kNone;
-      if constexpr (WIDE) {
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), bo, o, 0, 0);
-      } else {
-        const bf16x4 q{static_cast<__bf16>(v[0]), static_cast<__bf16>(v[1]), static_cast<__bf16>(v[2]),
-                       static_cast<__bf16>(v[3])};
-        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, q), bo, o, 0, 0);
-      }
       if constexpr (EX) e += (ex[t][0] * v[0] + ex[t][1] * v[1]) + (ex[t][2] * v[2] + ex[t][3] * v[3]);
+      if constexpr (J::SUM) out.put(w, n, C, i, col + g4, col < w2, v + pv[t]);
+      else out.put(w, n, C, i, col + g4, col < w2, v);
     }
+    out.next(C);
     if constexpr (EX) {
       e = rows4_sum(e);
       const int64_t row = rev ? w.len - 1 - at - i : at + i;
@@ -707,20 +750,15 @@ __device__ __forceinline__ void out_by_columns(const LinChains& a, const Walk& w
   using E = typename OP::E;
   using F = typename OP::F;
   constexpr int C = T::C, NI = T::NI, KB = T::KB, KS = T::KS, NS = J::NS;
-  constexpr bool EX = J::EX, WIDE = J::WIDE;
+  constexpr bool EX = J::EX;
   constexpr uint32_t ES = sizeof(E);
   const LinChain& c = w.c;
   const int tid = threadIdx.x, lane = lane_id(), m = lane & 15, g4 = 4 * (lane >> 4), w2 = min(c.D2 - w.col0, kW2);
   const bool rev = c.rev;
   const int wc = 16 * wave;  // the wave's first column in the slice
-  // output rows, and those of e's other factor
-  constexpr uint32_t os = WIDE ? 4 : 2;
-  const int64_t first = w.len - 1;
-  const int64_t orow = c.out_partial ? w.b * a.T + w.t0 + (rev ? first : 0) : w.row0 + (rev ? first : 0);
-  Rows ro{static_cast<char*>(c.out) + ((orow * a.Hv + w.h) * c.D2 + w.col0) * os,
-          static_cast<uint32_t>(a.Hv) * c.D2 * os, w2 * os, rev};
+  Out<J> out;
+  out.init(a, w, w2);
   Rows re{};
-  const uint32_t oo = ro.row(m, C) + (wc + g4) * os;
   uint32_t oe = 0;
   if constexpr (EX) {
     re = walk_rows<E>(w, c.ex, c.er, c.eg, c.D2, w.col0, w2);
@@ -801,6 +839,10 @@ __device__ __forceinline__ void out_by_columns(const LinChains& a, const Walk& w
     F zf[KS];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) zf[ks] = OP::col(x.Z, T::LDZ, 32 * ks, wc, 4);
+    f32x4 pv[NI];
+    if constexpr (J::SUM)
+#pragma unroll
+      for (int k = 0; k < NI; ++k) pv[k] = out.before(w, n, C, 16 * blk[k] + m, wc + g4, has);
     float ex[NI][4];
     if constexpr (EX) {
       const rsrc_t be = re.chunk(n);
@@ -834,25 +876,17 @@ __device__ __forceinline__ void out_by_columns(const LinChains& a, const Walk& w
         for (int k = 0; k < NI; ++k) O[k] = OP::mma(zf[ks], pf[k], O[k]);
       }
     chunk_end(f, s, at);
-    const rsrc_t bo = ro.chunk(n);
-    const uint32_t step = ro.step(16), at0 = oo - ro.shift(n, C);
-    ro.next(C);
 #pragma unroll
     for (int k = 0; k < NI; ++k) {
       const f32x4 v = O[k];
-      const uint32_t o = has ? at0 + blk[k] * step : kNone;
-      if constexpr (WIDE) {
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), bo, o, 0, 0);
-      } else {
-        const bf16x4 q{static_cast<__bf16>(v[0]), static_cast<__bf16>(v[1]), static_cast<__bf16>(v[2]),
-                       static_cast<__bf16>(v[3])};
-        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, q), bo, o, 0, 0);
-      }
+      if constexpr (J::SUM) out.put(w, n, C, 16 * blk[k] + m, wc + g4, has, v + pv[k]);
+      else out.put(w, n, C, 16 * blk[k] + m, wc + g4, has, v);
       if constexpr (EX) {
         const float e = rows4_sum((ex[k][0] * v[0] + ex[k][1] * v[1]) + (ex[k][2] * v[2] + ex[k][3] * v[3]));
         if (lane < 16) s.e[wave][16 * blk[k] + m] = e;
       }
     }
+    out.next(C);
     __syncthreads();
     if constexpr (EX) {
       if (tid < n) {
@@ -875,41 +909,56 @@ __device__ __forceinline__ void walk(const LinChains& a, const Walk& w, f32x4 (&
   else out_by_rows<OP, D1P, R, J>(a, w, f, s, wave);
 }
 
-// Logical index of this workgroup: each of the 8 XCDs takes a contiguous
-// range, so that the workgroups that read the same rows share an L2.
-__device__ __forceinline__ int64_t xcd_index() {
-  const int64_t per = (static_cast<int64_t>(gridDim.x) + 7) / 8;
-  return static_cast<int64_t>(blockIdx.x % 8) * per + blockIdx.x / 8;
+// The launch's units of work: one chain, slice, segment, sequence and value
+// head each, or, in a sum over heads, key head (and the launch's value head of
+// it).  Those of the dq and dk chains come first: they take longest.  Within either kind slices are fastest, then
+// the value heads that share a key head, then sequences, then segments, then
+// key heads; and each of the 8 XCDs takes a contiguous range, so that units
+// that read the same rows share an L2, and as much of it as the others,
+// whatever the sequences' lengths.
+struct Units {
+  int64_t early, late;  // per XCD
+};
+__host__ __device__ inline Units units(const LinChains& a) {
+  int n = 0, keys = 0;
+  for (int i = 0; i < a.n; ++i) (a.c[i].key ? keys : n) += lin_slices(a.c[i].D2);
+  const int64_t heads = a.B * a.Hv * a.segments;
+  const int64_t early = keys * (a.sum ? heads / a.group : heads), late = n * heads;
+  return Units{(early + 7) / 8, (late + 7) / 8};
 }
 
-// Finds the workgroup's place; false: nothing to do.  Slices are fastest (of
-// all chains of a head), then the value heads that share a key head, then
-// sequences, then segments, then key heads: an XCD's share is a range of key
-// heads, the same for sequences of any lengths.
-__device__ __forceinline__ bool find(const LinChains& a, int64_t k, Walk& w) {
-  const int n0 = lin_slices(a.c[0].D2), n1 = a.n > 1 ? lin_slices(a.c[1].D2) : 0,
-            n2 = a.n > 2 ? lin_slices(a.c[2].D2) : 0, all = n0 + n1 + n2;
-  int s = static_cast<int>(k % all);
-  const int64_t r = k / all;
-  if (r >= a.B * a.Hv * a.segments) return false;
-  const int ci = s < n0 ? 0 : s < n0 + n1 ? 1 : 2;
-  s -= ci == 0 ? 0 : ci == 1 ? n0 : n0 + n1;
+// Finds the workgroup's unit; false: nothing to do.
+__device__ __forceinline__ bool find(const LinChains& a, const Units& u, int64_t block, Walk& w) {
+  const int64_t xcd = block % 8, k = block / 8;
+  const bool early = k < u.early;
+  const int64_t index = early ? xcd * u.early + k : xcd * u.late + k - u.early;
+  const int first = early || a.n < 3 ? 0 : 2, end = early ? 2 : a.n;
+  const int n0 = lin_slices(a.c[first == 2 ? 2 : 0].D2), all = n0 + (end - first > 1 ? lin_slices(a.c[1].D2) : 0);
+  int s = static_cast<int>(index % all);
+  int64_t r = index / all;
+  const int group = early && a.sum ? 1 : a.group, heads = early && a.sum ? a.Hv / a.group : a.Hv;
+  if (r >= a.B * heads * a.segments) return false;
+  const int ci = s < n0 ? first : first + 1;
+  s -= ci == first ? 0 : n0;
   w.c = lin_chain(ci);
   w.sl = s;
   w.col0 = s * kW2;
-  const int64_t per = a.group * a.B;
-  w.b = r % per / a.group;
+  const int64_t per = group * a.B;
+  w.b = r % per / group;
   w.seg = r / per % a.segments;
-  w.h = static_cast<int>(r / (per * a.segments)) * a.group + static_cast<int>(r % a.group);
+  w.h = static_cast<int>(r / (per * a.segments)) * group + static_cast<int>(r % group);
+  if (early && a.sum) w.h = w.h * a.group + a.head;
   w.bh = w.b * a.Hv + w.h;
   const LinSpan sp = lin_span(a.cu, w.b, a.T);
   w.t0 = w.seg * a.seg;
   if (w.t0 >= sp.len && w.seg > 0) return false;
   w.len = min(a.seg, sp.len - w.t0);
   w.row0 = sp.t0 + w.t0;
-  const bool begin = w.seg == 0, end = w.t0 + w.len >= sp.len;
-  w.first = w.c.rev ? end : begin;
-  w.last = w.c.rev ? begin : end;
+  const bool begin = w.seg == 0, last = w.t0 + w.len >= sp.len;
+  w.first = w.c.rev ? last : begin;
+  w.last = w.c.rev ? begin : last;
+  w.add = a.head > 0;
+  w.more_heads = a.head + 1 < a.group;
   return true;
 }
 
@@ -925,39 +974,24 @@ __device__ __forceinline__ void each_state(const LinChain& c, int col0, F&& f) {
   }
 }
 
-// JA: the job of the dq and dk chains, JB: that of the others.
-template <typename OP, int D1P, typename JA, typename JB>
-__global__ __launch_bounds__(512) void lin_chunk_kernel(LinChains a) {
-  constexpr int NS = JA::NS > JB::NS ? JA::NS : JB::NS;
-  using R = Room<OP, D1P, NS>;
-  __shared__ typename R::Buffers s;
-  const bool state = threadIdx.x >= 256;
-  int64_t index = xcd_index();
-  f32x4 H[D1P / 16];
-#pragma unroll
-  for (int t = 0; t < D1P / 16; ++t) H[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  {
-    Walk w;
-    if (!find(a, index, w)) return;
+// A unit's state waves load the state it starts from.
+template <int D1P>
+__device__ __forceinline__ void load_state(const LinChains& a, const Walk& w, f32x4 (&H)[D1P / 16]) {
   const LinChain& c = w.c;
   const int64_t one = static_cast<int64_t>(c.D1) * c.D2;
+#pragma unroll
+  for (int t = 0; t < D1P / 16; ++t) H[t] = f32x4{0.f, 0.f, 0.f, 0.f};
   const float* in = c.seg_in ? c.seg_in + (w.bh * a.segments + w.seg) * one : c.s_in ? c.s_in + w.bh * one : nullptr;
-  if (state && in)
+  if (in)
     each_state<D1P>(c, w.col0, [&](int t, int64_t at) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) H[t][e] = in[at + static_cast<int64_t>(e) * c.s1];
     });
-  if (w.len > 0) {
-    if (!std::is_same_v<JA, JB> && c.key) walk<OP, D1P, R, JA>(a, w, H, s);
-    else walk<OP, D1P, R, JB>(a, w, H, s);
-  }
-  }
-  if (!state) return;
-  // the place is found again: kept over the walk, it would crowd the walk's
-  // own scalars out of their registers
-  asm volatile("" : "+s"(index));
-  Walk w;
-  find(a, index, w);
+}
+
+// What they leave at its end: <state, dot> and the state.
+template <int D1P>
+__device__ __forceinline__ void leave_state(const LinChains& a, const Walk& w, const f32x4 (&H)[D1P / 16]) {
   const LinChain& c = w.c;
   const int64_t one = static_cast<int64_t>(c.D1) * c.D2;
   if (c.xdot) {
@@ -981,19 +1015,46 @@ __global__ __launch_bounds__(512) void lin_chunk_kernel(LinChains a) {
   }
 }
 
+// JA: the job of the dq and dk chains, JB: that of the others.
+template <typename OP, int D1P, typename JA, typename JB>
+__global__ __launch_bounds__(512) void lin_chunk_kernel(LinChains a, Units u) {
+  constexpr int NS = JA::NS > JB::NS ? JA::NS : JB::NS;
+  using R = Room<OP, D1P, NS>;
+  __shared__ typename R::Buffers s;
+  const bool state = threadIdx.x >= 256;
+  f32x4 H[D1P / 16];
+  int64_t block = blockIdx.x;
+  {
+    Walk w;
+    if (!find(a, u, block, w)) return;
+    if (state) load_state<D1P>(a, w, H);
+    if (w.len > 0) {
+      if (!std::is_same_v<JA, JB> && w.c.key) walk<OP, D1P, R, JA>(a, w, H, s);
+      else walk<OP, D1P, R, JB>(a, w, H, s);
+    }
+  }
+  if (!state) return;
+  // the unit is found again: kept over the walk, it would crowd the walk's
+  // own scalars out of their registers
+  asm volatile("" : "+s"(block));
+  Walk w;
+  find(a, u, block, w);
+  leave_state<D1P>(a, w, H);
+}
+
 // Every segment's own contribution to the state at its end (in the chain's
 // direction), from zero, by four state waves.  The last segment's is not
 // needed.  The chain forward in time leaves the segments' factors, but the
 // last one's, which only the chain backward in time needs and leaves.
 template <typename OP, int D1P>
-__global__ __launch_bounds__(256) void lin_segment_kernel(LinChains a, float* factor) {
+__global__ __launch_bounds__(256) void lin_segment_kernel(LinChains a, Units u, float* factor) {
   using T = Tiles<OP, D1P>;
   using E = typename OP::E;
   constexpr int C = T::C;
   __shared__ __align__(16) E Ys[C * T::LD1], Zs[C * T::LDZ];
   __shared__ __align__(16) Decay<C> d;
   Walk w;
-  if (!find(a, xcd_index(), w) || w.last) return;
+  if (!find(a, u, blockIdx.x, w) || w.last) return;
   const LinChain& c = w.c;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w2 = min(c.D2 - w.col0, kW2);
   f32x4 H[D1P / 16];
@@ -1058,21 +1119,6 @@ __global__ __launch_bounds__(256) void lin_scan_kernel(float* fwd, float* rev, c
   }
 }
 
-// Cutting sequences: workgroups wanted in the launch, the shortest segment.
-#ifndef TG
-#define TG 256
-#endif
-#ifndef MS
-#define MS 256
-#endif
-constexpr int64_t kTargetGroups = TG, kMinSegment = MS;
-
-unsigned chunk_blocks(const LinChains& a) {
-  int64_t all = 0;
-  for (int i = 0; i < a.n; ++i) all += lin_slices(a.c[i].D2);
-  return static_cast<unsigned>((all * a.B * a.Hv * a.segments + 7) / 8 * 8);
-}
-
 int max_d1(const LinChains& a) {
   int d = 0;
   for (int i = 0; i < a.n; ++i) d = std::max(d, a.c[i].D1);
@@ -1081,27 +1127,29 @@ int max_d1(const LinChains& a) {
 
 template <typename OP, int D1P, typename JA, typename JB = JA>
 hipError_t run_chunks(const LinChains& a, hipStream_t st) {
-  lin_chunk_kernel<OP, D1P, JA, JB><<<chunk_blocks(a), 512, 0, st>>>(a);
+  const Units u = units(a);
+  lin_chunk_kernel<OP, D1P, JA, JB><<<static_cast<unsigned>(8 * (u.early + u.late)), 512, 0, st>>>(a, u);
   return hipGetLastError();
 }
 
 template <typename OP, int D1P>
 hipError_t run_segments(const LinChains& a, float* factor, hipStream_t st) {
-  lin_segment_kernel<OP, D1P><<<chunk_blocks(a), 256, 0, st>>>(a, factor);
+  const Units u = units(a);
+  lin_segment_kernel<OP, D1P><<<static_cast<unsigned>(8 * (u.early + u.late)), 256, 0, st>>>(a, u, factor);
   return hipGetLastError();
 }
 
-// The kernel of a VJP: whether e is wanted, dq and dk go to fp32 parts, and
-// dv is returned in fp32 (then dq and dk are stored in fp32 in any case).
-template <typename OP, int D1P>
-hipError_t run_vjp(const LinChains& a, bool ex, bool part, bool wide, hipStream_t st) {
-  constexpr int N = OP::FULL;
-  if (wide) return ex ? run_chunks<OP, D1P, Job<N, true, true>, Job<N, false, true>>(a, st)
-                      : run_chunks<OP, D1P, Job<N, false, true>>(a, st);
-  if (ex) return part ? run_chunks<OP, D1P, Job<N, true, true>, Job<1, false, false>>(a, st)
-                      : run_chunks<OP, D1P, Job<N, true, false>, Job<1, false, false>>(a, st);
-  return part ? run_chunks<OP, D1P, Job<1, false, true>, Job<1, false, false>>(a, st)
-              : run_chunks<OP, D1P, Job<1, false, false>>(a, st);
+// The kernel of a VJP: whether e is wanted, dv is returned in fp32, dq and dk
+// are summed over heads launch by launch, or stored per value head in fp32.
+template <typename OP, int D1P, bool WIDE>
+hipError_t run_vjp(const LinChains& a, bool ex, bool sum, bool part, hipStream_t st) {
+  constexpr int N = OP::FULL, M = WIDE ? N : 1;  // operands with e, without
+  using JB = Job<M, false, WIDE>;
+  if (sum) return ex ? run_chunks<OP, D1P, Job<N, true, WIDE, true>, JB>(a, st)
+                     : run_chunks<OP, D1P, Job<M, false, WIDE, true>, JB>(a, st);
+  if (part || WIDE) return ex ? run_chunks<OP, D1P, Job<N, true, true>, JB>(a, st)
+                              : run_chunks<OP, D1P, Job<M, false, true>, JB>(a, st);
+  return ex ? run_chunks<OP, D1P, Job<N, true, WIDE>, JB>(a, st) : run_chunks<OP, D1P, Job<M, false, WIDE>, JB>(a, st);
 }
 
 // Calls f with the operand type and the padded width (an integral constant).
@@ -1117,23 +1165,64 @@ hipError_t by_type(bool io_bf16, int d1, F&& f) {
 
 }  // namespace
 
-// One direction's segment states, then their factors.
+// Cutting sequences.  A workgroup walks a segment's tokens one chunk after
+// another and a compute unit holds one workgroup, so a launch takes rounds of
+// 256 of them.  More segments fill the last round, or the only one, but cost a
+// pass that forms their states; a launch for each value head of a key head saves
+// the sum over them, but has fewer workgroups.  The plan with the
+// least estimated time is taken, from what was measured on MI355X at D = 128
+// (ns a token of a walk; smaller heads change all alike):
+//   a walk 45 (forward), 54 (VJP: 768 workgroups of 4096 tokens 664 us), and
+//   4 us to begin and end;
+//   the segment pass 29 with one workgroup on a compute unit, 15 more for each
+//   further one (16 segments of 2048 tokens 59 us, 32 of 1024 45 us);
+//   the scan 4 us, 0.3 us a segment and its states both ways at 4 TB/s;
+//   the sum over heads 5 us and 5.5 TB/s, a further launch 3 us.
+// What the rule chose, against the other side: VJP of 4 x 4096 tokens, 16 key
+// and 32 value heads, summed by launches 754-812 us, with the sum's pass 843;
+// of 1 x 4096 tokens, summed and in 4 segments 257-268, whole with the pass 274;
+// of 16384 tokens of 8 heads 234 in 16 segments, 334 in 11; forward of 333
+// tokens, fp32, 24 in segments of 64, 34 of 192; of 4 x 4096 tokens 182 whole,
+// 264 cut.
 LinPlan lin_plan(const LinShape& s, bool backward) {
-  LinPlan p{};
-  const int slices = backward ? 2 * lin_slices(s.Dk) + lin_slices(s.Dv) : lin_slices(s.Dv);
-  const int64_t groups = std::max<int64_t>(1, s.B * s.Hv) * slices;
-  const int64_t want = (kTargetGroups + groups - 1) / groups, most = (s.T + kMinSegment - 1) / kMinSegment;
-  const int64_t n = std::max<int64_t>(1, std::min(want, most));
-  p.seg = std::max<int64_t>(64, ((s.T + n - 1) / n + 63) / 64 * 64);
-  p.segments = std::max<int64_t>(1, (s.T + p.seg - 1) / p.seg);
-  if (p.segments > 1) {
-    const size_t bh = static_cast<size_t>(s.B) * s.Hv * p.segments;
-    p.states = bh * s.Dk * s.Dv * sizeof(float);
-    p.bytes = (backward ? 2 : 1) * p.states + (bh * sizeof(float) + 255) / 256 * 256;
+  LinPlan best{};
+  double least = 0.0;
+  const double bh = static_cast<double>(std::max<int64_t>(1, s.B * s.Hv)), bk = bh * s.Hk / s.Hv, group = s.Hv / s.Hk;
+  const double keys = backward ? 2.0 * lin_slices(s.Dk) : 0.0, rest = lin_slices(s.Dv);
+  const double token = backward ? 54e-3 : 45e-3;  // us
+  auto rounds = [](double n) { return std::ceil(n / 256.0); };
+  int64_t seg_before = 0;
+  for (int64_t n = 1; n <= 256; n += (n + 7) / 8) {
+    const int64_t seg = std::max<int64_t>(64, ((s.T + n - 1) / n + 63) / 64 * 64);
+    if (seg == seg_before) continue;
+    seg_before = seg;
+    const int64_t segments = std::max<int64_t>(1, (s.T + seg - 1) / seg);
+    const double m = static_cast<double>(segments), walk = 4.0 + seg * token, ways = backward ? 2.0 : 1.0;
+    double pre = 0.0;
+    if (segments > 1)
+      pre = seg * (29e-3 + 15e-3 * (rounds(ways * bh * rest * m) - 1)) + 4.0 + 0.3 * m +
+            2e-6 * ways * bh * m * s.Dk * s.Dv * sizeof(float) / 4.0;
+    for (int sum = 0; sum <= (backward && group > 1 ? 1 : 0); ++sum) {
+      double us = pre;
+      if (sum) us += (walk * rounds(bk * keys * m) + 3.0) * (group - 1) + walk * rounds((bk * keys + bh * rest) * m);
+      else us += walk * rounds(bh * (keys + rest) * m);
+      if (backward && group > 1 && !sum) us += 5.0 + 1e-6 * bh * s.T * s.Dk * 16.0 / 5.5;
+      if (best.segments == 0 || us < least) {
+        least = us;
+        best.segments = segments, best.seg = seg, best.sum = sum != 0;
+      }
+    }
+    if (seg == 64) break;
   }
-  return p;
+  if (best.segments > 1) {
+    const size_t n = static_cast<size_t>(s.B) * s.Hv * best.segments;
+    best.states = n * s.Dk * s.Dv * sizeof(float);
+    best.bytes = (backward ? 2 : 1) * best.states + (n * sizeof(float) + 255) / 256 * 256;
+  }
+  return best;
 }
 
+// One direction's segment states, then their factors.
 LinSegs lin_segs(const LinPlan& p, bool backward, char* base) {
   LinSegs g{};
   if (p.segments == 1) return g;
@@ -1203,16 +1292,32 @@ hipError_t launch_lin_chunk_bwd(const LinShape& s, const LinPlan& p, const LinBw
     a.c[1].seg_in = a.c[2].seg_in = g.rev;
   }
   a.c[0].key = a.c[1].key = 1;
+  if (p.sum) {
+    a.c[0].out = args.dq, a.c[1].out = args.dk;
+    a.c[0].out_partial = a.c[1].out_partial = 0;
+    a.c[0].sum = parts.pdq, a.c[1].sum = parts.pdk;
+  }
   {
     ProfScope prof("linear_chunks_vjp", st);
-    const hipError_t e = by_type(s.io_bf16, max_d1(a), [&](auto op, auto d1) {
-      return run_vjp<decltype(op), decltype(d1)::value>(a, args.dg != nullptr, s.Hv != s.Hk, !s.out_bf16, st);
-    });
-    if (e != hipSuccess) return e;
+    // summed over heads, dv joins the last of a key head's launches
+    a.sum = p.sum;
+    const int group = a.group;
+    for (a.head = p.sum ? 0 : group - 1; a.head < group; ++a.head) {
+      a.n = a.head + 1 < group ? 2 : 3;
+      const hipError_t e = by_type(s.io_bf16, std::max(s.Dk, s.Dv), [&](auto op, auto d1) {
+        using OP = decltype(op);
+        constexpr int D1P = decltype(d1)::value;
+        const bool ex = args.dg != nullptr, part = s.Hv != s.Hk && !p.sum;
+        return s.out_bf16 ? run_vjp<OP, D1P, false>(a, ex, p.sum, part, st)
+                          : run_vjp<OP, D1P, true>(a, ex, p.sum, part, st);
+      });
+      if (e != hipSuccess) return e;
+    }
   }
   // by rows, chunks of 32 tokens leave e in two parts
   const bool cols = s.io_bf16 && (!s.out_bf16 || args.dg), short_chunk = !s.io_bf16 || max_d1(a) > 128;
-  return launch_lin_bwd_tail(s, args, parts, lin_slices(s.Dk) * (short_chunk && !cols ? 2 : 1), 4 * lin_slices(s.Dk), p.segments, p.seg, st);
+  const int es = lin_slices(s.Dk) * (short_chunk && !cols ? 2 : 1);
+  return launch_lin_bwd_tail(s, args, parts, p.sum, es, 4 * lin_slices(s.Dk), p.segments, p.seg, st);
 }
 
 }  // namespace gdr

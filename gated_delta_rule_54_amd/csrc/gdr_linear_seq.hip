@@ -190,12 +190,15 @@ __global__ __launch_bounds__(256) void lin_group_sum_kernel(const float* pdq, co
 // dg of one segment of one sequence and value head: the suffix sums of
 // e_q - e_k from the segment's end, on top of <S, dS> there.  The sums run in
 // 64 bits: they telescope to what the later tokens of the segment give, so
-// their terms cancel.  One workgroup walks its segment from the end, 256
-// tokens at a time.
-__global__ __launch_bounds__(256) void lin_dg_kernel(const float* eq, const float* ek, const float* xdot, int nsl,
-                                                     int dots, float* dg, double* dgsum, int64_t B, int64_t T, int Hv,
-                                                     int64_t segments, int64_t seg, const int64_t* cu) {
-  __shared__ double wsum[4];
+// their terms cancel.  One workgroup walks its segment from the end, 1024
+// tokens at a time: a step is a chain of latencies (loads, shuffles, two
+// barriers), so long ones are worth their idle lanes in short segments.
+constexpr int kDgStep = 1024;
+__global__ __launch_bounds__(kDgStep) void lin_dg_kernel(const float* eq, const float* ek, const float* xdot, int nsl,
+                                                         int dots, float* dg, double* dgsum, int64_t B, int64_t T,
+                                                         int Hv, int64_t segments, int64_t seg, const int64_t* cu) {
+  constexpr int W = kDgStep / 64;
+  __shared__ double wsum[W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t s = blockIdx.x % segments, bh = blockIdx.x / segments, b = bh / Hv;
   const int h = static_cast<int>(bh % Hv);
@@ -203,15 +206,20 @@ __global__ __launch_bounds__(256) void lin_dg_kernel(const float* eq, const floa
   const int64_t t0 = s * seg, t1 = sp.len < t0 + seg ? sp.len : t0 + seg;
   double carry = 0.0, total = 0.0;
   for (int j = 0; j < dots; ++j) carry += xdot[(s * B * Hv + bh) * dots + j];
-  for (int64_t end = t1; end > t0; end -= 256) {
-    const int64_t t = end - 1 - tid;
+  auto term = [&](int64_t t) {
     double v = 0.0;
     if (t >= t0)
       for (int j = 0; j < nsl; ++j) {
         const int64_t at = (j * B * Hv + bh) * T + t;
         v += static_cast<double>(eq[at]) - static_cast<double>(ek[at]);
       }
-    double p = v;
+    return v;
+  };
+  double next = term(t1 - 1 - tid);
+  for (int64_t end = t1; end > t0; end -= kDgStep) {
+    const int64_t t = end - 1 - tid;
+    double p = next;
+    next = term(t - kDgStep);
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) {
       const double q = __shfl_up(p, m, 64);
@@ -221,7 +229,7 @@ __global__ __launch_bounds__(256) void lin_dg_kernel(const float* eq, const floa
     __syncthreads();
     double base = carry, all = 0.0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < W; ++w) {
       if (w < wave) base += wsum[w];
       all += wsum[w];
     }
@@ -238,7 +246,11 @@ __global__ __launch_bounds__(256) void lin_dg_kernel(const float* eq, const floa
     for (int m = 1; m < 64; m <<= 1) total += __shfl_xor(total, m, 64);
     if (lane == 0) wsum[wave] = total;
     __syncthreads();
-    if (tid == 0) dgsum[(b * segments + s) * Hv + h] = (wsum[0] + wsum[1]) + (wsum[2] + wsum[3]);
+    if (tid == 0) {
+      double all = 0.0;
+      for (int w = 0; w < W; ++w) all += wsum[w];
+      dgsum[(b * segments + s) * Hv + h] = all;
+    }
   }
 }
 
@@ -284,7 +296,7 @@ LinChains lin_forward_chains(const LinShape& s, const LinFwdArgs& a) {
   return L;
 }
 
-size_t lin_bwd_parts(const LinShape& s, int64_t segments, char* base, LinBwdParts* p) {
+size_t lin_bwd_parts(const LinShape& s, int64_t segments, bool summed, char* base, LinBwdParts* p) {
   size_t off = 0;
   auto take = [&](size_t bytes) {
     char* at = base ? base + off : nullptr;  // null: sizes only
@@ -295,9 +307,9 @@ size_t lin_bwd_parts(const LinShape& s, int64_t segments, char* base, LinBwdPart
   p->eq = reinterpret_cast<float*>(take(2 * nsl * n * 4));
   p->ek = reinterpret_cast<float*>(take(2 * nsl * n * 4));
   p->xdot = reinterpret_cast<float*>(take(segments * bh * nsl * 4 * 4));
-  const bool shared = s.Hv != s.Hk;
-  p->pdq = reinterpret_cast<float*>(take(shared ? n * s.Dk * 4 : 0));
-  p->pdk = reinterpret_cast<float*>(take(shared ? n * s.Dk * 4 : 0));
+  const size_t heads = s.Hv == s.Hk ? 0 : summed ? s.Hk : s.Hv, part = heads * s.B * s.T * s.Dk * 4;
+  p->pdq = reinterpret_cast<float*>(take(part));
+  p->pdk = reinterpret_cast<float*>(take(part));
   p->dgsum = reinterpret_cast<double*>(take(s.head_decay ? segments * bh * 8 : 0));
   return off;
 }
@@ -337,9 +349,9 @@ LinChains lin_backward_chains(const LinShape& s, const LinBwdArgs& a, const LinB
   return L;
 }
 
-hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p, int es, int dots,
-                               int64_t segments, int64_t seg, hipStream_t st) {
-  if (s.Hv != s.Hk) {
+hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const LinBwdParts& p, bool summed, int es,
+                               int dots, int64_t segments, int64_t seg, hipStream_t st) {
+  if (s.Hv != s.Hk && !summed) {
     ProfScope prof("linear_group_sum", st);
     const int64_t n = s.B * s.T * s.Hk * (s.Dk / 4);
     const dim3 grid(static_cast<unsigned>((n + 255) / 256), 2);
@@ -354,7 +366,7 @@ hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const Lin
   if (!a.dg) return hipSuccess;
   ProfScope prof("linear_dg", st);
   double* sums = s.head_decay ? p.dgsum : nullptr;
-  lin_dg_kernel<<<static_cast<unsigned>(s.B * s.Hv * segments), 256, 0, st>>>(
+  lin_dg_kernel<<<static_cast<unsigned>(s.B * s.Hv * segments), kDgStep, 0, st>>>(
       p.eq, p.ek, p.xdot, es, dots, a.dg, sums, s.B, s.T, s.Hv, segments, seg, a.cu);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   if (sums) lin_dg_head_kernel<<<s.Hv, 64, 0, st>>>(sums, a.dg, s.B * segments, s.Hv);
