@@ -136,6 +136,7 @@ hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const Lin
 
 hipError_t launch_lin_zero(float* p, int n, hipStream_t st);  // p[0 .. n) = 0
 
+hipError_t launch_lin_token(const LinShape& s, const LinChains& a, hipStream_t st);  // forward, T = 1
 hipError_t launch_lin_seq(const LinShape& s, const LinChains& a, hipStream_t st);
 
 // Chunked algorithm.  How a problem is cut, and its workspace: the segments'

@@ -114,7 +114,10 @@ gdr_status linear_forward(const gdr_linear_problem* p, const int64_t* cu, bool r
   const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
   if (s.T > 0 && chunked(p, false))
     return done(gdr::launch_lin_chunk_fwd(s, gdr::lin_plan(s, false), a, static_cast<char*>(ws), stream));
-  return done(gdr::launch_lin_seq(s, gdr::lin_forward_chains(s, a), stream));
+  const gdr::LinChains chains = gdr::lin_forward_chains(s, a);
+  // the sequential algorithm adds in one order however a sequence is cut into calls
+  const bool token = s.T == 1 && p->algo == GDR_ALGO_AUTO;
+  return done(token ? gdr::launch_lin_token(s, chains, stream) : gdr::launch_lin_seq(s, chains, stream));
 }
 
 gdr_status linear_backward(const gdr_linear_problem* p, const int64_t* cu, bool ragged, const void* q, const void* k,

@@ -53,10 +53,10 @@ def _row_stride(t, name):
     """Elements between the rows of t [..., rows, H, D] whose last two axes
     are dense and whose rows are equally spaced over all leading axes; 0 where
     they follow each other without a gap."""
+    if t.is_contiguous() or t.numel() == 0:
+        return 0
     shape, stride = t.shape, t.stride()
     H, D = shape[-2], shape[-1]
-    if t.numel() == 0 or t.is_contiguous():
-        return 0
     ok = (D == 1 or stride[-1] == 1) and (H == 1 or stride[-2] == D)
     row, n = None, 1
     for s, st in zip(reversed(shape[:-2]), reversed(stride[:-2])):
@@ -73,6 +73,8 @@ def _row_stride(t, name):
 
 def _want(t, name, shape, dtype, dev, contiguous=True):
     if t is None:
+        return
+    if t.shape == shape and t.dtype == dtype and t.device == dev and (not contiguous or t.is_contiguous()):
         return
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")

@@ -1,0 +1,214 @@
+"""Single tokens of linear attention, and the rules with the group norm of
+their outputs as a layer runs them: prefill, single tokens, VJP, captured.
+
+Tolerances of the rule and of the norm are those of their own tests: n 2^-24 of
+the sums of absolute values for a sum through n roundings, and
+c = 16 (D + 32) 2^-24 of the factors' magnitudes for a row of the norm.  Of both
+together: the derivative of n = (x - mean) / sd by x is a projection over sd, so
+an error of x moves y = (w n + b) silu(z) by at most max |w silu(z)| / sd of its
+2-norm within the group.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_54_amd as gdr
+from gated_delta_rule_54_amd.synth import make_inputs, round_bf16
+from oracle import linear_oracle as lo
+
+pytestmark = pytest.mark.gpu
+
+BF, F = torch.bfloat16, torch.float32
+U = 2.0 ** -24
+
+
+def dev(a, dt=F):
+    return None if a is None else torch.from_numpy(np.ascontiguousarray(a)).cuda().to(dt)
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+def inputs(seed, B, T, Hk, Hv, Dk, Dv, io=F, gate="token"):
+    r = np.random.default_rng(seed)
+    n = lambda *s: r.standard_normal(s).astype(np.float32)
+    x = dict(q=n(B, T, Hk, Dk) * Dk ** -0.5, k=n(B, T, Hk, Dk), v=n(B, T, Hv, Dv), z=n(B, T, Hv, Dv),
+             dy=n(B, T, Hv, Dv))
+    if io == BF:
+        x = {a: round_bf16(t) for a, t in x.items()}
+    x["g"] = {"token": -np.logaddexp(0, n(B, T, Hv)), "head": -2.0 ** -np.arange(Hv), "none": None}[gate]
+    x["h0"] = 0.5 * n(B, Hv, Dk, Dv)
+    x["w"], x["b"] = 1 + 0.2 * n(Hv, Dv), 0.3 * n(Hv, Dv)
+    return {a: t if t is None else t.astype(np.float32) for a, t in x.items()}
+
+
+def bounded(name, got, ref, A, n, out):
+    tol = n * U * A + 1e-30
+    if out == BF:
+        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+    assert got.shape == ref.shape and (np.abs(got - ref) <= tol).all(), (name, np.max(np.abs(got - ref) / tol))
+
+
+@pytest.mark.parametrize("Dk,Dv", [(16, 16), (128, 128), (64, 80), (256, 48), (48, 256), (112, 192)])
+@pytest.mark.parametrize("io,out", [(BF, BF), (BF, F), (F, F), (F, BF)])
+@pytest.mark.parametrize("gate", ["token", "head", "none"])
+def test_single_token(Dk, Dv, io, out, gate):
+    x = inputs(Dk + Dv, 3, 1, 2, 6, Dk, Dv, io, gate)
+    t = {a: dev(v, io if a in "qkv" else F) for a, v in x.items()}
+    n = Dk + 64 + 4
+    for h0 in (x["h0"], None):
+        args = x["q"], x["k"], x["v"], x["g"], h0
+        (o, ht), (Ao, Ah) = lo.forward(*args), lo.forward_abs(*args)[:2]
+        s = None if h0 is None else t["h0"].clone()
+        got, st = gdr.gdr_linear_forward(t["q"], t["k"], t["v"], t["g"], s, out_dtype=out)
+        bounded("o", host(got), o, Ao, n, out)
+        bounded("ht", host(st), ht, Ah, n, F)
+        only, none = gdr.gdr_linear_forward(t["q"], t["k"], t["v"], t["g"], s, ht=None, out_dtype=out)
+        assert none is None and torch.equal(only, got)
+        if s is not None:
+            over, same = gdr.gdr_linear_forward(t["q"], t["k"], t["v"], t["g"], s, ht=s, out_dtype=out)
+            assert same is s and torch.equal(over, got) and torch.equal(s, st)
+
+
+@pytest.mark.parametrize("Dv", [64, 144])
+def test_single_tokens_of_a_ragged_batch(Dv):
+    """Sequences of one token or none, rows between and behind them, q, k and v
+    cut out of one projection's rows."""
+    Hk, Hv, Dk, rows = 2, 4, 64, 9
+    x = inputs(5, 1, rows, Hk, Hv, Dk, Dv, BF)
+    x["h0"] = np.concatenate([x["h0"]] * 5)
+    cu = [0, 1, 1, 2, 2, 3]  # lengths 1, 0, 1, 0, 1: six rows left over
+    wide = torch.cat([dev(x[a], BF).flatten(2) for a in "qkv"], -1)
+    c = np.cumsum([0] + [x[a].shape[2] * x[a].shape[3] for a in "qkv"])
+    q, k, v = (wide[..., c[i]:c[i + 1]].unflatten(-1, x[a].shape[2:]) for i, a in enumerate("qkv"))
+    o = torch.full((1, rows, Hv, Dv), 7.0, device="cuda")
+    h0 = dev(x["h0"])
+    _, ht = gdr.gdr_linear_forward(q, k, v, dev(x["g"]), h0, o=o, cu_seqlens=torch.tensor(cu, device="cuda"),
+                                   max_seqlen=1)
+    assert (o[:, 3:] == 7.0).all()
+    for i in range(5):
+        if cu[i + 1] == cu[i]:
+            assert torch.equal(ht[i], h0[i])
+            continue
+        r = slice(cu[i], cu[i + 1])
+        args = x["q"][:, r], x["k"][:, r], x["v"][:, r], x["g"][:, r], x["h0"][i:i + 1]
+        bounded("o", host(o[:, r]), lo.forward(*args)[0], lo.forward_abs(*args)[0], Dk + 68, F)
+        bounded("ht", host(ht[i:i + 1]), lo.forward(*args)[1], lo.forward_abs(*args)[1], Dk + 68, F)
+
+
+def silu(z):
+    return z / (1 + np.exp(-z.astype(np.float64)))
+
+
+def norm_bound(x, w, b, sz, center):
+    """Bound of the norm's own rounding, from its factors' magnitudes."""
+    D = x.shape[-1]
+    d = x - (x.mean(-1, keepdims=True) if center else 0)
+    n = np.abs(d) / np.sqrt((d * d).mean(-1, keepdims=True) + 1e-5)
+    top = np.max(n, -1, keepdims=True)
+    return 16 * (D + 32) * U * (np.abs(w) * top + np.abs(b)) * np.abs(sz)
+
+
+def near(y, o, x, center):
+    ref = lo.norm_forward(host(o), x["w"], x["b"], x["z"], center=center)
+    assert (np.abs(host(y) - ref) <= norm_bound(host(o), x["w"], x["b"], silu(x["z"]), center)).all()
+
+
+@pytest.mark.parametrize("center", [True, False])
+@pytest.mark.parametrize("T,steps", [(150, 3), (1, 2), (0, 2)])
+def test_prefill_then_tokens_with_norm(center, T, steps):
+    """A layer's serving run: the prompt, then tokens from its state; each
+    output through the gated norm, against both in 64 bits."""
+    B, Hk, Hv, Dk, Dv = 2, 2, 4, 64, 128
+    x = inputs(3, B, T + steps, Hk, Hv, Dk, Dv)
+    args = x["q"], x["k"], x["v"], x["g"], x["h0"]
+    o64, A = lo.forward(*args)[0], lo.forward_abs(*args)[0]
+    y64 = lo.norm_forward(o64, x["w"], x["b"], x["z"], center=center)
+    t = {a: dev(v) for a, v in x.items()}
+    s, out = t["h0"].clone(), []
+    for r in [slice(0, T)] + [slice(i, i + 1) for i in range(T, T + steps)]:
+        q, k, v, g, z = (t[a][:, r].contiguous() for a in ("q", "k", "v", "g", "z"))
+        o, _ = gdr.gdr_linear_forward(q, k, v, g, s, ht=s)
+        out.append(gdr.gdr_group_norm_forward(o, t["w"], t["b"], z, center=center))
+    y = host(torch.cat(out, 1))
+    sz = silu(x["z"])
+    d = o64 - (o64.mean(-1, keepdims=True) if center else 0)
+    sd = np.sqrt((d * d).mean(-1) + 1e-5)
+    rule = (Dk + 4 * (T + steps) + 64) * U * np.linalg.norm(A, axis=-1)
+    tol = np.max(np.abs(x["w"] * sz), -1) / sd * rule + np.linalg.norm(norm_bound(o64, x["w"], x["b"], sz, center),
+                                                                       axis=-1)
+    assert (np.linalg.norm(y - y64, axis=-1) <= tol).all()
+
+
+@pytest.mark.parametrize("T", [5, 130])
+def test_training_step_with_norm(T):
+    """Forward and VJP of the rule and the norm together: each stage against 64
+    bits from the values that the stage before left."""
+    B, Hk, Hv, Dk, Dv = 2, 2, 4, 64, 128
+    x = inputs(4, B, T, Hk, Hv, Dk, Dv)
+    t = {a: dev(v) for a, v in x.items()}
+    rule = t["q"], t["k"], t["v"], t["g"], t["h0"]
+    o, _ = gdr.gdr_linear_forward(*rule)
+    y = gdr.gdr_group_norm_forward(o, t["w"], t["b"], t["z"], center=True)
+    do, dz, dw, db = gdr.gdr_group_norm_backward(o, t["w"], t["b"], t["z"], t["dy"], center=True)
+    got = gdr.gdr_linear_backward(*rule, do)
+    near(y, o, x, True)
+    want = lo.norm_backward(host(o), x["w"], x["b"], x["z"], x["dy"], center=True)
+    for name, a, b in zip(("dx", "dz", "dw", "db"), (do, dz, dw, db), want):
+        terms = B * T if name in ("dw", "db") else 0
+        two = np.linalg.norm(host(a) - b) / np.linalg.norm(b)
+        assert two <= 16 * np.sqrt(Dv + 32 + terms) * U, (name, two)
+    args = tuple(x[a] for a in ("q", "k", "v", "g", "h0")) + (host(do),)
+    ref, A = lo.backward(*args), lo.backward_abs(*args)
+    for name, a, b, c in zip(("dq", "dk", "dv", "dg", "dh0"), got, ref, A):
+        bounded(name, host(a), b, c, Dk + Dv + 8 * T + 64 * (Hv // Hk), F)
+
+
+def test_norm_of_the_delta_rule():
+    """The gated norm on the outputs of the gated delta rule, and its gradient
+    into that rule's VJP."""
+    B, T, Hk, Hv, D = 1, 96, 2, 4, 128
+    i = make_inputs(7, B, T, Hk, Hv, D, D, "bf16")
+    t = {a: dev(i[a], BF if a in ("q", "k", "v") else F) for a in ("q", "k", "v", "g", "beta", "h0")}
+    x = inputs(8, B, T, Hk, Hv, D, D, BF)
+    z, dy, w, b = dev(x["z"]), dev(x["dy"]), dev(x["w"]), dev(x["b"])
+    o = gdr.gdr_forward(t["q"], t["k"], t["v"], t["g"], t["beta"], t["h0"], out_dtype=F)[0]
+    y = gdr.gdr_group_norm_forward(o, w, b, z)
+    do = gdr.gdr_group_norm_backward(o, w, b, z, dy)[0]
+    near(y, o, x, False)
+    ref = lo.norm_backward(host(o), x["w"], x["b"], x["z"], x["dy"])[0]
+    assert np.linalg.norm(host(do) - ref) <= 16 * np.sqrt(D + 32) * U * np.linalg.norm(ref)
+    for a in gdr.gdr_backward(t["q"], t["k"], t["v"], t["g"], t["beta"], t["h0"], do.to(BF)):
+        assert a is None or torch.isfinite(a).all()
+
+
+def test_layer_captured_and_replayed():
+    """Forward and VJP of the layer in one graph on a stream of its own, with
+    eager calls of the same shapes between replays: the eager bits every time."""
+    B, T, Hk, Hv, D = 2, 300, 2, 8, 64
+    x = inputs(9, B, T, Hk, Hv, D, D, BF)
+    t = {a: dev(v, BF if a in ("q", "k", "v", "z", "dy") else F) for a, v in x.items()}
+
+    def step():
+        rule = t["q"], t["k"], t["v"], t["g"], t["h0"]
+        o, ht = gdr.gdr_linear_forward(*rule, out_dtype=BF)
+        y = gdr.gdr_group_norm_forward(o, t["w"], t["b"], t["z"], out_dtype=BF)
+        do, *p = gdr.gdr_group_norm_backward(o, t["w"], t["b"], t["z"], t["dy"], out_dtype=BF)
+        one = tuple(a[:, :1].contiguous() for a in rule[:4])
+        return (y, ht, *p, *gdr.gdr_linear_backward(*rule, do, out_dtype=BF), *gdr.gdr_linear_forward(*one, ht))
+
+    want = step()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        got = step()
+    for _ in range(3):
+        for a in got:
+            a.fill_(float("nan"))
+        graph.replay()
+        again = step()
+        torch.cuda.synchronize()
+        for a, b, c in zip(got, want, again):
+            assert torch.equal(a, b) and torch.equal(c, b)
