@@ -391,6 +391,55 @@ def bench_vjp_sweep(torch, gdr):
     return out
 
 
+def bench_linear_attention(torch, gdr, steps=10):
+    """The operators beside the rule at the step's shape: linear attention with
+    a decay and the gated norm of its outputs, forward, VJP and one token from
+    a state (states rotating, as in the decode leg); time per call of both
+    from events around back-to-back calls, bf16 in and out."""
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    rn = lambda *s: torch.randn(*s, device="cuda", generator=gen)
+    bf = torch.bfloat16
+    q, k = (rn(B, T, HK, D).to(bf) for _ in range(2))
+    v, z, dy = (rn(B, T, HV, D).to(bf) for _ in range(3))
+    q = q * D ** -0.5
+    g = -torch.nn.functional.softplus(rn(B, T, HV))
+    w, b = 1 + 0.1 * rn(HV, D), 0.1 * rn(HV, D)
+    states = [rn(B, HV, D, D) * 0.02 for _ in range(DEC_BUFFERS)]
+
+    def forward():
+        o, _ = gdr.gdr_linear_forward(q, k, v, g, states[0], out_dtype=bf)
+        return o, gdr.gdr_group_norm_forward(o, w, b, z, center=True, out_dtype=bf)
+
+    o, _ = forward()
+
+    def vjp():
+        do = gdr.gdr_group_norm_backward(o, w, b, z, dy, center=True, out_dtype=bf)[0]
+        gdr.gdr_linear_backward(q, k, v, g, states[0], do, out_dtype=bf)
+
+    tok = [t[:, :1].contiguous() for t in (q, k, v, g, z)]
+    turn = iter(range(1 << 30))
+
+    def token():
+        s = states[next(turn) % DEC_BUFFERS]
+        o1, _ = gdr.gdr_linear_forward(*tok[:4], s, ht=s, out_dtype=bf)
+        gdr.gdr_group_norm_forward(o1, w, b, tok[4], center=True, out_dtype=bf)
+
+    out = {}
+    for name, call, reps in (("forward", forward, steps), ("vjp", vjp, steps), ("token", token, 20 * steps)):
+        for _ in range(3):
+            call()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        for _ in range(reps):
+            call()
+        e1.record()
+        torch.cuda.synchronize()
+        out[f"{name}_us"] = round(1000.0 * e0.elapsed_time(e1) / reps, 2)
+    out["config"] = (f"B={B} T={T} Hk={HK} Hv={HV} Dk=Dv={D}, bf16 io, decay per token and head, then the "
+                     "centred norm gated by silu(z)")
+    return out
+
+
 def bench_channelwise_decode(torch, gdr, t_prefill=2048, steps=128):
     """Channelwise gate: a B=1 prefill of t_prefill tokens (chunked), then
     `steps` single-token steps carrying the state in place (Hk=16, Hv=32,
@@ -612,8 +661,8 @@ def _cpu_model():
 
 def variants(torch, gdr, args, tokens):
     """The other measured legs: the same step with fused gates and with the
-    stateless VJP, the channelwise prefill and decode, the ragged prefill and
-    the backward sweep."""
+    stateless VJP, the channelwise prefill and decode, the ragged prefill, the
+    backward sweep, and linear attention with its norm."""
     fms, _, _ = bench_chunked(torch, gdr, args.steps, args.warmup, fused_gates=True)
     sms, _, skern = bench_chunked(torch, gdr, args.steps, args.warmup, saved=False)
     return {
@@ -627,6 +676,7 @@ def variants(torch, gdr, args, tokens):
         "channelwise_decode": bench_channelwise_decode(torch, gdr),
         "ragged_prefill": bench_ragged(torch, gdr),
         "vjp_sweep": bench_vjp_sweep(torch, gdr),
+        "linear_attention": bench_linear_attention(torch, gdr),
     }
 
 

@@ -77,10 +77,13 @@ COPY_PATTERN = r"calib_copy_kernel"
 
 
 def src_digest():
-    """Digest of the kernel sources (same definition as bench.py's)."""
+    """Digest of the sources of the kernels that the profiles measure: those of
+    the gated delta rule, not of the operators beside it."""
     h = hashlib.sha256()
     csrc = os.path.join(_HERE, "csrc")
     for f in sorted(os.listdir(csrc)):
+        if f.startswith(("gdr_linear", "gdr_norm")):
+            continue
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(f.encode() + fh.read())
     return h.hexdigest()[:16]
