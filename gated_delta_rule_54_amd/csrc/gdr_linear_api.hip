@@ -42,9 +42,10 @@ gdr_status check(const gdr_linear_problem* p) {
                         check_row(p->v_row, v, p->io_dtype),
                         check_row(0, static_cast<int64_t>(p->Hv) * p->Dk, p->io_dtype)})
     if (st != GDR_OK) return st;
-  // grid limits: workgroups are numbered by (segment, b, v-head, slice) in 31 bits
+  // grid limits: a launch has at most 2^32 threads, up to 512 for each slice of
+  // the heads' states (segments only where there are few)
   if (p->B > 65535 || p->Hv > 65535 || p->T > 0x7fffffffLL) return GDR_ERR_UNSUPPORTED;
-  if (p->B * p->Hv > (1 << 22) || p->B * p->T > 0x7fffffffLL || p->B * p->T * p->Hk > 0x7fffffffLL)
+  if (p->B * p->Hv * (2 * gdr::lin_slices(p->Dk) + gdr::lin_slices(p->Dv)) > (1 << 22) || p->B * p->T > 0x7fffffffLL || p->B * p->T * p->Hk > 0x7fffffffLL)
     return GDR_ERR_UNSUPPORTED;
   return GDR_OK;
 }

@@ -102,6 +102,11 @@ def _here(dev, stream):
     return stream is None and dev.index == torch.cuda.current_device()
 
 
+# The current stream's handle, without the Stream object around it: a call for
+# one token is bound by the host.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _check_status(st, where):
     if st != GDR_OK:
         raise GdrError(st, where)
@@ -180,7 +185,7 @@ def gdr_linear_forward(q, k, v, g=None, h0=None, *, algo="auto", out_dtype=torch
         _want(ht, "ht", state, torch.float32, dev)
     ws = _workspace(gdr_linear_forward_workspace(prob), dev)
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(h0), _ptr(o), _ptr(ht), _ptr(ws),
-            0 if ws is None else ws.numel(), torch.cuda.current_stream(dev).cuda_stream)
+            0 if ws is None else ws.numel(), _raw_stream(dev.index))
     if cu_seqlens is not None:
         st = lib().gdr_linear_forward_varlen(ctypes.byref(prob), _ptr(cu_seqlens), *args)
     else:
@@ -211,7 +216,7 @@ def gdr_linear_backward(q, k, v, g, h0, dout, dht=None, *, algo="auto", out_dtyp
     ws = _workspace(gdr_linear_backward_workspace(prob), dev)
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(h0), _ptr(dout), _ptr(dht), _ptr(dq), _ptr(dk), _ptr(dv),
             _ptr(dg), _ptr(dh0), _ptr(ws), 0 if ws is None else ws.numel(),
-            torch.cuda.current_stream(dev).cuda_stream)
+            _raw_stream(dev.index))
     if cu_seqlens is not None:
         st = lib().gdr_linear_backward_varlen(ctypes.byref(prob), _ptr(cu_seqlens), *args)
     else:
@@ -262,7 +267,7 @@ def gdr_group_norm_forward(x, weight=None, bias=None, z=None, *, center=False, s
     else:
         _want(y, "y", tuple(x.shape), y.dtype, dev)
     st = lib().gdr_group_norm_forward(ctypes.byref(prob), _ptr(x), _ptr(weight), _ptr(bias), _ptr(z), _ptr(y),
-                                      torch.cuda.current_stream(dev).cuda_stream)
+                                      _raw_stream(dev.index))
     _check_status(st, "gdr_group_norm_forward")
     return y
 
@@ -292,6 +297,6 @@ def gdr_group_norm_backward(x, weight, bias, z, dy, *, center=False, silu=False,
     ws = _workspace(gdr_group_norm_backward_workspace(prob) if dw is not None or db is not None else 0, dev)
     st = lib().gdr_group_norm_backward(ctypes.byref(prob), _ptr(x), _ptr(weight), _ptr(bias), _ptr(z), _ptr(dy),
                                        _ptr(dx), _ptr(dz), _ptr(dw), _ptr(db), _ptr(ws),
-                                       0 if ws is None else ws.numel(), torch.cuda.current_stream(dev).cuda_stream)
+                                       0 if ws is None else ws.numel(), _raw_stream(dev.index))
     _check_status(st, "gdr_group_norm_backward")
     return dx, dz, dw, db
