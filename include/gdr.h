@@ -246,13 +246,17 @@ gdr_status gdr_backward_varlen(const gdr_problem* p, const int64_t* cu_seqlens,
  * g is [B, T, Hv], or [Hv] with GDR_LINEAR_HEAD_DECAY (one constant factor
  * per head; dg is then [Hv], summed over all tokens), or NULL (alpha = 1).
  * Any g, -Inf included (the state is dropped there), is allowed; growth past
- * the fp32 range gives Inf or NaN.
+ * the fp32 range gives Inf or NaN, and with GDR_ALGO_CHUNKED so does growth of
+ * more than that range over the tokens of one chunk (64).
  *
  * Dk and Dv are multiples of 16 up to 256, independent of each other; q_row,
  * k_row, v_row are the elements between one token's row and the next of q, k
  * and v (0: dense), so that the three may be column ranges of one projection:
  * at least H * D, in whole 16-byte units.  Rows of a batch follow each other
- * at the same distance.  All other tensors are dense, as above.
+ * at the same distance.  All other tensors are dense, as above.  A row, with
+ * its gap, holds at most 2^22 elements; B and Hv are at most 65535, and
+ * B * Hv * (2 ceil(Dk/64) + ceil(Dv/64)) at most 2^22 (else
+ * GDR_ERR_UNSUPPORTED).
  *
  * Results: sums, the state and everything returned in fp32 (an fp32 o, dq,
  * dk, dv, and ht, dg, dh0 always) carry fp32 accuracy also from bf16 inputs;
@@ -262,8 +266,10 @@ gdr_status gdr_backward_varlen(const gdr_problem* p, const int64_t* cu_seqlens,
  * GDR_ALGO_CHUNKED they may reach earlier tokens of their chunk of 64.
  *
  * GDR_ALGO_SEQUENTIAL runs token by token (decoding, with ht == h0 allowed);
- * GDR_ALGO_CHUNKED groups tokens for the matrix cores; GDR_ALGO_AUTO picks by
- * T.  Both take every supported problem. */
+ * its sums do not depend on how a sequence is cut into calls.
+ * GDR_ALGO_CHUNKED groups tokens for the matrix cores.  GDR_ALGO_AUTO picks by
+ * T, and has a kernel of its own for one token.  All take every supported
+ * problem. */
 enum { GDR_LINEAR_HEAD_DECAY = 1u };
 
 typedef struct gdr_linear_problem {

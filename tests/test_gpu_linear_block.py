@@ -212,3 +212,78 @@ def test_layer_captured_and_replayed():
         torch.cuda.synchronize()
         for a, b, c in zip(got, want, again):
             assert torch.equal(a, b) and torch.equal(c, b)
+
+
+@pytest.mark.parametrize("B,T,Hk,Hv,Dk,Dv", [(16, 70, 4, 8, 128, 128), (16, 130, 4, 16, 128, 64),
+                                             (32, 65, 4, 12, 64, 144), (8, 33, 4, 8, 256, 128)])
+@pytest.mark.parametrize("io,out", [(BF, BF), (BF, F), (F, F), (F, BF)])
+@pytest.mark.parametrize("want_dg", [True, False])
+def test_gradients_summed_over_heads(B, T, Hk, Hv, Dk, Dv, io, out, want_dg):
+    """Enough key heads to fill the card: dq and dk are summed over value heads
+    launch by launch.  The last sequence of the ragged form is empty, the one
+    before short; rows behind them stay out of it.  Three sequences are compared
+    with 64 bits, the others with the same sequences in a batch of their own."""
+    x = inputs(T, B, T, Hk, Hv, Dk, Dv, io)
+    t = {a: dev(v, io if a in ("q", "k", "v", "dy") else F) for a, v in x.items()}
+    kw = dict(algo="chunked", out_dtype=out, want_dg=want_dg)
+    gdr.gdr_profile_enable(True)
+    got = gdr.gdr_linear_backward(t["q"], t["k"], t["v"], t["g"], t["h0"], t["dy"], **kw)
+    names = gdr.gdr_profile_read()
+    gdr.gdr_profile_enable(False)
+    assert "linear_group_sum" not in names, "the case no longer reaches the path it is for"
+    n = max(Dk, Dv) + 4 * T + 64 + Hv // Hk
+    for i in (0, B // 2, B - 1):
+        args = tuple(x[a][i:i + 1] for a in ("q", "k", "v", "g", "h0", "dy"))
+        for name, a, b, A in zip(("dq", "dk", "dv", "dg", "dh0"), got, lo.backward(*args), lo.backward_abs(*args)):
+            if name == "dg" and not want_dg:
+                assert a is None
+                continue
+            o = F if name in ("dg", "dh0") else out
+            # a bf16 output may come from operands rounded to bf16, one a product
+            two = 2.0 ** -8 * A if o == BF else 0.0
+            err = np.abs(host(a[i:i + 1]) - b)
+            assert (err <= 2 * n * U * A + two + (2.0 ** -8 * (np.abs(b) + A * n * U) if o == BF else 0)).all(), name
+    lens = [T] * (B - 2) + [3, 0]
+    cu = torch.tensor(np.cumsum([0] + lens), device="cuda")
+    flat = {a: t[a].reshape(1, B * T, *t[a].shape[2:]) for a in ("q", "k", "v", "g", "dy")}
+    rag = gdr.gdr_linear_backward(flat["q"], flat["k"], flat["v"], flat["g"], t["h0"], flat["dy"], cu_seqlens=cu,
+                                  max_seqlen=T, **kw)
+    rows = (B - 2) * T
+    for name, a, b in zip(("dq", "dk", "dv", "dg"), rag, got):
+        if a is not None:
+            assert torch.equal(a[0, :rows], b.reshape(1, B * T, *b.shape[2:])[0, :rows]), name
+    short = gdr.gdr_linear_backward(*(flat[a][:, rows:rows + 3].contiguous() for a in ("q", "k", "v", "g")),
+                                    t["h0"][B - 2:B - 1], flat["dy"][:, rows:rows + 3].contiguous(), **kw)
+    for name, a, b in zip(("dq", "dk", "dv", "dg"), rag, short):
+        if a is not None:
+            # fp32 sums over heads in another order; a bf16 result may then round to the next value
+            tol = 2.0 ** -7 if a.dtype == BF else 2.0 ** -18
+            assert ((a[0, rows:rows + 3] - b[0]).abs() <= tol * (b[0].abs() + b.abs().max())).all(), name
+    assert torch.equal(rag[4][B - 1], torch.zeros_like(rag[4][0]))
+
+
+@pytest.mark.parametrize("B,T,Hk,Hv,D", [(1, 2100, 16, 32, 128), (2, 1500, 16, 32, 64)])
+@pytest.mark.parametrize("out", [BF, F])
+def test_gradients_summed_over_heads_of_cut_sequences(B, T, Hk, Hv, D, out):
+    """The same with the sequences cut in segments, against the token-by-token
+    kernels; their sums over absolute values bound both sides' roundings."""
+    x = inputs(T, B, T, Hk, Hv, D, D, BF)
+    names = ("q", "k", "v", "g", "h0", "dy")
+    io = lambda a: BF if a in ("q", "k", "v", "dy") else F
+    t = [dev(x[a], io(a)) for a in names]
+    gdr.gdr_profile_enable(True)
+    got = gdr.gdr_linear_backward(*t, algo="chunked", out_dtype=out)
+    ran = gdr.gdr_profile_read()
+    gdr.gdr_profile_enable(False)
+    assert "linear_group_sum" not in ran and "linear_segments" in ran
+    ref = gdr.gdr_linear_backward(*t, algo="sequential")
+    A = gdr.gdr_linear_backward(*(a if n == "g" else a.abs() for n, a in zip(names, t)), algo="sequential")
+    n = D + 4 * T + 64 + Hv // Hk
+    for name, a, b, c in zip(("dq", "dk", "dv", "dg", "dh0"), got, ref, A):
+        if name == "dg":  # |q dq| + |k dk| summed to the end bounds its terms
+            group = lambda s: s.repeat_interleave(Hv // Hk, 2) if s.shape[2] == Hk else s
+            c = sum((group(t[i].abs().float()) * group(A[i])).sum(-1) for i in (0, 1)).flip(1).cumsum(1).flip(1)
+        tol = 4 * n * U * c.double() + 1e-30
+        if out == BF and name in ("dq", "dk", "dv"):
+            tol = tol + 2.0 ** -8 * (b.abs() + c + tol)
+        assert ((a.double() - b.double()).abs() <= tol).all(), name
