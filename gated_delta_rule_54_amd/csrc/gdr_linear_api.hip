@@ -45,8 +45,8 @@ gdr_status check(const gdr_linear_problem* p) {
   // grid limits: a launch has at most 2^32 threads, up to 512 for each slice of
   // the heads' states (segments only where there are few)
   if (p->B > 65535 || p->Hv > 65535 || p->T > 0x7fffffffLL) return GDR_ERR_UNSUPPORTED;
-  if (p->B * p->Hv * (2 * gdr::lin_slices(p->Dk) + gdr::lin_slices(p->Dv)) > (1 << 22) || p->B * p->T > 0x7fffffffLL || p->B * p->T * p->Hk > 0x7fffffffLL)
-    return GDR_ERR_UNSUPPORTED;
+  const int slices = 2 * gdr::lin_slices(p->Dk) + gdr::lin_slices(p->Dv);
+  if (p->B * p->Hv * slices > (1 << 22) || p->B * p->T * p->Hk > 0x7fffffffLL) return GDR_ERR_UNSUPPORTED;
   return GDR_OK;
 }
 
@@ -86,7 +86,8 @@ size_t backward_bytes(const gdr_linear_problem* p) {
   const gdr::LinPlan plan = gdr::lin_plan(s, true);
   const bool chunk = chunked(p, true);
   gdr::LinBwdParts parts;
-  return gdr::lin_bwd_parts(s, chunk ? plan.segments : 1, chunk && plan.sum, nullptr, &parts) + (chunk ? plan.bytes : 0);
+  const size_t used = gdr::lin_bwd_parts(s, chunk ? plan.segments : 1, chunk && plan.sum, nullptr, &parts);
+  return used + (chunk ? plan.bytes : 0);
 }
 
 gdr_status check_ws(const void* ws, size_t have, size_t need) {

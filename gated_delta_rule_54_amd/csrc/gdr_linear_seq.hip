@@ -362,7 +362,8 @@ LinChains lin_forward_chains(const LinShape& s, const LinFwdArgs& a) {
   LinChains L{};
   const int G = s.Hv / s.Hk;
   L.n = 1, L.segments = 1, L.seg = s.T;
-  L.B = s.B, L.T = s.T, L.Hv = s.Hv, L.group = G, L.g = a.g, L.head_decay = s.head_decay, L.out_bf16 = s.out_bf16, L.cu = a.cu;
+  L.B = s.B, L.T = s.T, L.Hv = s.Hv, L.group = G, L.g = a.g, L.head_decay = s.head_decay;
+  L.out_bf16 = s.out_bf16, L.cu = a.cu;
   LinChain& c = L.c[0];
   c.x = a.q, c.xr = s.q_row, c.xg = G;
   c.y = a.k, c.yr = s.k_row, c.yg = G;
@@ -396,7 +397,8 @@ LinChains lin_backward_chains(const LinShape& s, const LinBwdArgs& a, const LinB
   const int G = s.Hv / s.Hk;
   const int64_t d_row = static_cast<int64_t>(s.Hv) * s.Dv;
   L.n = 3, L.segments = 1, L.seg = s.T;
-  L.B = s.B, L.T = s.T, L.Hv = s.Hv, L.group = G, L.g = a.g, L.head_decay = s.head_decay, L.out_bf16 = s.out_bf16, L.cu = a.cu;
+  L.B = s.B, L.T = s.T, L.Hv = s.Hv, L.group = G, L.g = a.g, L.head_decay = s.head_decay;
+  L.out_bf16 = s.out_bf16, L.cu = a.cu;
   LinChain& q = L.c[0];  // dq
   q.x = a.dout, q.xr = d_row, q.xg = 1;
   q.y = a.v, q.yr = s.v_row, q.yg = 1;

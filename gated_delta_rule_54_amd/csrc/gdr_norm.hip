@@ -13,7 +13,7 @@
 // keeps one group index for all the rows it walks, so weights are read once
 // and the weights' gradients are summed in its registers.  Bound: memory; 16384
 // rows of 32 x 128, bf16, with a gate: forward 80 us (5.04 TB/s), VJP 136 (4.92
-// TB/s), of which norm_params 9; a copy of 512 MiB reaches 6.2 TB/s.
+// TB/s); back to back 71 and 128; a copy of 512 MiB reaches 6.2 TB/s.
 
 #include <algorithm>
 
@@ -34,7 +34,10 @@ template <typename T> __device__ __forceinline__ void ld8(const T* p, float (&x)
   if constexpr (sizeof(T) == 2) {
     const u32x4n w = __builtin_nontemporal_load(reinterpret_cast<const u32x4n*>(p));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
   } else {
     ld4<T>(p, a);
     ld4<T>(p + 4, b);
@@ -210,19 +213,36 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormArgs a, int phases) {
 }
 
 // dw, db: column sums of the n partial rows, in a fixed order: 64 row lanes
-// per 16 columns, each over every 64th row, then the 64 in turn (64 bits).
-__global__ __launch_bounds__(1024) void norm_params_kernel(const float* part, float* dw, float* db, int64_t n, int C) {
+// per 16 columns, each over every 64th row, then the 64 eight at a time (64
+// bits).  Bound: latency; eight rows are in flight at a time.
+__global__ __launch_bounds__(1024) void norm_params_kernel(const float* part, float* dw, float* db, int64_t n,
+                                                           int C) {
   __shared__ double sum[64][17];
   const int col = threadIdx.x & 15, lane = threadIdx.x >> 4, c = blockIdx.x * 16 + col;
   float* out = blockIdx.y ? db : dw;
   if (!out) return;
   double s = 0.0;
   if (c < C)
-    for (int64_t i = lane; i < n; i += 64) s += part[(i * 2 + blockIdx.y) * C + c];
+    for (int64_t i = lane; i < n; i += 512) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = i + 64 * u < n ? part[((i + 64 * u) * 2 + blockIdx.y) * C + c] : 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += v[u];
+    }
   sum[lane][col] = s;
   __syncthreads();
+  if (lane < 8) {
+    s = 0.0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += sum[8 * lane + k][col];
+  }
+  __syncthreads();
+  if (lane < 8) sum[lane][col] = s;
+  __syncthreads();
   if (lane == 0 && c < C) {
-    for (int k = 1; k < 64; ++k) s += sum[k][col];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) s += sum[k][col];
     out[c] = static_cast<float>(s);
   }
 }
