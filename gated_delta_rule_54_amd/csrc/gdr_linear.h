@@ -60,7 +60,8 @@ struct LinChain {
   float* s_out;         // null: not wanted
   int s1, s2;
   void* out;            // null: only the state is wanted
-  float* sum;           // chunked, summed over heads: fp32 [B][T][Hk][D2]
+  float* sum;           // chunked, over heads: what is added, fp32 [B][T][Hv / og][D2]
+  int og = 1;           // chunked: value heads to a head of out
   int out_partial;      // 0: out type, rows of the batch; 1: fp32, [B][T] rows (a ragged batch has T rows per sequence)
   const void* ex;       // e_t = ex_t . out_t, ex [.., Hv / eg heads, D2], rows er elements apart; null: not wanted
   int64_t er;

@@ -304,17 +304,15 @@ struct Walk {
   int64_t t0, len;           // the segment's first token in its sequence, its length
   int h, col0, sl;
   bool first, last;          // of the sequence's segments, in the chain's direction
-  bool more_heads, add;      // of a sum over heads: one follows; some went before
 };
 
 // What a walk computes.  NS: operands that P and H enter the output's products
-// as; EX: the terms e too; WIDE: the output is stored in fp32; SUM: the output
-// is summed over the value heads of a key head, one launch for each, in fp32
-// rows of the workspace until the last.
-template <int NS_, bool EX_, bool WIDE_, bool SUM_ = false>
+// as; EX: the terms e too; WIDE: the output is stored in fp32; ADD: what earlier
+// launches left of it, over other value heads, is added.
+template <int NS_, bool EX_, bool WIDE_, bool ADD_ = false>
 struct Job {
   static constexpr int NS = NS_;
-  static constexpr bool EX = EX_, WIDE = WIDE_, SUM = SUM_;
+  static constexpr bool EX = EX_, WIDE = WIDE_, ADD = ADD_;
 };
 
 template <typename OP, int D1P>
@@ -368,8 +366,8 @@ struct Gates {
   }
 };
 
-// Where an output wave stores: 4 columns of a row at a time.  Offsets are those
-// of the output's type; the sum's rows are fp32.
+// Where an output wave stores, 4 columns of a row at a time, and with ADD the
+// fp32 rows that it adds.
 template <typename J>
 struct Out {
   static constexpr uint32_t SIZE = J::WIDE ? 4 : 2;
@@ -378,27 +376,20 @@ struct Out {
     const LinChain& c = w.c;
     const bool rev = c.rev != 0;
     const int64_t first = rev ? w.len - 1 : 0, bt = w.b * a.T + w.t0 + first;
-    const int heads = J::SUM ? a.Hv / a.group : a.Hv, h = J::SUM ? w.h / a.group : w.h;
+    const int heads = a.Hv / c.og, h = w.h / c.og;
     const int64_t row = c.out_partial ? bt : w.row0 + first;
     const uint32_t wide = static_cast<uint32_t>(heads) * c.D2;
     o = Rows{static_cast<char*>(c.out) + ((row * heads + h) * c.D2 + w.col0) * SIZE, wide * SIZE, w2 * SIZE, rev};
-    if constexpr (J::SUM)
+    if constexpr (J::ADD)
       p = Rows{reinterpret_cast<char*>(c.sum) + ((bt * heads + h) * c.D2 + w.col0) * 4, wide * 4,
                static_cast<uint32_t>(w2) * 4, rev};
   }
-  // The sum so far at row i, column col (kNone: outside).
-  __device__ __forceinline__ f32x4 before(const Walk& w, int n, int C, int i, int col, bool on) const {
-    if (!w.add) return f32x4{0.f, 0.f, 0.f, 0.f};
+  // The sum so far at row i, column col (on: inside).
+  __device__ __forceinline__ f32x4 before(int n, int C, int i, int col, bool on) const {
     const uint32_t at = p.row(i, C) + col * 4 - p.shift(n, C);
     return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(p.chunk(n), on ? at : kNone, 0, 0));
   }
-  __device__ __forceinline__ void put(const Walk& w, int n, int C, int i, int col, bool on, f32x4 v) const {
-    if constexpr (J::SUM)
-      if (w.more_heads) {
-        const uint32_t at = p.row(i, C) + col * 4 - p.shift(n, C);
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), p.chunk(n), on ? at : kNone, 0, 0);
-        return;
-      }
+  __device__ __forceinline__ void put(int n, int C, int i, int col, bool on, f32x4 v) const {
     const uint32_t at = on ? o.row(i, C) + col * SIZE - o.shift(n, C) : kNone;
     if constexpr (J::WIDE) {
       __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), o.chunk(n), at, 0, 0);
@@ -410,7 +401,7 @@ struct Out {
   }
   __device__ __forceinline__ void next(int C) {
     o.next(C);
-    if constexpr (J::SUM) p.next(C);
+    if constexpr (J::ADD) p.next(C);
   }
 };
 
@@ -652,9 +643,9 @@ __device__ __forceinline__ void out_by_rows(const LinChains& a, const Walk& w, F
     }
 
     f32x4 pv[NI];
-    if constexpr (J::SUM)
+    if constexpr (J::ADD)
 #pragma unroll
-      for (int t = 0; t < NI; ++t) pv[t] = out.before(w, n, C, i, 16 * (ct0 + t) + g4, 16 * (ct0 + t) < w2);
+      for (int t = 0; t < NI; ++t) pv[t] = out.before(n, C, i, 16 * (ct0 + t) + g4, 16 * (ct0 + t) < w2);
 
     // X H of the wave's rows, transposed; fragments are read a step ahead of
     // the products that take them
@@ -737,8 +728,8 @@ __device__ __forceinline__ void out_by_rows(const LinChains& a, const Walk& w, F
       const f32x4 v = O[t];
       const int col = 16 * (ct0 + t);
       if constexpr (EX) e += (ex[t][0] * v[0] + ex[t][1] * v[1]) + (ex[t][2] * v[2] + ex[t][3] * v[3]);
-      if constexpr (J::SUM) out.put(w, n, C, i, col + g4, col < w2, v + pv[t]);
-      else out.put(w, n, C, i, col + g4, col < w2, v);
+      if constexpr (J::ADD) out.put(n, C, i, col + g4, col < w2, v + pv[t]);
+      else out.put(n, C, i, col + g4, col < w2, v);
     }
     out.next(C);
     if constexpr (EX) {
@@ -852,9 +843,9 @@ __device__ __forceinline__ void out_by_columns(const LinChains& a, const Walk& w
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) zf[ks] = OP::col(x.Z, T::LDZ, 32 * ks, wc, 4);
     f32x4 pv[NI];
-    if constexpr (J::SUM)
+    if constexpr (J::ADD)
 #pragma unroll
-      for (int k = 0; k < NI; ++k) pv[k] = out.before(w, n, C, 16 * blk[k] + m, wc + g4, has);
+      for (int k = 0; k < NI; ++k) pv[k] = out.before(n, C, 16 * blk[k] + m, wc + g4, has);
     float ex[NI][4];
     if constexpr (EX) {
       const rsrc_t be = re.chunk(n);
@@ -891,8 +882,8 @@ __device__ __forceinline__ void out_by_columns(const LinChains& a, const Walk& w
 #pragma unroll
     for (int k = 0; k < NI; ++k) {
       const f32x4 v = O[k];
-      if constexpr (J::SUM) out.put(w, n, C, 16 * blk[k] + m, wc + g4, has, v + pv[k]);
-      else out.put(w, n, C, 16 * blk[k] + m, wc + g4, has, v);
+      if constexpr (J::ADD) out.put(n, C, 16 * blk[k] + m, wc + g4, has, v + pv[k]);
+      else out.put(n, C, 16 * blk[k] + m, wc + g4, has, v);
       if constexpr (EX) {
         const float e = rows4_sum((ex[k][0] * v[0] + ex[k][1] * v[1]) + (ex[k][2] * v[2] + ex[k][3] * v[3]));
         if (lane < 16) s.e[wave][16 * blk[k] + m] = e;
@@ -969,8 +960,6 @@ __device__ __forceinline__ bool find(const LinChains& a, const Units& u, int64_t
   const bool begin = w.seg == 0, last = w.t0 + w.len >= sp.len;
   w.first = w.c.rev ? last : begin;
   w.last = w.c.rev ? begin : last;
-  w.add = a.head > 0;
-  w.more_heads = a.head + 1 < a.group;
   return true;
 }
 
@@ -1153,12 +1142,14 @@ hipError_t run_segments(const LinChains& a, float* factor, hipStream_t st) {
 }
 
 // The kernel of a VJP: whether e is wanted, dv is returned in fp32, dq and dk
-// are summed over heads launch by launch, or stored per value head in fp32.
+// are stored in fp32 in any case (`part`), and added to what is there (`add`).
 template <typename OP, int D1P, bool WIDE>
-hipError_t run_vjp(const LinChains& a, bool ex, bool sum, bool part, hipStream_t st) {
+hipError_t run_vjp(const LinChains& a, bool ex, bool add, bool part, hipStream_t st) {
   constexpr int N = OP::FULL, M = WIDE ? N : 1;  // operands with e, without
   using JB = Job<M, false, WIDE>;
-  if (sum) return ex ? run_chunks<OP, D1P, Job<N, true, WIDE, true>, JB>(a, st)
+  if (add && (part || WIDE)) return ex ? run_chunks<OP, D1P, Job<N, true, true, true>, JB>(a, st)
+                                       : run_chunks<OP, D1P, Job<M, false, true, true>, JB>(a, st);
+  if (add) return ex ? run_chunks<OP, D1P, Job<N, true, WIDE, true>, JB>(a, st)
                      : run_chunks<OP, D1P, Job<M, false, WIDE, true>, JB>(a, st);
   if (part || WIDE) return ex ? run_chunks<OP, D1P, Job<N, true, true>, JB>(a, st)
                               : run_chunks<OP, D1P, Job<M, false, true>, JB>(a, st);
@@ -1305,24 +1296,31 @@ hipError_t launch_lin_chunk_bwd(const LinShape& s, const LinPlan& p, const LinBw
     a.c[1].seg_in = a.c[2].seg_in = g.rev;
   }
   a.c[0].key = a.c[1].key = 1;
-  if (p.sum) {
-    a.c[0].out = args.dq, a.c[1].out = args.dk;
-    a.c[0].out_partial = a.c[1].out_partial = 0;
-    a.c[0].sum = parts.pdq, a.c[1].sum = parts.pdk;
-  }
   {
     ProfScope prof("linear_chunks_vjp", st);
-    // summed over heads, dv joins the last of a key head's launches
+    // summed over heads: one launch for each of a key head's value heads, in
+    // fp32 rows of the workspace until the last, which dv joins
     a.sum = p.sum;
     const int group = a.group;
+    if (p.sum)
+      for (int i = 0; i < 2; ++i) {
+        a.c[i].out = a.c[i].sum = i ? parts.pdk : parts.pdq;
+        a.c[i].og = group;
+        a.c[i].out_partial = 1;
+      }
     for (a.head = p.sum ? 0 : group - 1; a.head < group; ++a.head) {
-      a.n = a.head + 1 < group ? 2 : 3;
+      const bool last = a.head + 1 == group;
+      a.n = last ? 3 : 2;
+      if (p.sum && last) {
+        a.c[0].out = args.dq, a.c[1].out = args.dk;
+        a.c[0].out_partial = a.c[1].out_partial = 0;
+      }
+      const bool ex = args.dg != nullptr, add = p.sum && a.head > 0, part = s.Hv != s.Hk && !(p.sum && last);
       const hipError_t e = by_type(s.io_bf16, std::max(s.Dk, s.Dv), [&](auto op, auto d1) {
         using OP = decltype(op);
         constexpr int D1P = decltype(d1)::value;
-        const bool ex = args.dg != nullptr, part = s.Hv != s.Hk && !p.sum;
-        return s.out_bf16 ? run_vjp<OP, D1P, false>(a, ex, p.sum, part, st)
-                          : run_vjp<OP, D1P, true>(a, ex, p.sum, part, st);
+        return s.out_bf16 ? run_vjp<OP, D1P, false>(a, ex, add, part, st)
+                          : run_vjp<OP, D1P, true>(a, ex, add, part, st);
       });
       if (e != hipSuccess) return e;
     }
