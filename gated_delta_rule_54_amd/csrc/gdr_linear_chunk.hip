@@ -25,7 +25,7 @@
 // cycles), and LDS delivers their operands: 2.8 us a chunk of 64 tokens and 64
 // columns forward, 3.5 in the VJP.  4 x 4096 tokens, 16 key and 32 value heads
 // of 128, bf16: forward 144-183 us (2.3-2.9 TB/s; its bytes alone 67 us), VJP
-// 700-810 us (bytes 110 us), of which dg 19 us.  Measured and set aside: 32
+// 664-760 us (bytes 110 us), of which dg 19 us.  Measured and set aside: 32
 // columns a wave (spills), chunks of 32 with two workgroups a compute unit, the
 // state's update after the output in the same waves (262 us forward against
 // 186), output by columns also where H is one operand (195 against 180).
@@ -1183,7 +1183,7 @@ hipError_t by_type(bool io_bf16, int d1, F&& f) {
 //   the scan 4 us, 0.3 us a segment and its states both ways at 4 TB/s;
 //   the sum over heads 5 us and 5.5 TB/s, a further launch 3 us.
 // What the rule chose, against the other side: VJP of 4 x 4096 tokens, 16 key
-// and 32 value heads, summed by launches 754-812 us, with the sum's pass 843;
+// and 32 value heads, summed by launches 664-760 us, with the sum's pass 843;
 // of 1 x 4096 tokens, summed and in 4 segments 257-268, whole with the pass 274;
 // of 16384 tokens of 8 heads 234 in 16 segments, 334 in 11; forward of 333
 // tokens, fp32, 24 in segments of 64, 34 of 192; of 4 x 4096 tokens 182 whole,
