@@ -103,7 +103,7 @@ __device__ __forceinline__ double log2_decay(float g) {
 template <int CC>
 struct OpB {
   using E = uint16_t;
-  static constexpr int C = CC, PAD = 8, PER = 8, FULL = 3;
+  static constexpr int C = CC, PAD = 8, PER = 8, FULL = 3, NARROW = 2;
   typedef bf16x8 F;
   static __device__ __forceinline__ F run(const E* p) { return *reinterpret_cast<const F*>(p); }
   // Rows k0 + 8g .. +7 of column n0 + step (p / 4) + p % 4, p = lane % 16, of
@@ -172,7 +172,7 @@ struct OpB {
 
 struct OpF {
   using E = float;
-  static constexpr int C = 32, PAD = 4, PER = 4, FULL = 1;
+  static constexpr int C = 32, PAD = 4, PER = 4, FULL = 1, NARROW = 1;
   struct F { float v[8]; };
   static __device__ __forceinline__ F run(const E* p) {
     F f;
@@ -463,7 +463,7 @@ struct Room {
   struct State {
     typename OP::F f[4][T::KB][NS][64];  // [16 columns][32 rows][operand][lane]
   };
-  static constexpr bool COLS = NS > 1;
+  static constexpr bool COLS = NS > 2;
   struct Rest {
     Decay<T::C> d[COLS ? 1 : 2];
     alignas(16) E P[COLS ? NS * T::C * T::C : 8];
@@ -1145,7 +1145,7 @@ hipError_t run_segments(const LinChains& a, float* factor, hipStream_t st) {
 // are stored in fp32 in any case (`part`), and added to what is there (`add`).
 template <typename OP, int D1P, bool WIDE>
 hipError_t run_vjp(const LinChains& a, bool ex, bool add, bool part, hipStream_t st) {
-  constexpr int N = OP::FULL, M = WIDE ? N : 1;  // operands with e, without
+  constexpr int N = OP::FULL, M = WIDE ? N : OP::NARROW;  // operands with e, without
   using JB = Job<M, false, WIDE>;
   if (add && (part || WIDE)) return ex ? run_chunks<OP, D1P, Job<N, true, true, true>, JB>(a, st)
                                        : run_chunks<OP, D1P, Job<M, false, true, true>, JB>(a, st);
@@ -1274,7 +1274,7 @@ hipError_t launch_lin_chunk_fwd(const LinShape& s, const LinPlan& p, const LinFw
   return by_type(s.io_bf16, s.Dk, [&](auto op, auto d1) {
     using OP = decltype(op);
     constexpr int D1P = decltype(d1)::value;
-    return s.out_bf16 ? run_chunks<OP, D1P, Job<1, false, false>>(a, st)
+    return s.out_bf16 ? run_chunks<OP, D1P, Job<OP::NARROW, false, false>>(a, st)
                       : run_chunks<OP, D1P, Job<OP::FULL, false, true>>(a, st);
   });
 }
