@@ -18,24 +18,28 @@
 // 32 (t / 2) + 8 g + 4 (t % 2) + e (lane group g, element e), which is the
 // order of X's operands.  O is formed transposed, a lane storing 4 consecutive
 // columns of one token.  Output waves share the work by rows (out_by_rows)
-// where H is one operand, by columns (out_by_columns) where it is three.
+// where H is one or two operands, by columns (out_by_columns) where it is three.
 //
 // Bound: issue.  Two waves of a SIMD take turns at the matrix cores and the
 // vector ALUs (a 16 x 16 x 32 product holds the issue of its SIMD for 16-18
 // cycles), and LDS delivers their operands: 2.8 us a chunk of 64 tokens and 64
 // columns forward, 3.5 in the VJP.  4 x 4096 tokens, 16 key and 32 value heads
-// of 128, bf16: forward 144-183 us (2.3-2.9 TB/s; its bytes alone 67 us), VJP
-// 664-760 us (bytes 110 us), of which dg 19 us.  Measured and set aside: 32
+// of 128, bf16: forward 174 us (2.4 TB/s; its bytes alone 67 us), VJP
+// 683-686 us (bytes 110 us), of which dg 19 us.  Measured and set aside: 32
 // columns a wave (spills), chunks of 32 with two workgroups a compute unit, the
 // state's update after the output in the same waves (262 us forward against
-// 186), output by columns also where H is one operand (195 against 180).
+// 186), output by columns also where H is two operands (175 against 174 us; 17
+// ragged sequences 224 against 221).
 //
 // Precision.  bf16 inputs are matrix-core operands as they are.  What is
 // computed on the way (P, H, the decayed Z) is fp32: where a result is
 // returned in fp32, or a sum over all tokens is (the state; the terms of the
 // decay's gradient), it enters the product as a sum of three bf16 values (24
-// bits); otherwise, for an output that is rounded to bf16 itself, as one.
-// fp32 inputs use fp32 operands.
+// bits); otherwise, for an output that is rounded to bf16 itself, as two (16
+// bits: the error before the output's rounding is 2^-8 of that rounding's).  One
+// (8 bits) is as coarse as the output: the 2-norm error is then 2.1e-3 where the
+// rounding alone gives 1.7e-3, and the forward above takes 150 us instead of 174,
+// the VJP 655 instead of 683.  fp32 inputs use fp32 operands.
 
 #include <algorithm>
 #include <cmath>
@@ -99,7 +103,8 @@ __device__ __forceinline__ double log2_decay(float g) {
 
 // Matrix-core operands: lane group g holds steps 8g .. 8g + 7 of a 32-step
 // block of the summed index.  C chunk rows; PAD elements between LDS rows; PER
-// elements of a 16-byte unit; FULL operands hold an fp32 value.
+// elements of a 16-byte unit; FULL operands hold an fp32 value, NARROW one that
+// is enough for a result in bf16.
 template <int CC>
 struct OpB {
   using E = uint16_t;

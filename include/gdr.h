@@ -260,8 +260,9 @@ gdr_status gdr_backward_varlen(const gdr_problem* p, const int64_t* cu_seqlens,
  *
  * Results: sums, the state and everything returned in fp32 (an fp32 o, dq,
  * dk, dv, and ht, dg, dh0 always) carry fp32 accuracy also from bf16 inputs;
- * bf16 outputs are rounded once from sums whose matrix-core operands hold 8
- * bits or more.  Every row past a sequence's end, and rows that no sequence
+ * bf16 outputs are rounded once from sums whose matrix-core operands hold 16
+ * bits or more (24 in dq and dk where dg is wanted: asking for it can move one
+ * of their values to the next bf16).  Every row past a sequence's end, and rows that no sequence
  * covers, are neither read nor written.  Inf and NaN inputs propagate; with
  * GDR_ALGO_CHUNKED they may reach earlier tokens of their chunk of 64.
  *
