@@ -3,7 +3,8 @@ a decay for each head, and the group norm of the heads' outputs
 (include/gdr.h).  Argument marshalling only, as in ``binding``.
 
 q, k, v, x and z may be column ranges of a wider row (a fused projection's
-output): the last axes dense, the rows any 16-byte-aligned distance apart.
+output): the last axes dense, the rows any 16-byte-aligned distance apart that
+keeps them disjoint (an expanded tensor is refused).
 Every other tensor is contiguous.  Outputs and workspaces are allocated on the
 stream the call runs on: the current stream of the tensors' device, or
 ``stream``.
@@ -52,7 +53,8 @@ def _ptr(t):
 def _row_stride(t, name):
     """Elements between the rows of t [..., rows, H, D] whose last two axes
     are dense and whose rows are equally spaced over all leading axes; 0 where
-    they follow each other without a gap."""
+    they follow each other without a gap.  Rows that share storage (an expanded
+    tensor's lie 0 elements apart) are refused: 0 says that they are dense."""
     if t.is_contiguous() or t.numel() == 0:
         return 0
     shape, stride = t.shape, t.stride()
@@ -66,8 +68,9 @@ def _row_stride(t, name):
             row = st
         ok = ok and st == n * row
         n *= s
-    if not ok:
-        raise ValueError(f"{name} must have dense last axes and equally spaced rows, got strides {stride}")
+    if not ok or (row is not None and row < H * D):
+        raise ValueError(f"{name} must have dense last axes and equally spaced rows that do not overlap, "
+                         f"got strides {stride}")
     return 0 if row is None or row == H * D else row
 
 
