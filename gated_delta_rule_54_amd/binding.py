@@ -26,6 +26,7 @@ SYMBOLS = ("gdr_keeps_chunks", "gdr_forward_workspace", "gdr_backward_workspace"
            "gdr_backward", "gdr_forward_noalloc", "gdr_forward_varlen", "gdr_backward_varlen",
            "gdr_linear_forward_workspace", "gdr_linear_backward_workspace", "gdr_linear_forward",
            "gdr_linear_backward", "gdr_linear_forward_varlen", "gdr_linear_backward_varlen",
+           "gdr_linear_backward_varlen_workspace", "gdr_linear_backward_varlen_rows",
            "gdr_group_norm_forward", "gdr_group_norm_backward_workspace", "gdr_group_norm_backward",
            "gdr_profile_enable", "gdr_profile_read",
            "gdr_status_str", "gdr_last_hip_error", "gdr_abi_version")
@@ -88,10 +89,13 @@ def lib():
         L.gdr_linear_forward_varlen.argtypes = [vp] * 10 + [sz, vp]
         L.gdr_linear_backward.argtypes = [vp] * 14 + [sz, vp]
         L.gdr_linear_backward_varlen.argtypes = [vp] * 15 + [sz, vp]
+        L.gdr_linear_backward_varlen_workspace.argtypes = [vp, ctypes.c_int64, ctypes.POINTER(sz)]
+        L.gdr_linear_backward_varlen_rows.argtypes = [vp, ctypes.c_int64] + [vp] * 14 + [sz, vp]
         L.gdr_group_norm_forward.argtypes = [vp] * 7
         L.gdr_group_norm_backward.argtypes = [vp] * 11 + [sz, vp]
         for name in ("gdr_linear_forward_workspace", "gdr_linear_backward_workspace", "gdr_linear_forward",
                      "gdr_linear_backward", "gdr_linear_forward_varlen", "gdr_linear_backward_varlen",
+                     "gdr_linear_backward_varlen_workspace", "gdr_linear_backward_varlen_rows",
                      "gdr_group_norm_forward", "gdr_group_norm_backward_workspace", "gdr_group_norm_backward",
                      "gdr_keeps_chunks", "gdr_calib_copy", "gdr_calib_mfma",
                      "gdr_forward_workspace", "gdr_backward_workspace",

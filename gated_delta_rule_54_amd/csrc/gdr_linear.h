@@ -28,6 +28,11 @@ struct LinShape {
   int Hk, Hv, Dk, Dv;
   bool io_bf16, out_bf16, head_decay;
   int64_t q_row, k_row, v_row;  // elements between tokens
+  // Rows of the VJP's partial results, one for each token: row cu[b] + t for
+  // token t of sequence b (`packed`: a dense batch, or a ragged one whose rows
+  // are counted), or row b T + t.
+  int64_t rows;
+  bool packed;
 };
 
 struct LinFwdArgs {
@@ -60,13 +65,13 @@ struct LinChain {
   float* s_out;         // null: not wanted
   int s1, s2;
   void* out;            // null: only the state is wanted
-  float* sum;           // chunked, over heads: what is added, fp32 [B][T][Hv / og][D2]
+  float* sum;           // chunked, over heads: what is added, fp32 [rows][Hv / og][D2]
   int og = 1;           // chunked: value heads to a head of out
-  int out_partial;      // 0: out type, rows of the batch; 1: fp32, [B][T] rows (a ragged batch has T rows per sequence)
+  int out_partial;      // 0: out type, rows of the batch; 1: fp32, partial rows (LinShape)
   const void* ex;       // e_t = ex_t . out_t, ex [.., Hv / eg heads, D2], rows er elements apart; null: not wanted
   int64_t er;
   int eg;
-  float* e;             // in parts, [slices][B][Hv][T] (sequential) or [slices][1 or 2][..] (chunked)
+  float* e;             // in parts, [slices][Hv][rows] (sequential) or [slices][1 or 2][..] (chunked)
   const float* dot;     // gradient of the last state (element (d1, d2) as for s_in) or null
   float* xdot;          // <last state, dot> in parts, [segments][B][Hv][slices] (sequential) or [..][slices][4]
                         // (chunked); null: not wanted
@@ -81,6 +86,8 @@ struct LinChains {
   LinChain c[3];
   int n;                // chains in the launch
   int64_t B, T;
+  int64_t rows;         // partial rows (LinShape)
+  int packed;
   int Hv, group;        // value heads; those that share a key head
   const float* g;       // null: no decay
   int head_decay;       // g is [Hv]
@@ -115,15 +122,19 @@ __device__ __forceinline__ LinSpan lin_span(const int64_t* cu, int64_t b, int64_
   const int64_t s0 = cu[b], n = cu[b + 1] - s0;
   return LinSpan{s0, n < 0 ? 0 : (n > T ? T : n)};
 }
+// The partial row of token t of sequence b.
+__device__ __forceinline__ int64_t lin_part_row(const LinChains& a, int64_t b, const LinSpan& sp, int64_t t) {
+  return (a.packed ? sp.t0 : b * a.T) + t;
+}
 #endif
 
 LinChains lin_forward_chains(const LinShape& s, const LinFwdArgs& a);
 
 // Carved parts of a backward workspace, common to both algorithms.
 struct LinBwdParts {
-  float *eq, *ek;    // [slices(Dk)][up to 2][B][Hv][T]
+  float *eq, *ek;    // [slices(Dk)][up to 2][Hv][rows]
   float* xdot;       // [segments][B][Hv][slices(Dk)][4]
-  float *pdq, *pdk;  // only where value heads share a key head: [B][T][Hv][Dk], or sums [B][T][Hk][Dk]
+  float *pdq, *pdk;  // only where value heads share a key head: [rows][Hv][Dk], or sums [rows][Hk][Dk]
   double* dgsum;     // [B][segments][Hv], only with a decay per head
 };
 size_t lin_bwd_parts(const LinShape& s, int64_t segments, bool summed, char* base, LinBwdParts* p);  // their bytes

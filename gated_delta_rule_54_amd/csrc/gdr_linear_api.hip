@@ -29,7 +29,13 @@ gdr_status check_row(int64_t stride, int64_t dense, int32_t dtype) {
   return stride % (dtype == GDR_BF16 ? 8 : 4) ? GDR_ERR_BAD_ALIGNMENT : GDR_OK;
 }
 
-gdr_status check(const gdr_linear_problem* p) {
+// Rows of a VJP's partial results: a ragged batch's own, where the caller
+// counts them (kUncounted: it does not) and they are no more than the bound B * T.
+constexpr int64_t kUncounted = -1;
+bool counted(const gdr_linear_problem* p, int64_t rows) { return rows != kUncounted && rows <= p->B * p->T; }
+int64_t partial_rows(const gdr_linear_problem* p, int64_t rows) { return counted(p, rows) ? rows : p->B * p->T; }
+
+gdr_status check(const gdr_linear_problem* p, int64_t rows = kUncounted) {
   if (!p) return GDR_ERR_NULL_ARG;
   if (p->B < 0 || p->T < 0 || p->Hk <= 0 || p->Hv <= 0 || p->Dk <= 0 || p->Dv <= 0) return GDR_ERR_BAD_SHAPE;
   if (p->Hv % p->Hk != 0) return GDR_ERR_BAD_SHAPE;
@@ -46,11 +52,11 @@ gdr_status check(const gdr_linear_problem* p) {
   // the heads' states (segments only where there are few)
   if (p->B > 65535 || p->Hv > 65535 || p->T > 0x7fffffffLL) return GDR_ERR_UNSUPPORTED;
   const int slices = 2 * gdr::lin_slices(p->Dk) + gdr::lin_slices(p->Dv);
-  if (p->B * p->Hv * slices > (1 << 22) || p->B * p->T * p->Hk > 0x7fffffffLL) return GDR_ERR_UNSUPPORTED;
+  if (p->B * p->Hv * slices > (1 << 22) || partial_rows(p, rows) * p->Hk > 0x7fffffffLL) return GDR_ERR_UNSUPPORTED;
   return GDR_OK;
 }
 
-LinShape shape_of(const gdr_linear_problem* p) {
+LinShape shape_of(const gdr_linear_problem* p, bool ragged = false, int64_t rows = kUncounted) {
   LinShape s;
   s.B = p->B, s.T = p->T, s.Hk = p->Hk, s.Hv = p->Hv, s.Dk = p->Dk, s.Dv = p->Dv;
   s.io_bf16 = p->io_dtype == GDR_BF16;
@@ -59,6 +65,8 @@ LinShape shape_of(const gdr_linear_problem* p) {
   s.q_row = p->q_row ? p->q_row : static_cast<int64_t>(p->Hk) * p->Dk;
   s.k_row = p->k_row ? p->k_row : static_cast<int64_t>(p->Hk) * p->Dk;
   s.v_row = p->v_row ? p->v_row : static_cast<int64_t>(p->Hv) * p->Dv;
+  s.rows = partial_rows(p, rows);
+  s.packed = !ragged || counted(p, rows);
   return s;
 }
 
@@ -81,8 +89,8 @@ bool chunked(const gdr_linear_problem* p, bool backward) {
 size_t forward_bytes(const gdr_linear_problem* p) {
   return chunked(p, false) ? gdr::lin_plan(shape_of(p), false).bytes : 0;
 }
-size_t backward_bytes(const gdr_linear_problem* p) {
-  const LinShape s = shape_of(p);
+size_t backward_bytes(const gdr_linear_problem* p, int64_t rows) {
+  const LinShape s = shape_of(p, rows != kUncounted, rows);
   const gdr::LinPlan plan = gdr::lin_plan(s, true);
   const bool chunk = chunked(p, true);
   gdr::LinBwdParts parts;
@@ -122,14 +130,16 @@ gdr_status linear_forward(const gdr_linear_problem* p, const int64_t* cu, bool r
   return done(token ? gdr::launch_lin_token(s, chains, stream) : gdr::launch_lin_seq(s, chains, stream));
 }
 
-gdr_status linear_backward(const gdr_linear_problem* p, const int64_t* cu, bool ragged, const void* q, const void* k,
-                           const void* v, const float* g, const float* h0, const void* dout, const float* dht,
-                           void* dq, void* dk, void* dv, float* dg, float* dh0, void* ws, size_t ws_bytes,
-                           void* hip_stream) {
-  gdr_status st = check(p);
+bool nothing(const gdr_linear_problem* p, int64_t rows) { return p->B == 0 || p->T == 0 || rows == 0; }
+
+gdr_status linear_backward(const gdr_linear_problem* p, const int64_t* cu, bool ragged, int64_t rows, const void* q,
+                           const void* k, const void* v, const float* g, const float* h0, const void* dout,
+                           const float* dht, void* dq, void* dk, void* dv, float* dg, float* dh0, void* ws,
+                           size_t ws_bytes, void* hip_stream) {
+  gdr_status st = check(p, rows);
   if (st != GDR_OK) return st;
-  const LinShape s = shape_of(p);
-  const bool empty = s.B == 0 || s.T == 0;
+  const LinShape s = shape_of(p, ragged, rows);
+  const bool empty = nothing(p, rows);
   if (!empty && (!q || !k || !v || !dout || !dq || !dk || !dv)) return GDR_ERR_NULL_ARG;
   if (ragged && !empty && !cu) return GDR_ERR_NULL_ARG;
   if (dg && !g) return GDR_ERR_NULL_ARG;
@@ -138,7 +148,7 @@ gdr_status linear_backward(const gdr_linear_problem* p, const int64_t* cu, bool 
                           static_cast<const void*>(dh0)})
     if (misaligned(ptr)) return GDR_ERR_BAD_ALIGNMENT;
   if (misaligned(g, 4) || misaligned(dg, 4) || misaligned(cu, 8)) return GDR_ERR_BAD_ALIGNMENT;
-  if ((st = check_ws(ws, ws_bytes, empty ? 0 : backward_bytes(p))) != GDR_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, empty ? 0 : backward_bytes(p, rows))) != GDR_OK) return st;
   const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
   const gdr::LinBwdArgs a{q, k, v, dout, g, h0, dht, dq, dk, dv, dg, dh0, cu};
   const bool chunk = !empty && chunked(p, true);
@@ -203,7 +213,16 @@ gdr_status gdr_linear_backward_workspace(const gdr_linear_problem* p, size_t* by
   const gdr_status st = check(p);
   if (st != GDR_OK) return st;
   if (!bytes) return GDR_ERR_NULL_ARG;
-  *bytes = p->B == 0 || p->T == 0 ? 0 : backward_bytes(p);
+  *bytes = nothing(p, kUncounted) ? 0 : backward_bytes(p, kUncounted);
+  return GDR_OK;
+}
+
+gdr_status gdr_linear_backward_varlen_workspace(const gdr_linear_problem* p, int64_t rows, size_t* bytes) {
+  if (rows < 0) return p ? GDR_ERR_BAD_SHAPE : GDR_ERR_NULL_ARG;
+  const gdr_status st = check(p, rows);
+  if (st != GDR_OK) return st;
+  if (!bytes) return GDR_ERR_NULL_ARG;
+  *bytes = nothing(p, rows) ? 0 : backward_bytes(p, rows);
   return GDR_OK;
 }
 
@@ -223,15 +242,25 @@ gdr_status gdr_linear_backward(const gdr_linear_problem* p, const void* q, const
                                const float* g, const float* h0, const void* dout, const float* dht, void* dq,
                                void* dk, void* dv, float* dg, float* dh0, void* ws, size_t ws_bytes,
                                void* hip_stream) {
-  return linear_backward(p, nullptr, false, q, k, v, g, h0, dout, dht, dq, dk, dv, dg, dh0, ws, ws_bytes,
-                         hip_stream);
+  return linear_backward(p, nullptr, false, kUncounted, q, k, v, g, h0, dout, dht, dq, dk, dv, dg, dh0, ws,
+                         ws_bytes, hip_stream);
 }
 
 gdr_status gdr_linear_backward_varlen(const gdr_linear_problem* p, const int64_t* cu_seqlens, const void* q,
                                       const void* k, const void* v, const float* g, const float* h0,
                                       const void* dout, const float* dht, void* dq, void* dk, void* dv, float* dg,
                                       float* dh0, void* ws, size_t ws_bytes, void* hip_stream) {
-  return linear_backward(p, cu_seqlens, true, q, k, v, g, h0, dout, dht, dq, dk, dv, dg, dh0, ws, ws_bytes,
+  return linear_backward(p, cu_seqlens, true, kUncounted, q, k, v, g, h0, dout, dht, dq, dk, dv, dg, dh0, ws,
+                         ws_bytes, hip_stream);
+}
+
+gdr_status gdr_linear_backward_varlen_rows(const gdr_linear_problem* p, int64_t rows, const int64_t* cu_seqlens,
+                                           const void* q, const void* k, const void* v, const float* g,
+                                           const float* h0, const void* dout, const float* dht, void* dq, void* dk,
+                                           void* dv, float* dg, float* dh0, void* ws, size_t ws_bytes,
+                                           void* hip_stream) {
+  if (rows < 0) return p ? GDR_ERR_BAD_SHAPE : GDR_ERR_NULL_ARG;
+  return linear_backward(p, cu_seqlens, true, rows, q, k, v, g, h0, dout, dht, dq, dk, dv, dg, dh0, ws, ws_bytes,
                          hip_stream);
 }
 

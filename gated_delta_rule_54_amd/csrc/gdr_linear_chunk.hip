@@ -308,6 +308,7 @@ struct Walk {
   int64_t b, bh, seg, row0;  // row0: the segment's first token row
   int64_t t0, len;           // the segment's first token in its sequence, its length
   int h, col0, sl;
+  int64_t part0;             // its first partial row
   bool first, last;          // of the sequence's segments, in the chain's direction
 };
 
@@ -380,13 +381,13 @@ struct Out {
   __device__ __forceinline__ void init(const LinChains& a, const Walk& w, int w2) {
     const LinChain& c = w.c;
     const bool rev = c.rev != 0;
-    const int64_t first = rev ? w.len - 1 : 0, bt = w.b * a.T + w.t0 + first;
+    const int64_t first = rev ? w.len - 1 : 0, part = w.part0 + first;
     const int heads = a.Hv / c.og, h = w.h / c.og;
-    const int64_t row = c.out_partial ? bt : w.row0 + first;
+    const int64_t row = c.out_partial ? part : w.row0 + first;
     const uint32_t wide = static_cast<uint32_t>(heads) * c.D2;
     o = Rows{static_cast<char*>(c.out) + ((row * heads + h) * c.D2 + w.col0) * SIZE, wide * SIZE, w2 * SIZE, rev};
     if constexpr (J::ADD)
-      p = Rows{reinterpret_cast<char*>(c.sum) + ((bt * heads + h) * c.D2 + w.col0) * 4, wide * 4,
+      p = Rows{reinterpret_cast<char*>(c.sum) + ((part * heads + h) * c.D2 + w.col0) * 4, wide * 4,
                static_cast<uint32_t>(w2) * 4, rev};
   }
   // The sum so far at row i, column col (on: inside).
@@ -616,7 +617,8 @@ __device__ __forceinline__ void out_by_rows(const LinChains& a, const Walk& w, F
     oe = re.row(i, C) + g4 * ES;
   }
   // e in parts: a wave sums its NI tiles of columns
-  float* const ep = EX ? c.e + ((w.sl * (4 / NI) + wave / NI) * a.B * a.Hv + w.bh) * a.T + w.t0 : nullptr;
+  float* const ep =
+      EX ? c.e + (static_cast<int64_t>(w.sl * (4 / NI) + wave / NI) * a.Hv + w.h) * a.rows + w.part0 : nullptr;
   __syncthreads();
 
   int b = 0;
@@ -898,8 +900,8 @@ __device__ __forceinline__ void out_by_columns(const LinChains& a, const Walk& w
     __syncthreads();
     if constexpr (EX) {
       if (tid < n) {
-        const int64_t t = rev ? w.t0 + w.len - 1 - at - tid : w.t0 + at + tid;
-        c.e[(w.sl * a.B * a.Hv + w.bh) * a.T + t] = (s.e[0][tid] + s.e[1][tid]) + (s.e[2][tid] + s.e[3][tid]);
+        const int64_t row = w.part0 + (rev ? w.len - 1 - at - tid : at + tid);
+        c.e[(static_cast<int64_t>(w.sl) * a.Hv + w.h) * a.rows + row] = (s.e[0][tid] + s.e[1][tid]) + (s.e[2][tid] + s.e[3][tid]);
       }
     }
   }
@@ -962,6 +964,7 @@ __device__ __forceinline__ bool find(const LinChains& a, const Units& u, int64_t
   if (w.t0 >= sp.len && w.seg > 0) return false;
   w.len = min(a.seg, sp.len - w.t0);
   w.row0 = sp.t0 + w.t0;
+  w.part0 = lin_part_row(a, w.b, sp, w.t0);
   const bool begin = w.seg == 0, last = w.t0 + w.len >= sp.len;
   w.first = w.c.rev ? last : begin;
   w.last = w.c.rev ? begin : last;

@@ -118,14 +118,14 @@ __global__ __launch_bounds__(256) void lin_seq_kernel(LinChains a) {
         for (int j = 0; j < 4; ++j)
           s[j] = (buf[0][4 * cg + j] + buf[1][4 * cg + j]) + (buf[2][4 * cg + j] + buf[3][4 * cg + j]);
         if (col < c.D2) {
-          const int64_t row = c.out_partial ? b * a.T + t : sp.t0 + t;
+          const int64_t row = c.out_partial ? lin_part_row(a, b, sp, t) : sp.t0 + t;
           const int64_t at = (row * a.Hv + h) * c.D2 + col;
           if (c.out_partial || !a.out_bf16) st4<float>(static_cast<float*>(c.out) + at, s);
           else st4<bf16_t>(static_cast<bf16_t*>(c.out) + at, s);
         }
         if (c.ex) {
           const float e = row16_sum(s[0] * k.ex[0] + s[1] * k.ex[1] + s[2] * k.ex[2] + s[3] * k.ex[3]);
-          if (tid == 0) c.e[(sl * a.B * a.Hv + bh) * a.T + t] = e;
+          if (tid == 0) c.e[(static_cast<int64_t>(sl) * a.Hv + h) * a.rows + lin_part_row(a, b, sp, t)] = e;
         }
       }
     }
@@ -238,22 +238,35 @@ __global__ __launch_bounds__(256) void lin_token_kernel(LinChains a) {
   }
 }
 
-// Sums fp32 rows [B][T][Hv][Dk] over the value heads of each key head into
-// [rows][Hk][Dk] of TO; blockIdx.y: dq, dk.  One thread per 4 columns.
+// The sequence that holds row r of a ragged batch: the last one that starts at
+// or before it.
+__device__ __forceinline__ int64_t lin_sequence_of(const int64_t* cu, int64_t B, int64_t r) {
+  int64_t lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int64_t m = (lo + hi) / 2;
+    if (cu[m] <= r) lo = m;
+    else hi = m;
+  }
+  return lo;
+}
+
+// Sums fp32 partial rows [n][Hv][Dk] over the value heads of each key head into
+// rows [..][Hk][Dk] of TO; blockIdx.y: dq, dk.  One thread per 4 columns.
 template <typename TO>
 __global__ __launch_bounds__(256) void lin_group_sum_kernel(const float* pdq, const float* pdk, TO* dq, TO* dk,
-                                                            int64_t B, int64_t T, int Hk, int Hv, int Dk,
-                                                            const int64_t* cu) {
+                                                            int64_t B, int64_t T, int64_t n, bool packed, int Hk,
+                                                            int Hv, int Dk, const int64_t* cu) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int per = Hk * (Dk / 4);
-  const int64_t bt = i / per;
-  if (bt >= B * T) return;
+  const int64_t r = i / per;
+  if (r >= n) return;
   const int u = static_cast<int>(i % per), hk = u / (Dk / 4), d = u % (Dk / 4) * 4;
-  const int64_t b = bt / T, t = bt % T;
+  const int64_t b = cu && packed ? lin_sequence_of(cu, B, r) : r / T;
   const LinSpan sp = lin_span(cu, b, T);
-  if (t >= sp.len) return;
+  const int64_t t = packed ? r - sp.t0 : r % T;
+  if (t < 0 || t >= sp.len) return;
   const int G = Hv / Hk;
-  const float* p = (blockIdx.y ? pdk : pdq) + (bt * Hv + hk * G) * Dk + d;
+  const float* p = (blockIdx.y ? pdk : pdq) + (r * Hv + hk * G) * Dk + d;
   float s[4] = {0.f, 0.f, 0.f, 0.f};
   for (int j = 0; j < G; ++j) {
     float x[4];
@@ -273,7 +286,8 @@ __global__ __launch_bounds__(256) void lin_group_sum_kernel(const float* pdq, co
 constexpr int kDgStep = 1024;
 __global__ __launch_bounds__(kDgStep) void lin_dg_kernel(const float* eq, const float* ek, const float* xdot, int nsl,
                                                          int dots, float* dg, double* dgsum, int64_t B, int64_t T,
-                                                         int Hv, int64_t segments, int64_t seg, const int64_t* cu) {
+                                                         int64_t rows, bool packed, int Hv, int64_t segments,
+                                                         int64_t seg, const int64_t* cu) {
   constexpr int W = kDgStep / 64;
   __shared__ double wsum[W];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -283,11 +297,12 @@ __global__ __launch_bounds__(kDgStep) void lin_dg_kernel(const float* eq, const 
   const int64_t t0 = s * seg, t1 = sp.len < t0 + seg ? sp.len : t0 + seg;
   double carry = 0.0, total = 0.0;
   for (int j = 0; j < dots; ++j) carry += xdot[(s * B * Hv + bh) * dots + j];
+  const int64_t row0 = packed ? sp.t0 : b * T;
   auto term = [&](int64_t t) {
     double v = 0.0;
     if (t >= t0)
       for (int j = 0; j < nsl; ++j) {
-        const int64_t at = (j * B * Hv + bh) * T + t;
+        const int64_t at = (static_cast<int64_t>(j) * Hv + h) * rows + row0 + t;
         v += static_cast<double>(eq[at]) - static_cast<double>(ek[at]);
       }
     return v;
@@ -362,7 +377,7 @@ LinChains lin_forward_chains(const LinShape& s, const LinFwdArgs& a) {
   LinChains L{};
   const int G = s.Hv / s.Hk;
   L.n = 1, L.segments = 1, L.seg = s.T;
-  L.B = s.B, L.T = s.T, L.Hv = s.Hv, L.group = G, L.g = a.g, L.head_decay = s.head_decay;
+  L.B = s.B, L.T = s.T, L.rows = s.rows, L.packed = s.packed, L.Hv = s.Hv, L.group = G, L.g = a.g, L.head_decay = s.head_decay;
   L.out_bf16 = s.out_bf16, L.cu = a.cu;
   LinChain& c = L.c[0];
   c.x = a.q, c.xr = s.q_row, c.xg = G;
@@ -381,11 +396,11 @@ size_t lin_bwd_parts(const LinShape& s, int64_t segments, bool summed, char* bas
     off += (bytes + 255) / 256 * 256;
     return at;
   };
-  const size_t bh = static_cast<size_t>(s.B) * s.Hv, n = bh * s.T, nsl = lin_slices(s.Dk);
+  const size_t bh = static_cast<size_t>(s.B) * s.Hv, n = static_cast<size_t>(s.Hv) * s.rows, nsl = lin_slices(s.Dk);
   p->eq = reinterpret_cast<float*>(take(2 * nsl * n * 4));
   p->ek = reinterpret_cast<float*>(take(2 * nsl * n * 4));
   p->xdot = reinterpret_cast<float*>(take(segments * bh * nsl * 4 * 4));
-  const size_t heads = s.Hv == s.Hk ? 0 : summed ? s.Hk : s.Hv, part = heads * s.B * s.T * s.Dk * 4;
+  const size_t heads = s.Hv == s.Hk ? 0 : summed ? s.Hk : s.Hv, part = heads * s.rows * s.Dk * 4;
   p->pdq = reinterpret_cast<float*>(take(part));
   p->pdk = reinterpret_cast<float*>(take(part));
   p->dgsum = reinterpret_cast<double*>(take(s.head_decay ? segments * bh * 8 : 0));
@@ -397,7 +412,7 @@ LinChains lin_backward_chains(const LinShape& s, const LinBwdArgs& a, const LinB
   const int G = s.Hv / s.Hk;
   const int64_t d_row = static_cast<int64_t>(s.Hv) * s.Dv;
   L.n = 3, L.segments = 1, L.seg = s.T;
-  L.B = s.B, L.T = s.T, L.Hv = s.Hv, L.group = G, L.g = a.g, L.head_decay = s.head_decay;
+  L.B = s.B, L.T = s.T, L.rows = s.rows, L.packed = s.packed, L.Hv = s.Hv, L.group = G, L.g = a.g, L.head_decay = s.head_decay;
   L.out_bf16 = s.out_bf16, L.cu = a.cu;
   LinChain& q = L.c[0];  // dq
   q.x = a.dout, q.xr = d_row, q.xg = 1;
@@ -432,21 +447,21 @@ hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const Lin
                                int dots, int64_t segments, int64_t seg, hipStream_t st) {
   if (s.Hv != s.Hk && !summed) {
     ProfScope prof("linear_group_sum", st);
-    const int64_t n = s.B * s.T * s.Hk * (s.Dk / 4);
+    const int64_t n = s.rows * s.Hk * (s.Dk / 4);
     const dim3 grid(static_cast<unsigned>((n + 255) / 256), 2);
     if (s.out_bf16)
       lin_group_sum_kernel<<<grid, 256, 0, st>>>(p.pdq, p.pdk, static_cast<bf16_t*>(a.dq), static_cast<bf16_t*>(a.dk),
-                                                 s.B, s.T, s.Hk, s.Hv, s.Dk, a.cu);
+                                                 s.B, s.T, s.rows, s.packed, s.Hk, s.Hv, s.Dk, a.cu);
     else
       lin_group_sum_kernel<<<grid, 256, 0, st>>>(p.pdq, p.pdk, static_cast<float*>(a.dq), static_cast<float*>(a.dk),
-                                                 s.B, s.T, s.Hk, s.Hv, s.Dk, a.cu);
+                                                 s.B, s.T, s.rows, s.packed, s.Hk, s.Hv, s.Dk, a.cu);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
   if (!a.dg) return hipSuccess;
   ProfScope prof("linear_dg", st);
   double* sums = s.head_decay ? p.dgsum : nullptr;
   lin_dg_kernel<<<static_cast<unsigned>(s.B * s.Hv * segments), kDgStep, 0, st>>>(
-      p.eq, p.ek, p.xdot, es, dots, a.dg, sums, s.B, s.T, s.Hv, segments, seg, a.cu);
+      p.eq, p.ek, p.xdot, es, dots, a.dg, sums, s.B, s.T, s.rows, s.packed, s.Hv, segments, seg, a.cu);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   if (sums) lin_dg_head_kernel<<<s.Hv, 64, 0, st>>>(sums, a.dg, s.B * segments, s.Hv);
   return hipGetLastError();

@@ -150,10 +150,14 @@ def gdr_linear_forward_workspace(prob):
     return n.value
 
 
-def gdr_linear_backward_workspace(prob):
+def gdr_linear_backward_workspace(prob, rows=None):
+    """``rows``: the token rows of a ragged batch, where they are counted."""
     n = ctypes.c_size_t(0)
-    _check_status(lib().gdr_linear_backward_workspace(ctypes.byref(prob), ctypes.byref(n)),
-                  "gdr_linear_backward_workspace")
+    if rows is None:
+        st = lib().gdr_linear_backward_workspace(ctypes.byref(prob), ctypes.byref(n))
+    else:
+        st = lib().gdr_linear_backward_varlen_workspace(ctypes.byref(prob), rows, ctypes.byref(n))
+    _check_status(st, "gdr_linear_backward_workspace")
     return n.value
 
 
@@ -216,12 +220,13 @@ def gdr_linear_backward(q, k, v, g, h0, dout, dht=None, *, algo="auto", out_dtyp
     dv = torch.empty(v.shape, dtype=out_dtype, device=dev)
     dg = torch.empty(g.shape, dtype=torch.float32, device=dev) if want_dg and g is not None else None
     dh0 = torch.empty(state, dtype=torch.float32, device=dev) if want_dh0 else None
-    ws = _workspace(gdr_linear_backward_workspace(prob), dev)
+    rows = None if cu_seqlens is None else q.shape[1]
+    ws = _workspace(gdr_linear_backward_workspace(prob, rows), dev)
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(h0), _ptr(dout), _ptr(dht), _ptr(dq), _ptr(dk), _ptr(dv),
             _ptr(dg), _ptr(dh0), _ptr(ws), 0 if ws is None else ws.numel(),
             _raw_stream(dev.index))
     if cu_seqlens is not None:
-        st = lib().gdr_linear_backward_varlen(ctypes.byref(prob), _ptr(cu_seqlens), *args)
+        st = lib().gdr_linear_backward_varlen_rows(ctypes.byref(prob), rows, _ptr(cu_seqlens), *args)
     else:
         st = lib().gdr_linear_backward(ctypes.byref(prob), *args)
     _check_status(st, "gdr_linear_backward")

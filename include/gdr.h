@@ -310,6 +310,19 @@ gdr_status gdr_linear_backward_varlen(const gdr_linear_problem* p, const int64_t
                                       const void* dout, const float* dht, void* dq, void* dk, void* dv, float* dg,
                                       float* dh0, void* ws, size_t ws_bytes, void* hip_stream);
 
+/* The ragged VJP with its token rows counted.  gdr_linear_backward_workspace
+ * of a ragged problem has to hold B * T tokens, the longest sequence's length
+ * for each; given `rows`, the rows of q, k, v, dout and g (cu_seqlens[B] and
+ * uncovered rows behind it included), it holds one entry for each of them
+ * where that is less.  The limit on B * T * Hk then is one on rows * Hk.
+ * Every offset lies in [0, rows]; rows = 0 is a batch of empty sequences. */
+gdr_status gdr_linear_backward_varlen_workspace(const gdr_linear_problem* p, int64_t rows, size_t* bytes);
+gdr_status gdr_linear_backward_varlen_rows(const gdr_linear_problem* p, int64_t rows, const int64_t* cu_seqlens,
+                                           const void* q, const void* k, const void* v, const float* g,
+                                           const float* h0, const void* dout, const float* dht, void* dq, void* dk,
+                                           void* dv, float* dg, float* dh0, void* ws, size_t ws_bytes,
+                                           void* hip_stream);
+
 /* ---------------------------------------------------------------------------
  * Group norm of the heads' outputs, with an affine map and an activation:
  * what a layer does with o of either recurrence.  x is [rows, groups,

@@ -1,0 +1,135 @@
+"""The ragged VJP's workspace follows the rows that are there, not the longest
+sequence's length for every sequence; and the VJP that is not told the rows
+gives the same bits."""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_54_amd as gdr
+from gated_delta_rule_54_amd import binding as B
+from gated_delta_rule_54_amd import linear as L
+from tests.test_gpu_linear import BF, F, draw, to_dev, verify
+from tests.test_linear_abi import FAKE, PAST, prob
+
+GiB = 1 << 30
+
+
+def need(p, rows):
+    n = ctypes.c_size_t(12345)
+    return B.lib().gdr_linear_backward_varlen_workspace(ctypes.byref(p), rows, ctypes.byref(n)), n.value
+
+
+def call(p, rows, cu=FAKE, ws=FAKE, nws=PAST, **over):
+    a = dict(q=FAKE, k=FAKE, v=FAKE, g=FAKE, h0=None, dout=FAKE, dht=None, dq=FAKE, dk=FAKE, dv=FAKE, dg=FAKE,
+             dh0=None)
+    a.update(over)
+    return B.lib().gdr_linear_backward_varlen_rows(ctypes.byref(p), rows, cu, *a.values(), ws, nws, None)
+
+
+@pytest.mark.parametrize("algo", [0, 1, 2])
+@pytest.mark.parametrize("flags", [0, 1])
+def test_one_long_document_and_short_prompts(algo, flags):
+    """32768 tokens and 63 prompts of 100."""
+    p = prob(B=64, T=32768, Hk=16, Hv=32, Dk=128, Dv=128, algo=algo, flags=flags)
+    rows = 32768 + 63 * 100
+    st, n = need(p, rows)
+    tensors = rows * (2 * 16 * 128 + 2 * 32 * 128 + 2 * 16 * 128 + 32 * 128) * 2
+    assert st == 0 and n % 256 == 0 and n <= 2 * tensors, (n, tensors)
+    # no more than what is asked without the rows, whatever they are
+    st, bound = need(p, 1 << 40)
+    plain = ctypes.c_size_t(0)
+    assert B.lib().gdr_linear_backward_workspace(ctypes.byref(p), ctypes.byref(plain)) == 0
+    assert st == 0 and bound == plain.value and need(p, 64 * 32768) == (0, bound)
+    assert gdr.gdr_linear_backward_workspace(p, rows) == n and gdr.gdr_linear_backward_workspace(p) == bound
+
+
+def test_limits_and_arguments():
+    p = prob(B=64, T=1 << 22, Hk=16, Hv=32)  # B T Hk is past 2^31, the rows are not
+    assert need(p, 1 << 22)[0] == 0 and need(p, 1 << 28) == (3, 12345)
+    assert need(prob(), -1) == (2, 12345) and call(prob(), -1) == 2
+    assert B.lib().gdr_linear_backward_varlen_workspace(None, 5, None) == 1
+    assert B.lib().gdr_linear_backward_varlen_workspace(ctypes.byref(prob()), 5, None) == 1
+    assert B.lib().gdr_linear_backward_varlen_rows(None, 5, *[FAKE] * 14, 0, None) == 1
+    assert need(prob(), 0) == (0, 0) and need(prob(T=0), 9) == (0, 0)
+    for name in ("q", "k", "v", "dout", "dq", "dk", "dv"):
+        assert call(prob(), 90, **{name: None}) == 1
+    assert call(prob(), 90, cu=None) == 1 and call(prob(), 90, g=None) == 1
+    n = need(prob(), 90)[1]
+    assert call(prob(), 90, ws=None, nws=0) == 1 and call(prob(), 90, nws=n - 1) == 5
+    assert call(prob(), 90, cu=FAKE + 4) == 4 and call(prob(Dk=24), 90) == 3
+
+
+def uncounted(t, cu, T, out, algo):
+    """gdr_linear_backward_varlen, whose workspace holds T rows a sequence."""
+    N, (_, rows, Hk, Dk), (Hv, Dv) = cu.numel() - 1, t["q"].shape, t["v"].shape[2:]
+    p = L.GdrLinearProblem(N, T, Hk, Hv, Dk, Dv, L._dtype(t["q"].dtype, "q"), L._dtype(out, "out"),
+                           1 if t["g"].dim() == 1 else 0, B.ALGOS[algo], 0, 0, 0)
+    e = lambda a, dt: torch.full_like(a, 7.0, dtype=dt)
+    res = [e(t["q"], out), e(t["k"], out), e(t["v"], out), e(t["g"], F), e(t["dht"], F)]
+    ws = torch.full((gdr.gdr_linear_backward_workspace(p),), 255, dtype=torch.uint8, device="cuda")
+    st = B.lib().gdr_linear_backward_varlen(
+        ctypes.byref(p), cu.data_ptr(), *(t[n].data_ptr() for n in ("q", "k", "v", "g", "h0", "do", "dht")),
+        *(a.data_ptr() for a in res), ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    return res
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("algo", ["sequential", "chunked"])
+@pytest.mark.parametrize("Hk,Hv,gate", [(2, 2, "token"), (2, 6, "token"), (1, 4, "head")])
+@pytest.mark.parametrize("lens,front,behind", [([400, 3, 0, 17, 1, 64, 70], 0, 0), ([0, 5, 300, 0], 900, 4),
+                                               ([30, 31, 29], 2, 1), ([0, 0], 3, 0)])
+def test_rows_counted_and_not(algo, Hk, Hv, gate, lens, front, behind):
+    """Uncovered rows before and behind, few rows and more rows than B * T."""
+    cu = np.concatenate([[front], front + np.cumsum(lens)]).astype(np.int64)
+    x = draw(41, 1, int(cu[-1]) + behind, Hk, Hv, 64, 128, BF, gate)
+    r = np.random.default_rng(42)
+    x["h0"], x["dht"] = (r.standard_normal((len(lens), Hv, 64, 128)).astype(np.float32) for _ in range(2))
+    t = to_dev(x, BF)
+    c, T = torch.from_numpy(cu).cuda(), max(1, max(lens))
+    got = gdr.gdr_linear_backward(t["q"], t["k"], t["v"], t["g"], t["h0"], t["do"], t["dht"], algo=algo, out_dtype=F,
+                                  cu_seqlens=c, max_seqlen=T)
+    other = uncounted(t, c, T, F, algo)
+    inside = slice(int(cu[0]), int(cu[-1]))
+    for i, (a, b) in enumerate(zip(got, other)):
+        if i == 4 or (i == 3 and gate == "head"):
+            assert torch.equal(a, b), i
+        else:
+            assert torch.equal(a[:, inside], b[:, inside]), i
+            assert (b[:, :front] == 7).all() and (b[:, int(cu[-1]):] == 7).all(), i
+    for i, n in enumerate(lens):  # and against 64 bits
+        if n and gate == "token":
+            s = slice(cu[i], cu[i + 1])
+            one = {a: x[a][:, s] for a in ("q", "k", "v", "g", "do")}
+            one.update(h0=x["h0"][i:i + 1], dht=x["dht"][i:i + 1])
+            o, ht = gdr.gdr_linear_forward(*(t[a][:, s].contiguous() for a in ("q", "k", "v", "g")), t["h0"][i:i + 1],
+                                           algo=algo)
+            verify(one, F, o, ht, [a[:, s] for a in got[:4]] + [got[4][i:i + 1]])
+
+
+@pytest.mark.gpu
+def test_a_document_among_short_prompts_on_the_card():
+    """The batch whose workspace would be tens of GiB by the longest length,
+    with dq and dk of several value heads: the short sequences' gradients are
+    those of a call of their own."""
+    lens = [9000] + [40] * 47
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
+    g = torch.Generator(device="cuda").manual_seed(43)
+    n = lambda *s: torch.randn(1, int(cu[-1]), *s, device="cuda", generator=g)
+    q, k, v, do = (n(h, 128).to(BF) for h in (8, 8, 32, 32))
+    gate = -torch.nn.functional.softplus(n(32))
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    got = gdr.gdr_linear_backward(q, k, v, gate, None, do, out_dtype=BF, cu_seqlens=torch.from_numpy(cu).cuda())
+    torch.cuda.synchronize()
+    assert torch.cuda.max_memory_allocated() - before < 3 * GiB
+    s = slice(int(cu[20]), int(cu[21]))
+    one = gdr.gdr_linear_backward(*(a[:, s].contiguous() for a in (q, k, v, gate)), None, do[:, s].contiguous(),
+                                  algo="chunked", out_dtype=BF)
+    for a, b in zip(got[:4], one[:4]):
+        # fp32 sums over heads in another order; a bf16 result may then round to the next value
+        tol = 2.0 ** -7 if a.dtype == BF else 2.0 ** -18
+        assert ((a[:, s] - b).abs() <= tol * (b.abs() + b.abs().max())).all()
