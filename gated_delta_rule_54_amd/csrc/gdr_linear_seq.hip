@@ -282,10 +282,13 @@ __global__ __launch_bounds__(256) void lin_group_sum_kernel(const float* pdq, co
 // 64 bits: they telescope to what the later tokens of the segment give, so
 // their terms cancel.  One workgroup walks its segment from the end, 1024
 // tokens at a time: a step is a chain of latencies (loads, shuffles, two
-// barriers), so long ones are worth their idle lanes in short segments.
+// barriers), so long ones are worth their idle lanes in short segments.  Where
+// the factor is zero the state before has no part in anything after it: dg is 0,
+// not what the sums' roundings leave.
+constexpr float kNoFactor = -104.f;  // e^g below half of fp32's least value
 constexpr int kDgStep = 1024;
 __global__ __launch_bounds__(kDgStep) void lin_dg_kernel(const float* eq, const float* ek, const float* xdot, int nsl,
-                                                         int dots, float* dg, double* dgsum, int64_t B, int64_t T,
+                                                         int dots, const float* g, float* dg, double* dgsum, int64_t B, int64_t T,
                                                          int64_t rows, bool packed, int Hv, int64_t segments,
                                                          int64_t seg, const int64_t* cu) {
   constexpr int W = kDgStep / 64;
@@ -330,7 +333,10 @@ __global__ __launch_bounds__(kDgStep) void lin_dg_kernel(const float* eq, const 
     p += base;
     if (t >= t0) {
       if (dgsum) total += p;
-      else dg[(sp.t0 + t) * Hv + h] = static_cast<float>(p);
+      else {
+        const int64_t at = (sp.t0 + t) * Hv + h;
+        dg[at] = g[at] < kNoFactor ? 0.f : static_cast<float>(p);
+      }
     }
   }
   if (dgsum) {
@@ -347,13 +353,14 @@ __global__ __launch_bounds__(kDgStep) void lin_dg_kernel(const float* eq, const 
 }
 
 // dg [Hv] with a decay per head: the segments' sums, one wave per head.
-__global__ __launch_bounds__(64) void lin_dg_head_kernel(const double* dgsum, float* dg, int64_t n, int Hv) {
+__global__ __launch_bounds__(64) void lin_dg_head_kernel(const double* dgsum, const float* g, float* dg, int64_t n,
+                                                         int Hv) {
   const int h = blockIdx.x;
   double s = 0.0;
   for (int64_t i = threadIdx.x; i < n; i += 64) s += dgsum[i * Hv + h];
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) s += __shfl_xor(s, m, 64);
-  if (threadIdx.x == 0) dg[h] = static_cast<float>(s);
+  if (threadIdx.x == 0) dg[h] = g[h] < kNoFactor ? 0.f : static_cast<float>(s);
 }
 
 __global__ __launch_bounds__(256) void lin_zero_kernel(float* p, int n) {
@@ -461,9 +468,9 @@ hipError_t launch_lin_bwd_tail(const LinShape& s, const LinBwdArgs& a, const Lin
   ProfScope prof("linear_dg", st);
   double* sums = s.head_decay ? p.dgsum : nullptr;
   lin_dg_kernel<<<static_cast<unsigned>(s.B * s.Hv * segments), kDgStep, 0, st>>>(
-      p.eq, p.ek, p.xdot, es, dots, a.dg, sums, s.B, s.T, s.rows, s.packed, s.Hv, segments, seg, a.cu);
+      p.eq, p.ek, p.xdot, es, dots, a.g, a.dg, sums, s.B, s.T, s.rows, s.packed, s.Hv, segments, seg, a.cu);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  if (sums) lin_dg_head_kernel<<<s.Hv, 64, 0, st>>>(sums, a.dg, s.B * segments, s.Hv);
+  if (sums) lin_dg_head_kernel<<<s.Hv, 64, 0, st>>>(sums, a.g, a.dg, s.B * segments, s.Hv);
   return hipGetLastError();
 }
 

@@ -259,7 +259,11 @@ gdr_status gdr_backward_varlen(const gdr_problem* p, const int64_t* cu_seqlens,
  * GDR_ERR_UNSUPPORTED).
  *
  * Results: sums, the state and everything returned in fp32 (an fp32 o, dq,
- * dk, dv, and ht, dg, dh0 always) carry fp32 accuracy also from bf16 inputs;
+ * dk, dv, and ht, dg, dh0 always) carry fp32 accuracy also from bf16 inputs,
+ * relative to the sums of their terms' absolute values.  dg's terms are those of
+ * dg_t = sum_{r >= t} (q_r . dq_r - k_r . dk_r) + <S_T, dS_T>, which cancel:
+ * where a head decays strongly, dg_t is far smaller than they are, and its
+ * rounding is not.  Where alpha_t is 0 in fp32, dg_t is 0.
  * bf16 outputs are rounded once from sums whose matrix-core operands hold 16
  * bits or more (24 in dq and dk where dg is wanted: asking for it can move one
  * of their values to the next bf16).  Every row past a sequence's end, and rows that no sequence
