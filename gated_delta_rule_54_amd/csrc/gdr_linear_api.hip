@@ -35,7 +35,7 @@ constexpr int64_t kUncounted = -1;
 bool counted(const gdr_linear_problem* p, int64_t rows) { return rows != kUncounted && rows <= p->B * p->T; }
 int64_t partial_rows(const gdr_linear_problem* p, int64_t rows) { return counted(p, rows) ? rows : p->B * p->T; }
 
-gdr_status check(const gdr_linear_problem* p, int64_t rows = kUncounted) {
+gdr_status check(const gdr_linear_problem* p, bool backward, int64_t rows = kUncounted) {
   if (!p) return GDR_ERR_NULL_ARG;
   if (p->B < 0 || p->T < 0 || p->Hk <= 0 || p->Hv <= 0 || p->Dk <= 0 || p->Dv <= 0) return GDR_ERR_BAD_SHAPE;
   if (p->Hv % p->Hk != 0) return GDR_ERR_BAD_SHAPE;
@@ -52,7 +52,9 @@ gdr_status check(const gdr_linear_problem* p, int64_t rows = kUncounted) {
   // the heads' states (segments only where there are few)
   if (p->B > 65535 || p->Hv > 65535 || p->T > 0x7fffffffLL) return GDR_ERR_UNSUPPORTED;
   const int slices = 2 * gdr::lin_slices(p->Dk) + gdr::lin_slices(p->Dv);
-  if (p->B * p->Hv * slices > (1 << 22) || partial_rows(p, rows) * p->Hk > 0x7fffffffLL) return GDR_ERR_UNSUPPORTED;
+  if (p->B * p->Hv * slices > (1 << 22)) return GDR_ERR_UNSUPPORTED;
+  // tokens, and in the VJP those of each key head
+  if (partial_rows(p, rows) * (backward ? p->Hk : 1) > 0x7fffffffLL) return GDR_ERR_UNSUPPORTED;
   return GDR_OK;
 }
 
@@ -108,7 +110,7 @@ gdr_status check_ws(const void* ws, size_t have, size_t need) {
 gdr_status linear_forward(const gdr_linear_problem* p, const int64_t* cu, bool ragged, const void* q, const void* k,
                           const void* v, const float* g, const float* h0, void* o, float* ht, void* ws,
                           size_t ws_bytes, void* hip_stream) {
-  gdr_status st = check(p);
+  gdr_status st = check(p, false);
   if (st != GDR_OK) return st;
   const LinShape s = shape_of(p);
   const bool empty = s.B == 0 || s.T == 0;
@@ -136,7 +138,7 @@ gdr_status linear_backward(const gdr_linear_problem* p, const int64_t* cu, bool 
                            const void* k, const void* v, const float* g, const float* h0, const void* dout,
                            const float* dht, void* dq, void* dk, void* dv, float* dg, float* dh0, void* ws,
                            size_t ws_bytes, void* hip_stream) {
-  gdr_status st = check(p, rows);
+  gdr_status st = check(p, true, rows);
   if (st != GDR_OK) return st;
   const LinShape s = shape_of(p, ragged, rows);
   const bool empty = nothing(p, rows);
@@ -202,7 +204,7 @@ gdr::NormArgs norm_args(const gdr_norm_problem* p) {
 extern "C" {
 
 gdr_status gdr_linear_forward_workspace(const gdr_linear_problem* p, size_t* bytes) {
-  const gdr_status st = check(p);
+  const gdr_status st = check(p, false);
   if (st != GDR_OK) return st;
   if (!bytes) return GDR_ERR_NULL_ARG;
   *bytes = p->B == 0 || p->T == 0 ? 0 : forward_bytes(p);
@@ -210,7 +212,7 @@ gdr_status gdr_linear_forward_workspace(const gdr_linear_problem* p, size_t* byt
 }
 
 gdr_status gdr_linear_backward_workspace(const gdr_linear_problem* p, size_t* bytes) {
-  const gdr_status st = check(p);
+  const gdr_status st = check(p, true);
   if (st != GDR_OK) return st;
   if (!bytes) return GDR_ERR_NULL_ARG;
   *bytes = nothing(p, kUncounted) ? 0 : backward_bytes(p, kUncounted);
@@ -219,7 +221,7 @@ gdr_status gdr_linear_backward_workspace(const gdr_linear_problem* p, size_t* by
 
 gdr_status gdr_linear_backward_varlen_workspace(const gdr_linear_problem* p, int64_t rows, size_t* bytes) {
   if (rows < 0) return p ? GDR_ERR_BAD_SHAPE : GDR_ERR_NULL_ARG;
-  const gdr_status st = check(p, rows);
+  const gdr_status st = check(p, true, rows);
   if (st != GDR_OK) return st;
   if (!bytes) return GDR_ERR_NULL_ARG;
   *bytes = nothing(p, rows) ? 0 : backward_bytes(p, rows);

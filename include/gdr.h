@@ -254,9 +254,9 @@ gdr_status gdr_backward_varlen(const gdr_problem* p, const int64_t* cu_seqlens,
  * and v (0: dense), so that the three may be column ranges of one projection:
  * at least H * D, in whole 16-byte units.  Rows of a batch follow each other
  * at the same distance.  All other tensors are dense, as above.  A row, with
- * its gap, holds at most 2^22 elements; B and Hv are at most 65535, and
- * B * Hv * (2 ceil(Dk/64) + ceil(Dv/64)) at most 2^22 (else
- * GDR_ERR_UNSUPPORTED).
+ * its gap, holds at most 2^22 elements, Hv * Dk too; B and Hv are at most 65535,
+ * B * Hv * (2 ceil(Dk/64) + ceil(Dv/64)) at most 2^22, B * T, and in the VJP
+ * B * T * Hk, at most 2^31 - 1 (else GDR_ERR_UNSUPPORTED).
  *
  * Results: sums, the state and everything returned in fp32 (an fp32 o, dq,
  * dk, dv, and ht, dg, dh0 always) carry fp32 accuracy also from bf16 inputs,
@@ -338,7 +338,9 @@ gdr_status gdr_linear_backward_varlen_rows(const gdr_linear_problem* p, int64_t 
  * statistics between tokens.  weight and bias are fp32 [groups, channels], or
  * [channels] for all groups with GDR_NORM_SHARED_WEIGHT, or NULL (ones,
  * zeros).  channels is a multiple of 8 up to 512; x_row and z_row are the
- * elements between rows of x and z (0: dense; in whole 16-byte units).
+ * elements between rows of x and z (0: dense; in whole 16-byte units).  There are
+ * at most 65535 groups and 2^40 rows, and a row, with its gap, holds at most 2^22
+ * elements (else GDR_ERR_UNSUPPORTED).
  * All arithmetic is fp32, outputs are rounded once.  z together with
  * GDR_NORM_SILU is GDR_ERR_UNSUPPORTED. */
 enum { GDR_NORM_CENTER = 1u, GDR_NORM_SILU = 2u, GDR_NORM_SHARED_WEIGHT = 4u };
