@@ -105,9 +105,10 @@ def _here(dev, stream):
     return stream is None and dev.index == torch.cuda.current_device()
 
 
-# The current stream's handle, without the Stream object around it: a call for
-# one token is bound by the host.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# The current stream's handle, without the Stream object around it where torch
+# has a call for that: a call for one token is bound by the host.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _check_status(st, where):
