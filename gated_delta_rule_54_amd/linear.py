@@ -136,8 +136,10 @@ def _linear_problem(q, k, v, g, h0, out_dtype, algo, cu_seqlens, max_seqlen):
     head = g is not None and g.dim() == 1
     _want(g, "g", (Hv,) if head else rows + (Hv,), torch.float32, dev)
     B, T = rows if cu_seqlens is None else _ragged_dims(q, cu_seqlens, max_seqlen)
-    if cu_seqlens is not None and not cu_seqlens.is_contiguous():
-        raise ValueError("cu_seqlens must be contiguous")
+    if cu_seqlens is not None:
+        if not cu_seqlens.is_contiguous():
+            raise ValueError("cu_seqlens must be contiguous")
+        T = min(T, rows[1])  # no sequence is longer than the batch
     _want(h0, "h0", (B, Hv, Dk, Dv), torch.float32, dev)
     return GdrLinearProblem(B, T, Hk, Hv, Dk, Dv, _dtype(q.dtype, "q"), _dtype(out_dtype, "out_dtype"),
                             GDR_LINEAR_HEAD_DECAY if head else 0, ALGOS[algo], _row_stride(q, "q"),

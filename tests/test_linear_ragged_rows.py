@@ -133,3 +133,37 @@ def test_a_document_among_short_prompts_on_the_card():
         # fp32 sums over heads in another order; a bf16 result may then round to the next value
         tol = 2.0 ** -7 if a.dtype == BF else 2.0 ** -18
         assert ((a[:, s] - b).abs() <= tol * (b.abs() + b.abs().max())).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("algo", ["auto", "sequential", "chunked"])
+@pytest.mark.parametrize("bound", [None, 0, 1, 100])
+def test_a_batch_without_rows(algo, bound):
+    """Sequences that are all empty, whatever bound the caller keeps for them:
+    the states pass through."""
+    e = lambda *s, dt=BF: torch.zeros(s, dtype=dt, device="cuda")
+    h0, dht = torch.randn(2, 3, 4, 64, 64, device="cuda")
+    kw = dict(algo=algo, cu_seqlens=torch.zeros(4, dtype=torch.int64, device="cuda"), max_seqlen=bound)
+    for g in (None, e(4, dt=F), e(1, 0, 4, dt=F)):
+        q, v = e(1, 0, 2, 64), e(1, 0, 4, 64)
+        o, ht = gdr.gdr_linear_forward(q, q, v, g, h0, **kw)
+        assert o.shape == (1, 0, 4, 64) and torch.equal(ht, h0)
+        assert not gdr.gdr_linear_forward(q, q, v, g, **kw)[1].any()
+        got = gdr.gdr_linear_backward(q, q, v, g, h0, v, dht, **kw)
+        assert torch.equal(got[4], dht) and (got[3] is None if g is None else not got[3].any())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bound", [70, 75, 4000])
+def test_a_bound_above_the_rows(bound):
+    """No more is asked for than the rows hold: the same bits whatever bound at
+    or above the longest length is given."""
+    x = draw(44, 1, 75, 2, 4, 64, 64, state=False)
+    t = to_dev(x, BF)
+    cu = torch.tensor([0, 70, 70, 75], device="cuda")
+    runs = []
+    for b in (70, bound):
+        kw = dict(cu_seqlens=cu, max_seqlen=b)
+        runs.append(gdr.gdr_linear_forward(t["q"], t["k"], t["v"], t["g"], **kw)
+                    + gdr.gdr_linear_backward(t["q"], t["k"], t["v"], t["g"], None, t["do"], **kw))
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
