@@ -174,7 +174,8 @@ def gdr_linear_forward(q, k, v, g=None, h0=None, *, algo="auto", out_dtype=torch
 
     q, k [B, T, Hk, Dk], v [B, T, Hv, Dv]; g [B, T, Hv], [Hv] (a constant
     decay per head) or None (no decay); h0 [B, Hv, Dk, Dv] or None.  ``o`` may
-    be a tensor to write into (its dtype is the output's); ``ht`` is True
+    be a tensor to write into (its dtype is the output's, its memory none of
+    the inputs'); ``ht`` is True
     (allocate), None (not wanted) or a tensor, which may be ``h0``.
     ``cu_seqlens`` / ``max_seqlen`` as for ``gdr_forward``: rows that no
     sequence covers are left as they were."""
@@ -266,7 +267,7 @@ def gdr_group_norm_forward(x, weight=None, bias=None, z=None, *, center=False, s
     with ``silu``, else u.  ``center`` subtracts the mean (a group norm;
     without it the root mean square's).  weight and bias: float32 [groups,
     channels], or [channels] for all groups, or None.  ``y`` may be a tensor
-    to write into."""
+    to write into, of none of the inputs' memory."""
     dev = _device(x, "x")
     if not _here(dev, stream):
         with _on(dev, stream):

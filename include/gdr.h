@@ -246,8 +246,10 @@ gdr_status gdr_backward_varlen(const gdr_problem* p, const int64_t* cu_seqlens,
  * g is [B, T, Hv], or [Hv] with GDR_LINEAR_HEAD_DECAY (one constant factor
  * per head; dg is then [Hv], summed over all tokens), or NULL (alpha = 1).
  * Any g, -Inf included (the state is dropped there), is allowed; growth past
- * the fp32 range gives Inf or NaN, and with GDR_ALGO_CHUNKED so does growth of
- * more than that range over the tokens of one chunk (64).
+ * the fp32 range gives Inf or NaN.  GDR_ALGO_CHUNKED (AUTO picks it for longer
+ * sequences) splits a factor between two tokens of a chunk (64) where it crosses
+ * 16 of them: growth of up to 2^48 over any run of a chunk's tokens keeps every
+ * term; more can give Inf or NaN, or lose a term that decays in between.
  *
  * Dk and Dv are multiples of 16 up to 256, independent of each other; q_row,
  * k_row, v_row are the elements between one token's row and the next of q, k
@@ -291,7 +293,8 @@ typedef struct gdr_linear_problem {
 gdr_status gdr_linear_forward_workspace(const gdr_linear_problem* p, size_t* bytes);
 gdr_status gdr_linear_backward_workspace(const gdr_linear_problem* p, size_t* bytes);
 
-/* h0 may be NULL (zeros); ht may be NULL (not wanted) and may be h0. */
+/* h0 may be NULL (zeros); ht may be NULL (not wanted) and may be h0.  o must
+ * not alias an input. */
 gdr_status gdr_linear_forward(const gdr_linear_problem* p, const void* q, const void* k, const void* v,
                               const float* g, const float* h0, void* o, float* ht, void* ws, size_t ws_bytes,
                               void* hip_stream);
@@ -342,7 +345,7 @@ gdr_status gdr_linear_backward_varlen_rows(const gdr_linear_problem* p, int64_t 
  * at most 65535 groups and 2^40 rows, and a row, with its gap, holds at most 2^22
  * elements (else GDR_ERR_UNSUPPORTED).
  * All arithmetic is fp32, outputs are rounded once.  z together with
- * GDR_NORM_SILU is GDR_ERR_UNSUPPORTED. */
+ * GDR_NORM_SILU is GDR_ERR_UNSUPPORTED.  Outputs must not alias inputs. */
 enum { GDR_NORM_CENTER = 1u, GDR_NORM_SILU = 2u, GDR_NORM_SHARED_WEIGHT = 4u };
 
 typedef struct gdr_norm_problem {
