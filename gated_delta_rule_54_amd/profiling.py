@@ -40,7 +40,8 @@ eight SQ counters a run)
         SQ_LDS_IDX_ACTIVE SQ_VALU_MFMA_BUSY_CYCLES SQ_BUSY_CYCLES -d DIR_S2 -o s -- python3 bench.py ...
     python -m gated_delta_rule_54_amd.profiling sq DIR_S1/s_results.db DIR_S2/s_results.db --md profiles/<name>.md
 
-give each kernel's wave time split by what its waves were doing.
+give each kernel's wave time split by what its waves were doing.  ``trace`` and
+``sq`` take ``--operators`` for profiles of linear attention and the group norm.
 """
 
 import argparse
@@ -73,16 +74,34 @@ KERNELS = [
     (r"calib_copy_kernel", "calib_copy"),
     (r"calib_mfma_kernel", "calib_mfma"),
 ]
+# the operators beside the rule; a VJP's chunk kernels by the job of dq and dk,
+# whose flags are: the terms of dg, fp32 results, added to what is there
+OPERATORS = [
+    (r"lin_chunk_kernel<.*?Job<\d+, true, (?:true|false), true>", "linear_chunks_vjp_add"),
+    (r"lin_chunk_kernel<.*?Job<\d+, true,", "linear_chunks_vjp"),
+    (r"lin_chunk_kernel", "linear_chunks"),
+    (r"lin_segment_kernel", "linear_segments"),
+    (r"lin_scan_kernel", "linear_scan"),
+    (r"lin_seq_kernel", "linear_seq"),
+    (r"lin_token_kernel", "linear_token"),
+    (r"lin_group_sum_kernel", "linear_group_sum"),
+    (r"lin_dg_kernel", "linear_dg"),
+    (r"norm_fwd_kernel", "norm_fwd"),
+    (r"norm_bwd_kernel", "norm_bwd"),
+    (r"norm_params_kernel", "norm_params"),
+]
 COPY_PATTERN = r"calib_copy_kernel"
 
 
-def src_digest():
-    """Digest of the sources of the kernels that the profiles measure: those of
-    the gated delta rule, not of the operators beside it."""
+def src_digest(operators=False):
+    """Digest of the sources of the kernels that a profile measures: those of
+    the gated delta rule, or of the operators beside it with what they share
+    with it."""
     h = hashlib.sha256()
     csrc = os.path.join(_HERE, "csrc")
     for f in sorted(os.listdir(csrc)):
-        if f.startswith(("gdr_linear", "gdr_norm")):
+        beside = f.startswith(("gdr_linear", "gdr_norm"))
+        if beside != operators and not (operators and f in ("gdr_device.h", "gdr_internal.h")):
             continue
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(f.encode() + fh.read())
@@ -104,7 +123,7 @@ def per_dispatch(db, counter):
 def label(name):
     if re.search(COPY_PATTERN, name):
         return "copy"
-    for pat, lab in KERNELS:
+    for pat, lab in KERNELS + OPERATORS:
         if re.search(pat, name):
             return lab
     return None
@@ -253,7 +272,7 @@ def sq(args):
         ins = [d.get(k) for k in ("SQ_INSTS_VALU", "SQ_INSTS_LDS", "SQ_INSTS_MFMA", "SQ_INSTS_SALU")]
         row.append(" / ".join(f"{x[0] / 1e6:.1f}" if x else "-" for x in ins))
         lines.append("| " + " | ".join(row) + " |")
-    lines += ["", f"Kernel sources digest: `{src_digest()}`", ""]
+    lines += ["", f"Kernel sources digest: `{src_digest(args.operators)}`", ""]
     text = "\n".join(lines)
     if args.md:
         with open(args.md, "w") as fh:
@@ -279,20 +298,22 @@ def trace(args):
                      f"{pct:.1f} |")
     # the same launches split by grid (workgroups), so a workload's launches
     # can be told apart from other shapes of the same kernel in the command
-    acc = collections.defaultdict(lambda: [0, 0.0])
-    for name, gx, gy, gz, wx, n, tot in con.execute(
-            "select name, grid_x / workgroup_x, grid_y, grid_z, workgroup_x, count(*), sum(duration) "
+    acc = collections.defaultdict(lambda: [0, 0.0, float("inf")])
+    for name, gx, gy, gz, wx, n, tot, least in con.execute(
+            "select name, grid_x / workgroup_x, grid_y, grid_z, workgroup_x, count(*), sum(duration), min(duration) "
             "from kernels group by name, grid_x, grid_y, grid_z, workgroup_x"):
         lab = label(name)
         if lab is not None:
             a = acc[(lab, int(gx), gy, gz, wx)]
             a[0] += n
             a[1] += tot
+            a[2] = min(a[2], least)
     lines += ["", "Library kernels by launch grid (all template instances of a kernel together):", "",
-              "| library name | grid (workgroups) | threads | calls | avg us |", "|---|---|---:|---:|---:|"]
-    for (lab, gx, gy, gz, wx), (n, tot) in sorted(acc.items(), key=lambda kv: (kv[0][0], -kv[1][0])):
-        lines.append(f"| {lab} | {gx} x {gy} x {gz} | {wx} | {n} | {tot / n / 1000.0:.2f} |")
-    lines += ["", f"Kernel sources digest: `{src_digest()}`", ""]
+              "| library name | grid (workgroups) | threads | calls | avg us | least us |",
+              "|---|---|---:|---:|---:|---:|"]
+    for (lab, gx, gy, gz, wx), (n, tot, least) in sorted(acc.items(), key=lambda kv: (kv[0][0], -kv[1][0])):
+        lines.append(f"| {lab} | {gx} x {gy} x {gz} | {wx} | {n} | {tot / n / 1000.0:.2f} | {least / 1000.0:.2f} |")
+    lines += ["", f"Kernel sources digest: `{src_digest(args.operators)}`", ""]
     text = "\n".join(lines)
     if args.md:
         with open(args.md, "w") as fh:
@@ -324,6 +345,9 @@ def main():
     q.add_argument("dbs", nargs="+")
     q.add_argument("--md", default=None)
     q.add_argument("--command", default="")
+    for s in (k, q):
+        s.add_argument("--operators", action="store_true",
+                       help="the profile is of linear attention and the group norm: their sources' digest")
     args = ap.parse_args()
     {"traffic": traffic, "trace": trace, "mfma": mfma, "sq": sq}[args.cmd](args)
 
