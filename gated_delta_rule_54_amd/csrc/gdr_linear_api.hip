@@ -76,10 +76,12 @@ gdr_status done(hipError_t e) { return e == hipSuccess ? GDR_OK : gdr::record_hi
 
 // Shortest T at which AUTO takes the chunked kernels, which take as long for a
 // few tokens as for a chunk.  Token by token against chunked, us, MI355X, 32
-// heads of 128 x 128, bf16: forward, 1 sequence 6.9 : 8.2 at T = 2 and 13.8 :
-// 8.2 at 8; 8 sequences 13.4 : 17.5 at 4, 18.6 : 16.9 at 8; 64 sequences 85 :
-// 122 at 4, 130 : 126 at 8.  VJP, 8 sequences 47 : 70 at 8, 71 : 71 at 16; 64
-// sequences 333 : 531 at 8, 546 : 535 at 16; 1 sequence 22 : 19 at 8.
+// heads of 128 x 128, bf16: forward, 1 sequence 6.9 : 8.8 at T = 2 and 13.8 :
+// 8.7 at 8; 8 sequences 12.1 : 18.6 at 4, 17.8 : 18.5 at 8, 28.9 : 18.5 at 16; 64
+// sequences 95 : 129 at 4, 125 : 130 at 8, 211 : 136 at 16.  VJP, 8 sequences 45 :
+// 72 at 8, 70 : 72 at 16; 64 sequences 325 : 528 at 8, 545 : 531 at 16; 1 sequence
+// 22 : 19 at 8.  fp32, 8 sequences of 8 heads: forward 7.6 : 11.1 at 4, 11.2 : 11.1
+// at 8; VJP 19.7 : 27.4 at 8, 27.7 : 27.6 at 16.
 constexpr int64_t kAutoForwardT = 8, kAutoBackwardT = 16;
 bool chunked(const gdr_linear_problem* p, bool backward) {
   if (p->algo != GDR_ALGO_AUTO) return p->algo == GDR_ALGO_CHUNKED;

@@ -20,16 +20,18 @@
 // columns of one token.  Output waves share the work by rows (out_by_rows)
 // where H is one or two operands, by columns (out_by_columns) where it is three.
 //
-// Bound: issue.  Two waves of a SIMD take turns at the matrix cores and the
-// vector ALUs (a 16 x 16 x 32 product holds the issue of its SIMD for 16-18
-// cycles), and LDS delivers their operands: 2.8 us a chunk of 64 tokens and 64
-// columns forward, 3.5 in the VJP.  4 x 4096 tokens, 16 key and 32 value heads
-// of 128, bf16: forward 174 us (2.4 TB/s; its bytes alone 67 us), VJP
-// 683-686 us (bytes 110 us), of which dg 19 us.  Measured and set aside: 32
-// columns a wave (spills), chunks of 32 with two workgroups a compute unit, the
-// state's update after the output in the same waves (262 us forward against
-// 186), output by columns also where H is two operands (175 against 174 us; 17
-// ragged sequences 224 against 221).
+// Bound: waits.  4 x 4096 tokens, 16 key and 32 value heads of 128, bf16:
+// forward 172-197 us (its bytes alone 67 us), VJP 673-870 us (bytes 110 us), of
+// which dg 19-23: the least over the same buffers, the most within a layer.  That
+// is 2.7-3.1 us a chunk of 64 tokens and 64 columns forward, 3.5-4.8 in the VJP.
+// Counters there: the matrix cores are busy 25 % of the forward's time (22-25 %
+// of the VJP's), LDS 47 % (37-44 %), over a third of that for bank conflicts.  Of
+// a wave's time 42 % is waiting for LDS, memory or a barrier, 22 % for its turn to
+// issue, 36 % issuing: two waves on a SIMD are too few to fill any of the units.
+// Measured and set aside: 32 columns a wave (spills), chunks of 32 with two
+// workgroups a compute unit, the state's update after the output in the same waves
+// (262 us forward against 186, with one operand), output by columns also where H
+// is two operands (175 against 174 us; 17 ragged sequences 224 against 221).
 //
 // Precision.  bf16 inputs are matrix-core operands as they are.  What is
 // computed on the way (P, H, the decayed Z) is fp32: where a result is
@@ -1182,20 +1184,23 @@ hipError_t by_type(bool io_bf16, int d1, F&& f) {
 // 256 of them.  More segments fill the last round, or the only one, but cost a
 // pass that forms their states; a launch for each value head of a key head saves
 // the sum over them, but has fewer workgroups.  The plan with the
-// least estimated time is taken, from what was measured on MI355X at D = 128
-// (ns a token of a walk; smaller heads change all alike):
-//   a walk 45 (forward), 54 (VJP: 768 workgroups of 4096 tokens 664 us), and
+// least estimated time is taken, from what was measured on MI355X in bf16 at D =
+// 128 (ns a token of a walk), for all types and widths:
+//   a walk 45 (forward), 54 (VJP: 768 workgroups of 4096 tokens 654-664 us), and
 //   4 us to begin and end;
 //   the segment pass 29 with one workgroup on a compute unit, 15 more for each
 //   further one (16 segments of 2048 tokens 59 us, 32 of 1024 45 us);
 //   the scan 4 us, 0.3 us a segment and its states both ways at 4 TB/s;
 //   the sum over heads 5 us and 5.5 TB/s, a further launch 3 us.
 // What the rule chose, against the other side: VJP of 4 x 4096 tokens, 16 key
-// and 32 value heads, summed by launches 664-760 us, with the sum's pass 843;
-// of 1 x 4096 tokens, summed and in 4 segments 257-268, whole with the pass 274;
-// of 16384 tokens of 8 heads 234 in 16 segments, 334 in 11; forward of 333
-// tokens, fp32, 24 in segments of 64, 34 of 192; of 4 x 4096 tokens 182 whole,
-// 264 cut.
+// and 32 value heads, summed by launches 675-690 us, with the sum's pass 752-756;
+// of 1 x 4096 tokens, summed and in 4 segments 237-241, whole with the pass
+// 262-264; of 16384 tokens of 8 heads 235-238 in 16 segments, 274-276 in 11, 903
+// whole; forward of 333 tokens, fp32, 22 in segments of 64, 35 of 192; of 4 x 4096
+// tokens 172-176 whole, 250 cut.  Over every cut of 777 .. 16384 tokens of 4 and 8
+// heads, forward and VJP, with and without shared key heads: the one chosen takes
+// at most 1.12 times the best one's time in bf16 (D = 32, 64, 128, 256) and 1.10
+// in fp32 (64, 128).
 LinPlan lin_plan(const LinShape& s, bool backward) {
   LinPlan best{};
   double least = 0.0;
