@@ -245,7 +245,7 @@ gdr_status gdr_backward_varlen(const gdr_problem* p, const int64_t* cu_seqlens,
  *
  * g is [B, T, Hv], or [Hv] with GDR_LINEAR_HEAD_DECAY (one constant factor
  * per head; dg is then [Hv], summed over all tokens), or NULL (alpha = 1).
- * Any g, -Inf included (the state is dropped there), is allowed; growth past
+ * Any g, -Inf included (a finite state is dropped there), is allowed; growth past
  * the fp32 range gives Inf or NaN.  GDR_ALGO_CHUNKED (AUTO picks it for longer
  * sequences) splits a factor between two tokens of a chunk (64) where it crosses
  * 16 of them: growth of up to 2^48 over any run of a chunk's tokens keeps every
@@ -265,12 +265,13 @@ gdr_status gdr_backward_varlen(const gdr_problem* p, const int64_t* cu_seqlens,
  * relative to the sums of their terms' absolute values.  dg's terms are those of
  * dg_t = sum_{r >= t} (q_r . dq_r - k_r . dk_r) + <S_T, dS_T>, which cancel:
  * where a head decays strongly, dg_t is far smaller than they are, and its
- * rounding is not.  Where alpha_t is 0 in fp32, dg_t is 0.
- * bf16 outputs are rounded once from sums whose matrix-core operands hold 16
- * bits or more (24 in dq and dk where dg is wanted: asking for it can move one
- * of their values to the next bf16).  Every row past a sequence's end, and rows that no sequence
- * covers, are neither read nor written.  Inf and NaN inputs propagate; with
- * GDR_ALGO_CHUNKED they may reach earlier tokens of their chunk of 64.
+ * rounding is not.  Where alpha_t is 0 in fp32, dg_t is 0.  bf16 outputs are
+ * rounded once from sums whose matrix-core operands hold 16 bits or more (24 in
+ * dq and dk where dg is wanted: asking for it can move one of their values to the
+ * next bf16).  Every row past a sequence's end, and rows that no sequence covers,
+ * are neither read nor written.  Inf and NaN inputs propagate; with
+ * GDR_ALGO_CHUNKED an Inf may come out as NaN, and either may reach earlier tokens
+ * of its chunk of 64.
  *
  * GDR_ALGO_SEQUENTIAL runs token by token (decoding, with ht == h0 allowed);
  * its sums do not depend on how a sequence is cut into calls.
