@@ -28,7 +28,10 @@ SYMBOLS = ("gdr_keeps_chunks", "gdr_forward_workspace", "gdr_backward_workspace"
            "gdr_linear_backward", "gdr_linear_forward_varlen", "gdr_linear_backward_varlen",
            "gdr_linear_backward_varlen_workspace", "gdr_linear_backward_varlen_rows",
            "gdr_group_norm_forward", "gdr_group_norm_backward_workspace", "gdr_group_norm_backward",
-           "gdr_profile_enable", "gdr_profile_read",
+           "gdr_rotary_forward", "gdr_rotary_backward", "gdr_cache_append", "gdr_cache_append_varlen",
+           "gdr_cache_attention_workspace", "gdr_cache_attention", "gdr_attention_forward",
+           "gdr_attention_forward_varlen", "gdr_attention_backward_workspace", "gdr_attention_backward",
+           "gdr_attention_backward_varlen", "gdr_profile_enable", "gdr_profile_read",
            "gdr_status_str", "gdr_last_hip_error", "gdr_abi_version")
 # Every symbol include/gdr_calib.h declares (device ceilings for the benchmark).
 CALIB_SYMBOLS = ("gdr_calib_copy", "gdr_calib_mfma")
@@ -93,11 +96,24 @@ def lib():
         L.gdr_linear_backward_varlen_rows.argtypes = [vp, ctypes.c_int64] + [vp] * 14 + [sz, vp]
         L.gdr_group_norm_forward.argtypes = [vp] * 7
         L.gdr_group_norm_backward.argtypes = [vp] * 11 + [sz, vp]
+        L.gdr_rotary_forward.argtypes = L.gdr_rotary_backward.argtypes = [vp] * 8
+        L.gdr_cache_append.argtypes = [vp] * 12
+        L.gdr_cache_append_varlen.argtypes = [vp] * 13
+        L.gdr_cache_attention_workspace.argtypes = [vp, ctypes.POINTER(sz)]
+        L.gdr_cache_attention.argtypes = [vp] * 9 + [sz, vp]
+        L.gdr_attention_forward.argtypes = [vp] * 7
+        L.gdr_attention_forward_varlen.argtypes = [vp] * 8
+        L.gdr_attention_backward_workspace.argtypes = [vp, ctypes.c_int64, ctypes.POINTER(sz)]
+        L.gdr_attention_backward.argtypes = [vp] * 11 + [sz, vp]
+        L.gdr_attention_backward_varlen.argtypes = [vp, ctypes.c_int64] + [vp] * 11 + [sz, vp]
         for name in ("gdr_linear_forward_workspace", "gdr_linear_backward_workspace", "gdr_linear_forward",
                      "gdr_linear_backward", "gdr_linear_forward_varlen", "gdr_linear_backward_varlen",
                      "gdr_linear_backward_varlen_workspace", "gdr_linear_backward_varlen_rows",
                      "gdr_group_norm_forward", "gdr_group_norm_backward_workspace", "gdr_group_norm_backward",
-                     "gdr_keeps_chunks", "gdr_calib_copy", "gdr_calib_mfma",
+                     "gdr_rotary_forward", "gdr_rotary_backward", "gdr_cache_append", "gdr_cache_append_varlen",
+                     "gdr_cache_attention_workspace", "gdr_cache_attention", "gdr_attention_forward",
+                     "gdr_attention_forward_varlen", "gdr_attention_backward_workspace", "gdr_attention_backward",
+                     "gdr_attention_backward_varlen", "gdr_keeps_chunks", "gdr_calib_copy", "gdr_calib_mfma",
                      "gdr_forward_workspace", "gdr_backward_workspace",
                      "gdr_forward", "gdr_backward", "gdr_forward_noalloc", "gdr_forward_varlen",
                      "gdr_backward_varlen"):

@@ -93,15 +93,18 @@ OPERATORS = [
 COPY_PATTERN = r"calib_copy_kernel"
 
 
-def src_digest(operators=False):
+def src_digest(operators=False, attention=False):
     """Digest of the sources of the kernels that a profile measures: those of
-    the gated delta rule, or of the operators beside it with what they share
-    with it."""
+    the gated delta rule, of the operators beside it (linear attention and the
+    norm), or of the attention layer, the latter two with what they share with
+    it."""
     h = hashlib.sha256()
     csrc = os.path.join(_HERE, "csrc")
     for f in sorted(os.listdir(csrc)):
         beside = f.startswith(("gdr_linear", "gdr_norm"))
-        if beside != operators and not (operators and f in ("gdr_device.h", "gdr_internal.h")):
+        layer = f.startswith(("gdr_attn", "gdr_cache", "gdr_rotary"))
+        shared = (operators or attention) and f in ("gdr_device.h", "gdr_internal.h")
+        if (beside, layer) != (operators, attention) and not shared:
             continue
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(f.encode() + fh.read())

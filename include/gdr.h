@@ -371,6 +371,169 @@ gdr_status gdr_group_norm_backward(const gdr_norm_problem* p, const void* x, con
                                    const void* z, const void* dy, void* dx, void* dz, float* dweight, float* dbias,
                                    void* ws, size_t ws_bytes, void* hip_stream);
 
+/* ---------------------------------------------------------------------------
+ * The attention layer that stands beside the recurrent ones: rotary positions,
+ * a paged cache of keys and values, attention of one new token over it, and
+ * causal attention over whole sequences with its VJP.  Query head h reads
+ * key/value head h / (Hq / Hk).  Head dims D are multiples of 16 up to 256 (the
+ * same for keys and values), io is fp32 or bf16.  All sums, the softmax's
+ * statistics and angles are held in fp32 or more; outputs are rounded once.
+ *
+ * Rotary positions.  Pair i < R / 2 of a head's first R channels, (i, i + R/2)
+ * or with GDR_ROTARY_ADJACENT (2i, 2i + 1), is turned by the angle
+ * pos[axis(i)] * freq[i]:
+ *     (a, b) -> (a cos - b sin, b cos + a sin);   channels from R on stay.
+ * The angle is formed and reduced in 64 bits, so far positions keep their
+ * precision.  freq is fp32 [R / 2], pos int64 [axes, rows]: one position for
+ * each axis (time, height, width).  section[a] pairs belong to axis a, summing
+ * to R / 2: the first section[0] to axis 0, the next to axis 1 and so on; with
+ * GDR_ROTARY_CYCLED pair i belongs to axis i % axes where i < axes *
+ * section[i % axes], else to axis 0 (then axes * (section[a] - 1) + a < R / 2
+ * for a > 0).  With one axis section is not read.  R is a multiple of 16. */
+enum { GDR_ROTARY_ADJACENT = 1u, GDR_ROTARY_CYCLED = 2u };
+
+typedef struct gdr_rotary {
+  int32_t R;                   /* channels turned: 0 .. D                     */
+  int32_t axes;                /* 1 .. 4                                      */
+  int32_t section[4];          /* pairs of each axis                          */
+  uint32_t flags;              /* GDR_ROTARY_*                                */
+} gdr_rotary;
+
+typedef struct gdr_rotary_problem {
+  int64_t rows;                /* tokens                                      */
+  int32_t Hq, Hk, D;           /* heads of q and of k (Hk 0: no k)            */
+  int32_t io_dtype, out_dtype; /* gdr_dtype of q and k; of their outputs      */
+  gdr_rotary rot;
+  int64_t q_row, k_row;        /* elements between token rows; 0: dense       */
+  int64_t qo_row, ko_row;      /* the same of the outputs                     */
+} gdr_rotary_problem;
+
+/* q [rows, Hq, D] and k [rows, Hk, D] turned into q_out and k_out.  An output
+ * may be its own input (same dtype and row distance: in place) and must not
+ * overlap an input otherwise.  backward is the VJP: the outputs' gradients in,
+ * the inputs' out (the opposite turn); freq and pos have no gradients.  Rows
+ * and row distances as for gdr_linear_forward; at most 2^31 - 1 rows. */
+gdr_status gdr_rotary_forward(const gdr_rotary_problem* p, const void* q, const void* k, const int64_t* pos,
+                              const float* freq, void* q_out, void* k_out, void* hip_stream);
+gdr_status gdr_rotary_backward(const gdr_rotary_problem* p, const void* dq_out, const void* dk_out,
+                               const int64_t* pos, const float* freq, void* dq, void* dk, void* hip_stream);
+
+/* A paged cache.  Keys and values lie in two buffers of the same layout:
+ * element (page, slot, head, channel) at page * page_stride + slot *
+ * token_stride + head * head_stride + channel, no two of them in one place; all
+ * strides 0 means dense [pages, page_size, Hk, D].  Strides are whole 16-byte
+ * units, and a buffer spans less than 64 GiB.  table (device, int32, [B,
+ * max_pages], rows table_row elements apart, 0: dense) holds each sequence's
+ * pages in order: place j of a sequence is slot j % page_size of page
+ * table[b][j / page_size].  An entry outside [0, pages) is a page that is not
+ * there: nothing is stored to it, and its tokens are not visible.  lengths
+ * (device, int64 [B]) are the tokens that each sequence holds. */
+typedef struct gdr_cache {
+  int64_t pages;
+  int32_t page_size, Hk, D;
+  int32_t dtype;               /* gdr_dtype of keys and values                */
+  int64_t page_stride, token_stride, head_stride;
+  int32_t max_pages;
+  int64_t table_row;
+} gdr_cache;
+
+/* Appending.  k and v [B, T, Hk, D] are the last T tokens of sequences that
+ * hold lengths[b] tokens with them; token t gets place lengths[b] - T + t.  k
+ * is turned (rot.R > 0) and stored in the cache's dtype, v is stored; with q
+ * [B, T, Hq, D], the turned q is written to q_out (cache dtype).  pos [axes, B,
+ * T] gives the positions; NULL: each token's place (one axis only).  A token
+ * without a place (negative, or past the table) is not stored, its q is still
+ * turned.  No two tokens of a call may have one slot (two sequences must not
+ * append to one page): one of them, or a mixture, would remain.  varlen:
+ * sequence b's new tokens are rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of
+ * `rows` rows, its last ones; p->T bounds their number, tokens past it are not
+ * stored; rows that no sequence covers are neither read nor written.  B is at
+ * most 65535, B * T and rows at most 2^31 - 1. */
+typedef struct gdr_append_problem {
+  int64_t B, T;                /* sequences; new tokens of each (or a bound)  */
+  int64_t rows;                /* varlen: rows of q, k, v                     */
+  int32_t Hq;                  /* heads of q (0: no q)                        */
+  int32_t io_dtype;            /* gdr_dtype of q, k, v                        */
+  gdr_rotary rot;
+  gdr_cache cache;
+  int64_t q_row, k_row, v_row; /* elements between token rows; 0: dense       */
+} gdr_append_problem;
+
+gdr_status gdr_cache_append(const gdr_append_problem* p, const int64_t* lengths, const int32_t* table,
+                            const void* q, const void* k, const void* v, const int64_t* pos, const float* freq,
+                            void* q_out, void* k_cache, void* v_cache, void* hip_stream);
+gdr_status gdr_cache_append_varlen(const gdr_append_problem* p, const int64_t* cu_seqlens, const int64_t* lengths,
+                                   const int32_t* table, const void* q, const void* k, const void* v,
+                                   const int64_t* pos, const float* freq, void* q_out, void* k_cache,
+                                   void* v_cache, void* hip_stream);
+
+/* Attention of one new token for each sequence over the cache, the token's own
+ * key and value in it already:
+ *     o = sum_j P_j v_j,  P = softmax_j(scale q . k_j)
+ * over the places j < lengths[b] with window == 0, or lengths[b] - 1 - j <
+ * window, or j < sinks.  q [B, Hq, D] in the cache's dtype (rows q_row
+ * elements apart, 0: dense), o [B, Hq, D] in out_dtype, lse [B, Hq] fp32 the
+ * logarithm of the softmax's sum (NULL: not wanted).  A sequence without a
+ * visible token, or whose visible scores are all -Inf, gives o = 0 and lse =
+ * -Inf.  What the pages hold in places that are not visible is never used; an Inf
+ * in a visible v may come out as NaN.
+ * Lengths are read on the device; they are clamped to [0, max_len], and max_len
+ * (0: max_pages * page_size, which it may not exceed) sizes the workspace and
+ * the launch, so a captured call serves all lengths up to it.  B * Hq is at
+ * most 2^22, scale > 0, window and sinks >= 0. */
+typedef struct gdr_cache_attention_problem {
+  int64_t B;
+  int32_t Hq;
+  int32_t out_dtype;
+  gdr_cache cache;
+  int64_t q_row;
+  int64_t max_len;
+  int64_t window, sinks;       /* window 0: all tokens                        */
+  float scale;
+} gdr_cache_attention_problem;
+
+gdr_status gdr_cache_attention_workspace(const gdr_cache_attention_problem* p, size_t* bytes);
+gdr_status gdr_cache_attention(const gdr_cache_attention_problem* p, const void* q, const void* k_cache,
+                               const void* v_cache, const int32_t* table, const int64_t* lengths, void* o,
+                               float* lse, void* ws, size_t ws_bytes, void* hip_stream);
+
+/* Causal attention over whole sequences: token i sees token j of its sequence
+ * where j <= i and (window == 0, or i - j < window, or j < sinks).  q, o, dout
+ * [B, T, Hq, D], k, v [B, T, Hk, D], lse fp32 [B, T, Hq].  The VJP takes the
+ * forward's inputs and its o and lse; dk and dv are summed over the query heads
+ * that share a key head, in a fixed order.  bf16 outputs are rounded once: the
+ * probabilities (and in the VJP their gradients) enter the matrix cores as two
+ * bf16 operands, as three for fp32 outputs; fp32 io is fp32 throughout.  varlen:
+ * cu_seqlens as for gdr_forward_varlen.  NaN and Inf propagate: scores that are
+ * +Inf, or all -Inf, give NaN; an Inf in v or dout may come out as NaN, and Inf or
+ * NaN in a token's v, k, q or dout may reach tokens of its sequence that are
+ * masked from it but share a tile of 64 with ones that are not.  B and Hq are at
+ * most 65535, T at most 2^22, a row at most 2^22 elements, B * Hq * ceil(T / 128)
+ * at most 2^23, token rows at most 2^31 - 1 (else GDR_ERR_UNSUPPORTED). */
+typedef struct gdr_attention_problem {
+  int64_t B, T;
+  int32_t Hq, Hk, D;
+  int32_t io_dtype;            /* gdr_dtype of q, k, v, dout                  */
+  int32_t out_dtype;           /* gdr_dtype of o, dq, dk, dv                  */
+  int64_t window, sinks;
+  float scale;
+  int64_t q_row, k_row, v_row; /* elements between token rows; 0: dense       */
+} gdr_attention_problem;
+
+gdr_status gdr_attention_forward(const gdr_attention_problem* p, const void* q, const void* k, const void* v, void* o,
+                                 float* lse, void* hip_stream);
+gdr_status gdr_attention_forward_varlen(const gdr_attention_problem* p, const int64_t* cu_seqlens, const void* q,
+                                        const void* k, const void* v, void* o, float* lse, void* hip_stream);
+/* `rows`: token rows of q (B * T, or a ragged batch's): they size the workspace. */
+gdr_status gdr_attention_backward_workspace(const gdr_attention_problem* p, int64_t rows, size_t* bytes);
+gdr_status gdr_attention_backward(const gdr_attention_problem* p, const void* q, const void* k, const void* v,
+                                  const void* o, const float* lse, const void* dout, void* dq, void* dk, void* dv,
+                                  void* ws, size_t ws_bytes, void* hip_stream);
+gdr_status gdr_attention_backward_varlen(const gdr_attention_problem* p, int64_t rows, const int64_t* cu_seqlens,
+                                         const void* q, const void* k, const void* v, const void* o,
+                                         const float* lse, const void* dout, void* dq, void* dk, void* dv, void* ws,
+                                         size_t ws_bytes, void* hip_stream);
+
 /* Per-kernel timing for benchmarks (not for use under graph capture).
  * While enabled, every kernel that gdr_forward / gdr_backward launch from the
  * calling thread is bracketed by a pair of HIP events recorded on the call's

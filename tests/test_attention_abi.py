@@ -1,0 +1,305 @@
+"""CPU checks of the attention layer's C entry points and their binding: bad
+arguments are refused before anything reaches the GPU."""
+
+import ctypes
+
+import pytest
+import torch
+
+import gated_delta_rule_54_amd as gdr
+from gated_delta_rule_54_amd import attention as A
+from gated_delta_rule_54_amd import binding as B
+
+FAKE = 0x10000  # an aligned address that is never dereferenced
+PAST = 1 << 40
+
+
+def turn(R=32, axes=1, section=(0, 0, 0, 0), flags=0):
+    return A.GdrRotary(R, axes, (ctypes.c_int32 * 4)(*section), flags)
+
+
+def cache(**kw):
+    base = dict(pages=10, page_size=16, Hk=2, D=64, dtype=1, page_stride=0, token_stride=0, head_stride=0,
+                max_pages=4, table_row=0)
+    base.update(kw)
+    return A.GdrCache(**base)
+
+
+def rot(**kw):
+    base = dict(rows=10, Hq=4, Hk=2, D=64, io_dtype=1, out_dtype=1, rot=turn(), q_row=0, k_row=0, qo_row=0, ko_row=0)
+    base.update(kw)
+    return A.GdrRotaryProblem(**base)
+
+
+def app(**kw):
+    base = dict(B=2, T=5, rows=10, Hq=4, io_dtype=1, rot=turn(), cache=cache(), q_row=0, k_row=0, v_row=0)
+    base.update(kw)
+    return A.GdrAppendProblem(**base)
+
+
+def dec(**kw):
+    base = dict(B=2, Hq=4, out_dtype=1, cache=cache(), q_row=0, max_len=0, window=0, sinks=0, scale=0.125)
+    base.update(kw)
+    return A.GdrCacheAttentionProblem(**base)
+
+
+def att(**kw):
+    base = dict(B=2, T=100, Hq=4, Hk=2, D=64, io_dtype=1, out_dtype=1, window=0, sinks=0, scale=0.125, q_row=0,
+                k_row=0, v_row=0)
+    base.update(kw)
+    return A.GdrAttentionProblem(**base)
+
+
+def call(entry, p, args, tail=(), first=(), **over):
+    a = {n: FAKE for n in args}
+    a.update(over)
+    return getattr(B.lib(), entry)(ctypes.byref(p), *first, *a.values(), *tail, None)
+
+
+def rotary(p, back=False, **over):
+    return call("gdr_rotary_backward" if back else "gdr_rotary_forward", p, ("q", "k", "pos", "freq", "qo", "ko"),
+                **over)
+
+
+def append(p, ragged=False, **over):
+    names = ("lengths", "table", "q", "k", "v", "pos", "freq", "qo", "kc", "vc")
+    return call("gdr_cache_append" + ("_varlen" if ragged else ""), p, (("cu",) if ragged else ()) + names, **over)
+
+
+def decode(p, ws=FAKE, nws=PAST, **over):
+    return call("gdr_cache_attention", p, ("q", "kc", "vc", "table", "lengths", "o", "lse"), (ws, nws), **over)
+
+
+def fwd(p, ragged=False, **over):
+    return call("gdr_attention_forward" + ("_varlen" if ragged else ""), p,
+                (("cu",) if ragged else ()) + ("q", "k", "v", "o", "lse"), **over)
+
+
+def bwd(p, ragged=False, rows=200, ws=FAKE, nws=PAST, **over):
+    names = ("q", "k", "v", "o", "lse", "dout", "dq", "dk", "dv")
+    return call("gdr_attention_backward" + ("_varlen" if ragged else ""), p, (("cu",) if ragged else ()) + names,
+                (ws, nws), (rows,) if ragged else (), **over)
+
+
+BAD_TURNS = [
+    (turn(R=-16), 2), (turn(R=80), 2), (turn(R=24), 3), (turn(axes=0), 2), (turn(axes=5), 3), (turn(flags=4), 3),
+    (turn(axes=2, section=(8, 7, 0, 0)), 2), (turn(axes=3, section=(18, -1, -1, 0)), 2),
+    (turn(axes=2, section=(4, 12, 0, 0), flags=2), 2),
+]
+
+
+@pytest.mark.parametrize("bad,status", BAD_TURNS)
+def test_bad_turns(bad, status):
+    assert rotary(rot(rot=bad), q=None) == status and rotary(rot(rot=bad), back=True, qo=None) == status
+    assert append(app(rot=bad), k=None) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(rows=-1), 2), (dict(Hq=0), 2), (dict(Hk=-1), 2), (dict(D=0), 2), (dict(D=40), 3), (dict(D=272), 3),
+    (dict(io_dtype=2), 3), (dict(out_dtype=-1), 3), (dict(rows=1 << 31), 3), (dict(q_row=248), 2), (dict(k_row=132), 4),
+    (dict(qo_row=260), 4), (dict(ko_row=-8), 2), (dict(q_row=(1 << 22) + 8), 3), (dict(Hq=1 << 17), 3),
+])
+def test_bad_rotary(kw, status):
+    assert rotary(rot(**kw), q=None) == status and rotary(rot(**kw), back=True, ko=None) == status
+
+
+def test_rotary_arguments():
+    for name in ("q", "k", "pos", "freq", "qo", "ko"):
+        assert rotary(rot(), **{name: None}) == 1
+    for name in ("q", "k", "qo", "ko"):
+        assert rotary(rot(), **{name: FAKE + 8}) == 4
+    assert rotary(rot(), pos=FAKE + 4) == 4 and rotary(rot(), back=True, freq=FAKE + 2) == 4
+    assert rotary(rot(rows=0), q=None, k=None, pos=None, freq=None, qo=None, ko=None) == 0
+    assert B.lib().gdr_rotary_forward(None, *[FAKE] * 6, None) == 1
+
+
+BAD_CACHES = [
+    (dict(pages=-1), 2), (dict(page_size=0), 2), (dict(Hk=0), 2), (dict(D=0), 2), (dict(D=72), 3), (dict(dtype=2), 3),
+    (dict(max_pages=-1), 2), (dict(table_row=3), 2), (dict(table_row=-4), 2), (dict(pages=1 << 31), 3),
+    # layouts in which elements share a place, or lie at odd ones
+    (dict(page_stride=2048, token_stride=128, head_stride=32), 2), (dict(page_stride=2048, token_stride=64, head_stride=64), 2),
+    (dict(page_stride=1024, token_stride=128, head_stride=64), 2), (dict(page_stride=0, token_stride=128, head_stride=64), 2),
+    (dict(page_stride=-2048, token_stride=128, head_stride=64), 2),
+    (dict(page_stride=2052, token_stride=128, head_stride=64), 4), (dict(page_stride=4096, token_stride=132, head_stride=64), 4),
+    (dict(pages=1 << 26), 3), (dict(pages=10, page_stride=1 << 60, token_stride=128, head_stride=64), 3),
+]
+
+
+@pytest.mark.parametrize("kw,status", BAD_CACHES)
+def test_bad_caches(kw, status):
+    c = cache(**kw)
+    assert append(app(cache=c), k=None) == status and append(app(cache=c), ragged=True, k=None) == status
+    assert decode(dec(cache=c), q=None) == status
+
+
+def test_cache_layouts():
+    for kw in (dict(page_stride=2048, token_stride=64, head_stride=1024),       # head by head
+               dict(page_stride=4096, token_stride=128, head_stride=64),        # keys and values in one page
+               dict(page_stride=128, token_stride=1280, head_stride=64),        # slot by slot
+               dict(pages=0), dict(pages=1, page_stride=8, token_stride=128, head_stride=64)):
+        assert decode(dec(B=0, cache=cache(**kw)), q=None) == 0, kw
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(B=-1), 2), (dict(T=-1), 2), (dict(Hq=-1), 2), (dict(io_dtype=3), 3), (dict(B=70000), 3),
+    (dict(B=60000, T=60000), 3), (dict(q_row=248), 2), (dict(k_row=124), 2), (dict(v_row=132), 4),
+])
+def test_bad_append(kw, status):
+    assert append(app(**kw), k=None) == status
+    if "B" not in kw or "T" not in kw:
+        assert append(app(**kw), ragged=True, k=None) == status
+
+
+def test_append_arguments():
+    for name in ("lengths", "table", "q", "k", "v", "freq", "qo", "kc", "vc"):
+        assert append(app(), **{name: None}) == 1 and append(app(), ragged=True, **{name: None}) == 1
+    assert append(app(), ragged=True, cu=None) == 1
+    assert append(app(rows=-1), ragged=True) == 2 and append(app(rows=1 << 31), ragged=True) == 3
+    assert append(app(rot=turn(axes=2, section=(8, 8, 0, 0))), pos=None) == 1
+    for name in ("q", "k", "v", "qo", "kc", "vc"):
+        assert append(app(), **{name: FAKE + 8}) == 4
+    for name, off in (("lengths", 4), ("table", 2), ("pos", 4), ("freq", 2)):
+        assert append(app(), **{name: FAKE + off}) == 4
+    assert append(app(), ragged=True, cu=FAKE + 4) == 4
+    none = dict.fromkeys(("lengths", "table", "q", "k", "v", "freq", "qo", "kc", "vc"))
+    assert append(app(B=0), **none) == 0 and append(app(T=0), **none) == 0
+    assert append(app(rows=0), ragged=True, cu=None, **none) == 0
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(B=-1), 2), (dict(Hq=0), 2), (dict(Hq=3), 2), (dict(max_len=-1), 2), (dict(max_len=65), 2),
+    (dict(window=-1), 2), (dict(sinks=-1), 2), (dict(scale=0.0), 2), (dict(scale=-1.0), 2),
+    (dict(scale=float("nan")), 2), (dict(scale=float("inf")), 2), (dict(out_dtype=2), 3), (dict(B=70000), 3),
+    (dict(B=60000, Hq=128), 3), (dict(q_row=248), 2), (dict(q_row=260), 4),
+])
+def test_bad_cache_attention(kw, status):
+    n = ctypes.c_size_t(12345)
+    assert B.lib().gdr_cache_attention_workspace(ctypes.byref(dec(**kw)), ctypes.byref(n)) == status
+    assert n.value == 12345
+    assert decode(dec(**kw), q=None) == status
+
+
+def test_cache_attention_arguments():
+    for name in ("q", "kc", "vc", "table", "lengths", "o"):
+        assert decode(dec(), **{name: None}) == 1
+    for name in ("q", "kc", "vc", "o"):
+        assert decode(dec(), **{name: FAKE + 8}) == 4
+    for name, off in (("table", 2), ("lengths", 4), ("lse", 2), ):
+        assert decode(dec(), **{name: FAKE + off}) == 4
+    assert decode(dec(), ws=FAKE + 16) == 4
+    assert decode(dec(B=0), q=None, o=None, lengths=None, table=None, kc=None, vc=None) == 0
+    big = dec(B=1, cache=cache(max_pages=1000, pages=1000))
+    n = ctypes.c_size_t(0)
+    assert B.lib().gdr_cache_attention_workspace(ctypes.byref(big), ctypes.byref(n)) == 0
+    assert n.value > 0 and n.value % 256 == 0
+    assert decode(big, ws=None, nws=0) == 1 and decode(big, nws=n.value - 1) == 5
+    assert B.lib().gdr_cache_attention_workspace(ctypes.byref(big), None) == 1
+    assert B.lib().gdr_cache_attention(None, *[FAKE] * 8, 0, None) == 1
+    # bounds past every length do not size the workspace
+    m = ctypes.c_size_t(0)
+    far = dec(B=1, window=1 << 62, sinks=1 << 62, cache=cache(max_pages=1000, pages=1000))
+    assert B.lib().gdr_cache_attention_workspace(ctypes.byref(far), ctypes.byref(m)) == 0 and m.value == n.value
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(B=-1), 2), (dict(T=-1), 2), (dict(Hq=0), 2), (dict(Hk=0), 2), (dict(Hq=3), 2), (dict(D=0), 2),
+    (dict(D=24), 3), (dict(D=288), 3), (dict(io_dtype=2), 3), (dict(out_dtype=2), 3), (dict(window=-1), 2),
+    (dict(sinks=-1), 2), (dict(scale=0.0), 2), (dict(scale=float("nan")), 2), (dict(scale=float("inf")), 2),
+    (dict(q_row=248), 2), (dict(k_row=132), 4), (dict(v_row=(1 << 22) + 8), 3), (dict(B=70000), 3),
+    (dict(T=(1 << 22) + 1), 3), (dict(B=1 << 62, T=1 << 62), 3), (dict(B=2048, Hq=64, T=16384), 3),
+    (dict(Hq=70000, Hk=70000), 3),
+])
+def test_bad_attention(kw, status):
+    p = att(**kw)
+    n = ctypes.c_size_t(12345)
+    assert B.lib().gdr_attention_backward_workspace(ctypes.byref(p), 200, ctypes.byref(n)) == status
+    assert n.value == 12345
+    for ragged in (False, True):
+        assert fwd(p, ragged, q=None) == status and bwd(p, ragged, dq=None) == status
+
+
+def test_attention_arguments():
+    for ragged in (False, True):
+        for name in ("q", "k", "v", "o", "lse"):
+            assert fwd(att(), ragged, **{name: None}) == 1
+        for name in ("q", "k", "v", "o", "lse", "dout", "dq", "dk", "dv"):
+            assert bwd(att(), ragged, **{name: None}) == 1
+        for name in ("q", "k", "v", "o"):
+            assert fwd(att(), ragged, **{name: FAKE + 8}) == 4
+        for name in ("q", "o", "dout", "dq", "dv"):
+            assert bwd(att(), ragged, **{name: FAKE + 8}) == 4
+        assert fwd(att(), ragged, lse=FAKE + 2) == 4 and bwd(att(), ragged, ws=FAKE + 16) == 4
+        assert fwd(att(B=0), ragged, q=None) == 0 and fwd(att(T=0), ragged, q=None) == 0
+        assert bwd(att(T=0), ragged, ws=None, nws=0, dq=None) == 0
+    assert fwd(att(), True, cu=None) == 1 and bwd(att(), True, cu=None) == 1 and fwd(att(), True, cu=FAKE + 4) == 4
+    assert bwd(att(), True, rows=-1) == 2 and bwd(att(), True, rows=1 << 31) == 3
+    assert bwd(att(), True, rows=0, q=None, ws=None, nws=0) == 0
+    n = ctypes.c_size_t(0)
+    assert B.lib().gdr_attention_backward_workspace(ctypes.byref(att()), 200, ctypes.byref(n)) == 0
+    assert n.value >= 200 * 4 * 4 and n.value % 256 == 0
+    assert bwd(att(), ws=None, nws=0) == 1 and bwd(att(), nws=n.value - 1) == 5
+    assert B.lib().gdr_attention_backward_workspace(ctypes.byref(att()), 200, None) == 1
+    assert B.lib().gdr_attention_forward(None, *[FAKE] * 5, None) == 1
+
+
+def test_ragged_workspace_follows_the_rows():
+    """One long sequence among short ones: the workspace holds the rows, not the
+    longest length for each sequence."""
+    p = att(B=64, T=32768, Hq=32, Hk=8, D=128, window=1024, sinks=4)
+    n, m = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    assert B.lib().gdr_attention_backward_workspace(ctypes.byref(p), 32768 + 63 * 100, ctypes.byref(n)) == 0
+    assert B.lib().gdr_attention_backward_workspace(ctypes.byref(p), 64 * 32768, ctypes.byref(m)) == 0
+    assert n.value < 1 << 30 and m.value > n.value
+
+
+def test_binding_refuses_host_tensors():
+    x, i, t = torch.zeros(1, 2, 2, 64), torch.zeros(1, 2, dtype=torch.int64), torch.zeros(1, 4, dtype=torch.int32)
+    for make in (lambda: gdr.gdr_rotary_forward(x, x, i, torch.zeros(32)),
+                 lambda: gdr.gdr_rotary_backward(x, x, i, torch.zeros(32)),
+                 lambda: gdr.gdr_cache_append(x, x, x, x, t, i[0, :1]),
+                 lambda: gdr.gdr_cache_attention(x, x, x, t, i[0, :1]),
+                 lambda: gdr.gdr_attention_forward(x, x, x),
+                 lambda: gdr.gdr_attention_backward(x, x, x, x, x[..., 0], x)):
+        with pytest.raises(ValueError, match="device tensor"):
+            make()
+
+
+def test_window_and_sinks():
+    assert A._span(None, 0) == 0 and A._span(5, 2) == 5
+    for bad in ((0, 0), (-3, 0), (None, -1)):
+        with pytest.raises(ValueError):
+            A._span(*bad)
+
+
+def test_cache_views():
+    dev = torch.device("cpu")
+    table, lengths = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int64)
+    kv = torch.zeros(10, 2, 16, 3, 64)
+    c = A._cache(kv[:, 0], kv[:, 1], table, lengths, dev)
+    assert (c.page_stride, c.token_stride, c.head_stride) == (2 * 16 * 192, 192, 64)
+    c = A._cache(*(torch.zeros(10, 3, 16, 64).transpose(1, 2) for _ in "kv"), table[:, :3], lengths, dev)
+    assert (c.page_stride, c.token_stride, c.head_stride, c.max_pages, c.table_row) == (3 * 1024, 64, 1024, 3, 4)
+    k = torch.zeros(10, 16, 3, 64)
+    for bad in ((k, k.transpose(1, 2).contiguous().transpose(1, 2), table, lengths),   # unlike strides
+                (k.expand(10, 16, 3, 64)[:1].expand(10, 16, 3, 64),) * 2 + (table, lengths),
+                (k, k[:9], table, lengths), (k, k, table.t(), lengths), (k, k, table, lengths[:1]),
+                (k, k, table[:1].expand(2, 4), lengths), (k[0], k[0], table, lengths)):
+        with pytest.raises(ValueError):
+            A._cache(*bad, dev)
+    for bad in ((k, k.double(), table, lengths), (k, k, table.long(), lengths), (k, k, table, lengths.int())):
+        with pytest.raises(TypeError):
+            A._cache(*bad, dev)
+
+
+def test_sections():
+    dev = torch.device("cpu")
+    freq = torch.zeros(16)
+    r = A._rotary(freq, (8, 4, 4), True, True, dev)
+    assert (r.R, r.axes, list(r.section), r.flags) == (32, 3, [8, 4, 4, 0], 3)
+    for bad in ((8, 4), (), (4,) * 5):
+        with pytest.raises(ValueError):
+            A._rotary(freq, bad, False, False, dev)
+    with pytest.raises(ValueError, match="shape"):
+        A._positions(torch.zeros(2, 5, dtype=torch.int64), r, (5,), dev)
+    with pytest.raises(TypeError):
+        A._positions(torch.zeros(5, dtype=torch.int32), A._rotary(freq, None, False, False, dev), (5,), dev)

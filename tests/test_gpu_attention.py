@@ -1,0 +1,324 @@
+"""Causal windowed attention and its VJP on the GPU, against the float64
+definitions of oracle/attention_oracle.py.
+
+Tolerances, u = 2^-24, t = 2^-16 where outputs are bf16 (two operands) and u where
+they are fp32.  A score, a sum of D products, is off by 2 D u of the sum A of
+their absolute values (a product and its addition); it, the maximum and lse are
+scaled and subtracted, 4 u of their sizes; the exponential rounds to 4 u.  So a
+weight is off by r = 2 D u A + 4 u (|s| + |m|) + 4 u of itself.
+  o    (2 r + (2 n + 16) u + t) sum P |v|           n: keys of the row
+  lse  r + (2 n + 8) u + u |lse|                     = e
+In the VJP P is off by p = r + e of itself.  delta is a sum of D products of dout
+and o, which has the forward's error (a bf16 o: 2^-8 of its value): d = sum |dout|
+(err o) + 2 D u sum |dout o|; dout . v is off by 2 D u of its absolute sum B.
+  dS   P (p |dP - delta| + 2 D u B + d + 4 u (B + |delta|))   = s
+  dv   sum over rows of P |dout| (p + (2 m + 8) u + t)         m: rows summed
+  dk   scale sum over rows of (s + ((2 m + 8) u + t) |dS|) |q|,  dq likewise over keys.
+A bf16 output adds 2^-8 of its value.  A rounding's errors are independent: in the
+2-norm a bf16 result is no further off than 2^-8 / sqrt(3), the rounding's
+deviation where every value has the least mantissa, and 5 % for what else there is
+(one bf16 operand for P or dS would double the square)."""
+
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_54_amd as gdr
+from gated_delta_rule_54_amd.synth import round_bf16
+from oracle import attention_oracle as ao
+from tests.test_gpu_rotary import BF, F, U, dev, host
+
+pytestmark = pytest.mark.gpu
+
+
+def draw(seed, T, Hq, Hk, D, io=F):
+    r = np.random.default_rng(seed)
+    x = [r.standard_normal(s).astype(np.float32) for s in ((T, Hq, D), (T, Hk, D), (T, Hk, D), (T, Hq, D))]
+    return [round_bf16(a) for a in x] if io == BF else x
+
+
+def bounds(q, k, v, do, o, scale, window, sinks, out):
+    """(o, lse, dq, dk, dv) and their tolerances; o: the kernel's (for the VJP)."""
+    T, Hq, D = q.shape
+    G = Hq // k.shape[1]
+    t = 2.0 ** -16 if out == BF else U
+    ok = ao.seen(T, window, sinks)
+    q, k, v, do = (x.astype(np.float64) for x in (q, k, v, do))
+    res = {n: np.zeros(s) for n, s in (("o", q.shape), ("lse", q.shape[:2]), ("dq", q.shape), ("dk", k.shape), ("dv", k.shape))}
+    tol = {n: np.zeros_like(x) for n, x in res.items()}
+    n = ok.sum(1)
+    m = ok.sum(0)[:, None] * G
+    for h in range(Hq):
+        g = h // G
+        S = np.where(ok, scale * q[:, h] @ k[:, g].T, -np.inf)
+        A = np.where(ok, scale * np.abs(q[:, h]) @ np.abs(k[:, g]).T, 0)
+        top = S.max(1, keepdims=True)
+        e = np.exp(S - top)
+        P = e / e.sum(1, keepdims=True)
+        lse = (top + np.log(e.sum(1, keepdims=True)))[:, 0]
+        Sz = np.where(ok, S, 0)
+        r = 2 * D * U * A.max(1) + 4 * U * (np.abs(Sz).max(1) + np.abs(top[:, 0])) + 4 * U
+        res["o"][:, h], res["lse"][:, h] = P @ v[:, g], lse
+        tol["o"][:, h] = (2 * r + (2 * n + 16) * U + t)[:, None] * (P @ np.abs(v[:, g]))
+        tol["lse"][:, h] = r + (2 * n + 8) * U + U * np.abs(lse)
+        dP, B = do[:, h] @ v[:, g].T, np.abs(do[:, h]) @ np.abs(v[:, g]).T
+        delta = np.sum(P * dP, 1, keepdims=True)
+        dS = P * (dP - delta)
+        err_o = np.abs(o[:, h] - res["o"][:, h])
+        d = np.sum(np.abs(do[:, h]) * err_o + 2 * D * U * np.abs(do[:, h] * res["o"][:, h]), 1)[:, None]
+        p = (2 * r + tol["lse"][:, h])[:, None]
+        s = P * (p * np.abs(dP - delta) + 2 * D * U * B + d + 4 * U * (B + np.abs(delta)))
+        res["dq"][:, h] = scale * dS @ k[:, g]
+        tol["dq"][:, h] = scale * (s + ((2 * n[:, None] + 8) * U + t) * np.abs(dS)) @ np.abs(k[:, g])
+        res["dk"][:, g] += scale * dS.T @ q[:, h]
+        tol["dk"][:, g] += scale * (s.T + ((2 * m + 8) * U + t) * np.abs(dS).T) @ np.abs(q[:, h])
+        res["dv"][:, g] += P.T @ do[:, h]
+        tol["dv"][:, g] += (P * p).T @ np.abs(do[:, h]) + ((2 * m + 8) * U + t) * (P.T @ np.abs(do[:, h]))
+    return res, tol
+
+
+def close(name, got, ref, tol, out, norm=True):
+    rnd = 2.0 ** -8 if out == BF and name != "lse" else 0.0
+    err = np.abs(got - ref)
+    assert got.shape == ref.shape
+    worst = float(np.max(err / (tol + rnd * (np.abs(ref) + tol) + 1e-37), initial=0.0))
+    assert worst <= 1.0, (name, worst)
+    if rnd and norm and ref.size >= 512:
+        assert np.linalg.norm(err) <= 1.05 * 2.0 ** -8 / np.sqrt(3) * np.linalg.norm(ref), name
+
+
+def check(T, Hq, Hk, D, io=BF, out=F, window=None, sinks=0, scale=None, seed=1, B=1, back=True):
+    x = [draw(seed + b, T, Hq, Hk, D, io) for b in range(B)]
+    q, k, v, do = (dev(np.stack([a[i] for a in x]), io) for i in range(4))
+    how = dict(window=window, sinks=sinks, scale=scale)
+    o, lse = gdr.gdr_attention_forward(q, k, v, out_dtype=out, **how)
+    got = {"o": o, "lse": lse}
+    if back:
+        got.update(zip(("dq", "dk", "dv"), gdr.gdr_attention_backward(q, k, v, o, lse, do, **how)))
+    assert all(t.dtype == (F if n == "lse" else out) for n, t in got.items())
+    for b in range(B):
+        res, tol = bounds(*x[b], host(o[b]), D ** -0.5 if scale is None else scale, window, sinks, out)
+        for n, t in got.items():
+            close(n, host(t[b]), res[n], tol[n], out)
+
+
+@pytest.mark.parametrize("T", [1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 200, 257])
+@pytest.mark.parametrize("io", [BF, F])
+def test_lengths(T, io):
+    check(T, 2, 1, 64, io=io)
+
+
+@pytest.mark.parametrize("D", [16, 48, 64, 80, 112, 128, 144, 192, 256])
+@pytest.mark.parametrize("io,out", [(BF, F), (BF, BF), (F, F), (F, BF)])
+def test_widths_and_types(D, io, out):
+    check(150, 2, 1, D, io=io, out=out)
+
+
+@pytest.mark.parametrize("Hq,Hk", [(1, 1), (3, 3), (8, 2), (7, 1), (6, 2), (16, 16)])
+@pytest.mark.parametrize("io", [BF, F])
+def test_head_groups(Hq, Hk, io):
+    check(140, Hq, Hk, 32, io=io, B=2)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 0), (31, 3), (32, 0), (33, 64), (64, 65), (100, 129), (128, 4),
+                                          (129, 0), (299, 2), (300, 1), (1000, 3), (5, 1000), (10, 290)])
+@pytest.mark.parametrize("io", [BF, F])
+def test_windows(window, sinks, io):
+    check(300, 4, 2, 64, io=io, window=window, sinks=sinks)
+
+
+def test_long():
+    check(1100, 2, 1, 128, out=BF)
+    check(1500, 4, 2, 64, out=BF, window=200, sinks=5)
+    check(1024, 2, 2, 256, out=BF, window=512)
+
+
+def test_scales():
+    check(200, 2, 1, 64, scale=1.0, out=BF)
+    check(200, 2, 1, 64, scale=0.01)
+    check(200, 2, 1, 64, io=F, scale=2.0, window=70, sinks=2)
+
+
+@pytest.mark.parametrize("io", [BF, F])
+def test_strided_rows(io):
+    """Column ranges of one projection's rows, NaN around them."""
+    x = draw(3, 170, 4, 2, 64, io)
+    row = torch.full((1, 170, 4 + 2 + 2 + 3, 64), float("nan"), device="cuda", dtype=io)
+    row[0, :, 1:5], row[0, :, 6:8], row[0, :, 8:10] = (dev(a, io) for a in x[:3])
+    q, k, v = row[:, :, 1:5], row[:, :, 6:8], row[:, :, 8:10]
+    dense = [dev(a, io)[None] for a in x]
+    o, lse = gdr.gdr_attention_forward(q, k, v, window=90, sinks=3)
+    ro, rl = gdr.gdr_attention_forward(*dense[:3], window=90, sinks=3)
+    assert torch.equal(o, ro) and torch.equal(lse, rl)
+    for a, b in zip(gdr.gdr_attention_backward(q, k, v, o, lse, dense[3], window=90, sinks=3),
+                    gdr.gdr_attention_backward(*dense[:3], ro, rl, dense[3], window=90, sinks=3)):
+        assert torch.equal(a, b)
+
+
+LENS = [0, 5, 129, 1, 0, 300, 64, 128]
+
+
+@pytest.mark.parametrize("io,out", [(BF, BF), (F, F), (BF, F)])
+@pytest.mark.parametrize("window,sinks", [(None, 0), (50, 3), (20, 140)])
+@pytest.mark.parametrize("front,behind", [(0, 0), (3, 70)])
+def test_ragged(io, out, window, sinks, front, behind):
+    """Each sequence is what it is alone; rows that none covers hold NaN and stay
+    as they were."""
+    x = [draw(20 + i, n, 4, 2, 64, io) for i, n in enumerate(LENS)]
+    cu = front + np.concatenate([[0], np.cumsum(LENS)])
+    rows = int(cu[-1]) + behind
+    t = []
+    for i, H in enumerate((4, 2, 2, 4)):
+        a = torch.full((1, rows, H, 64), float("nan"), device="cuda", dtype=io)
+        a[0, front:int(cu[-1])] = dev(np.concatenate([y[i] for y in x]), io)
+        t.append(a)
+    how = dict(window=window, sinks=sinks, cu_seqlens=dev(cu, torch.int64))
+    o = torch.full((1, rows, 4, 64), 7.0, device="cuda", dtype=out)
+    got, lse = gdr.gdr_attention_forward(*t[:3], o=o, **how)
+    assert got is o and torch.all(o[0, :front] == 7) and torch.all(o[0, int(cu[-1]):] == 7)
+    grads = gdr.gdr_attention_backward(*t[:3], o, lse, t[3], max_seqlen=None if front else 300, **how)
+    for i, n in enumerate(LENS):
+        if not n:
+            continue
+        s = slice(int(cu[i]), int(cu[i + 1]))
+        res, tol = bounds(*x[i], host(o[0, s]), 0.125, window, sinks, out)
+        for name, g in zip(("o", "lse", "dq", "dk", "dv"), (o, lse) + grads):
+            close(name, host(g[0, s]), res[name], tol[name], out, norm=False)
+
+
+def test_ragged_rows_past_the_bound_stay():
+    """A bound below a length: the tokens past it are neither read nor written."""
+    q, k, v, do = (dev(a)[None] for a in draw(4, 100, 2, 1, 32))
+    cu = dev([0, 60, 100], torch.int64)
+    o = torch.full_like(q, 7.0)
+    gdr.gdr_attention_forward(q, k, v, o=o, cu_seqlens=cu, max_seqlen=40)
+    assert torch.all(o[0, 40:60] == 7) and not torch.any(o[0, :40] == 7) and not torch.any(o[0, 60:] == 7)
+    ro, _ = gdr.gdr_attention_forward(q[:, :40].contiguous(), k[:, :40].contiguous(), v[:, :40].contiguous())
+    assert torch.equal(o[:, :40], ro)
+
+
+def test_empty():
+    q = torch.zeros(2, 0, 4, 64, device="cuda")
+    k = torch.zeros(2, 0, 2, 64, device="cuda")
+    o, lse = gdr.gdr_attention_forward(q, k, k)
+    assert o.shape == q.shape and lse.shape == (2, 0, 4)
+    assert [g.shape for g in gdr.gdr_attention_backward(q, k, k, o, lse, q)] == [q.shape, k.shape, k.shape]
+    q, k = torch.zeros(1, 5, 4, 64, device="cuda"), torch.zeros(1, 5, 2, 64, device="cuda")
+    cu = torch.zeros(4, dtype=torch.int64, device="cuda")
+    o = torch.full_like(q, 7.0)
+    _, lse = gdr.gdr_attention_forward(q, k, k, o=o, cu_seqlens=cu)
+    gdr.gdr_attention_backward(q, k, k, o, lse, q, cu_seqlens=cu)
+    assert torch.all(o == 7)
+
+
+@pytest.mark.parametrize("io", [BF, F])
+def test_same_bits_twice_replayed_and_elsewhere(io):
+    """Twice, on another stream and from a graph whose inputs change between
+    replays: forward and VJP, with parts that are joined."""
+    q, k, v, do = (dev(a, io)[None] for a in draw(5, 700, 4, 2, 64, io))
+    how = dict(window=130, sinks=5)
+
+    def step(stream=None):
+        o, lse = gdr.gdr_attention_forward(q, k, v, stream=stream, **how)
+        return (o, lse) + gdr.gdr_attention_backward(q, k, v, o, lse, do, stream=stream, **how)
+
+    one = step()
+    assert all(torch.equal(a, b) for a, b in zip(one, step()))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other = step(s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(one, other))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        res = step()
+    for i in range(4):
+        for t in (q, k, v, do):
+            t.copy_(torch.randn_like(t.float()).to(io))
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(res, step()))
+
+
+def test_two_streams_at_once():
+    sets = [[dev(a, BF)[None] for a in draw(40 + i, 900 - 100 * i, 4, 2, 64, BF)] for i in range(2)]
+
+    def step(t, stream):
+        o, lse = gdr.gdr_attention_forward(*t[:3], window=100, sinks=2, stream=stream)
+        return (o, lse) + gdr.gdr_attention_backward(*t[:3], o, lse, t[3], window=100, sinks=2, stream=stream)
+
+    want = [step(t, None) for t in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(4):
+        for i in range(2):
+            got[i].append(step(sets[i], streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for res in got[i] for a, b in zip(res, want[i]))
+
+
+def test_not_a_number_stays_in_its_head_and_sequence():
+    q, k, v, do = (dev(np.stack([a, a])) for a in draw(6, 150, 4, 2, 32))
+    v[1, 100, 1, 3] = float("nan")
+    q[0, 20, 0, 0] = float("nan")
+    o, lse = gdr.gdr_attention_forward(q, k, v)
+    bad = torch.isnan(o)
+    assert bad[1, 100:, 2:, 3].all() and bad[0, 20, 0].all()
+    bad[1, 64:, 2:, 3] = False   # tokens before it in its tile of keys
+    bad[0, 20, 0] = False
+    assert not bad.any()
+    dq, dk, dv = gdr.gdr_attention_backward(q, k, v, o, lse, do)
+    assert not torch.isnan(dq[0, :, 1:]).any() and not torch.isnan(dq[1, :, :2]).any()
+    assert not torch.isnan(dk[0, :, 1]).any() and not torch.isnan(dv[1, :, 0]).any()
+
+
+def test_gradients_against_differences():
+    """Directional differences of <dout, o> in fp32: the forward is off by no more
+    than its tolerance at both ends."""
+    x = draw(7, 90, 4, 2, 32)
+    how = dict(window=40, sinks=2)
+    t = [dev(a)[None] for a in x]
+    o, lse = gdr.gdr_attention_forward(*t[:3], **how)
+    grads = gdr.gdr_attention_backward(*t[:3], o, lse, t[3], **how)
+    eps = 2.0 ** -7
+    for i in range(3):
+        d = np.random.default_rng(8 + i).standard_normal(x[i].shape).astype(np.float32)
+        ends, off = [], 0.0
+        for sign in (1, -1):
+            y = [a.copy() for a in x]
+            y[i] = (y[i] + sign * eps * d).astype(np.float32)
+            got = host(gdr.gdr_attention_forward(*(dev(a)[None] for a in y[:3]), **how)[0][0])
+            res, tol = bounds(*y, got, 32 ** -0.5, 40, 2, F)
+            ends.append(np.sum(got * x[3]))
+            off += np.sum(tol["o"] * np.abs(x[3]))
+        slope = (ends[0] - ends[1]) / (2 * eps)
+        # the third derivative's share, from differences of half the step in 64 bits
+        def far(e):
+            y = [a.astype(np.float64) for a in x]
+            y[i] = y[i] + e * d
+            return np.sum(ao.attention(*y[:3], 32 ** -0.5, 40, 2)[0] * x[3])
+        cubic = abs((far(eps) - far(-eps)) / (2 * eps) - (far(eps / 16) - far(-eps / 16)) * 8 / eps)
+        want = np.sum(host(grads[i][0]) * d)
+        assert abs(slope - want) <= off / (2 * eps) + 1.1 * cubic + 1e-4 * abs(want)
+
+
+def test_refusals():
+    q, k, v, do = (dev(a, BF)[None] for a in draw(9, 50, 4, 2, 64, BF))
+    o, lse = gdr.gdr_attention_forward(q, k, v, out_dtype=BF)
+    f, b = gdr.gdr_attention_forward, gdr.gdr_attention_backward
+    for bad in (lambda: f(q[0], k[0], v[0]), lambda: f(q, k[:, :49], v), lambda: f(q, k, v[..., :32]), lambda: f(q, k, v, window=0),
+                lambda: f(q, k, v, sinks=-1), lambda: f(q, k, v, o=o[:, :40]), lambda: f(q, k.cpu(), v),
+                lambda: f(q[:, :1].expand(1, 50, 4, 64), k, v), lambda: b(q, k, v, o, lse[:, :49], do),
+                lambda: b(q, k, v, o, lse, do[:, :49]), lambda: b(q, k, v, o[:, :49], lse, do),
+                lambda: f(q, k, v, cu_seqlens=torch.tensor([0, 60], device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: f(q, k.float(), v), lambda: f(q, k, v, out_dtype=torch.float16), lambda: b(q, k, v, o, lse, do.float()),
+                lambda: b(q, k, v, o, lse.double(), do), lambda: f(q, k, v, cu_seqlens=torch.tensor([0, 50], device="cuda").int())):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: f(q[:, :, :3], k, v), lambda: f(q, k, v, scale=0.0), lambda: f(q[..., :24].contiguous(), *[t[..., :24].contiguous() for t in (k, v)])):
+        with pytest.raises(gdr.GdrError):
+            bad()
