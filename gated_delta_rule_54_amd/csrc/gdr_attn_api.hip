@@ -21,6 +21,7 @@ int per16(int32_t dtype) { return dtype == GDR_BF16 ? 8 : 4; }
 gdr_status done(hipError_t e) { return e == hipSuccess ? GDR_OK : gdr::record_hip_error(e); }
 
 constexpr int64_t kMaxRows = 0x7fffffffLL;
+constexpr int64_t kMaxLen = int64_t(1) << 30;  // tokens of a sequence in a cache
 
 // A row distance: 0 (dense), or at least the row, in whole 16-byte units; 64 rows
 // of it lie within 2^30 bytes, which 32-bit offsets reach.
@@ -177,6 +178,8 @@ gdr_status check(const gdr_cache_attention_problem* p) {
   if (p->Hq % c.Hk || !(p->scale > 0.f) || std::isinf(p->scale)) return GDR_ERR_BAD_SHAPE;
   if (p->max_len > static_cast<int64_t>(c.max_pages) * c.page_size) return GDR_ERR_BAD_SHAPE;
   if (!known(p->out_dtype) || p->B > 65535 || p->Hq > 65535 || p->B * p->Hq > (1 << 22)) return GDR_ERR_UNSUPPORTED;
+  if (p->max_len > kMaxLen || (!p->max_len && static_cast<int64_t>(c.max_pages) * c.page_size > kMaxLen))
+    return GDR_ERR_UNSUPPORTED;
   return check_row(p->q_row, static_cast<int64_t>(p->Hq) * c.D, c.dtype);
 }
 gdr::CacheAttnArgs args_of(const gdr_cache_attention_problem* p, const int32_t* table, const int64_t* lengths) {
