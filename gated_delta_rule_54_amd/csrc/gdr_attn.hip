@@ -27,6 +27,7 @@
 // as coarse as the output itself.  fp32 inputs use fp32 products.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "gdr_attn.h"
 #include "gdr_device.h"
@@ -43,8 +44,18 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kHeld = 32, kWaves = 4, kBlock = kHeld * kWaves;  // held rows of a wave, of a workgroup
+constexpr int64_t kWideFrom = 256;
 
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 63; }
+
+// What is the same in a whole wave, kept in scalar registers: the compiler does not
+// see it through 64-bit arithmetic, and would load from a buffer lane by lane.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  const uint32_t lo = uniform(static_cast<int>(x)), hi = uniform(static_cast<int>(x >> 32));
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+__device__ __forceinline__ int wave_id() { return uniform(static_cast<int>(threadIdx.x >> 6)); }
 
 // Element types: PER elements in 16 bytes, TILE rows walked at a time.
 template <typename T> struct El;
@@ -55,53 +66,61 @@ template <> struct El<float> {
   static constexpr int PER = 4, TILE = 32;
 };
 
-// A tile of ROWS x DP in LDS.  Unit u (16 bytes) of a row lies at u ^ mix(row):
-// rows read together by a wave's 16-lane groups fall on different banks.
-template <typename T, int DP> struct Tile {
-  static constexpr int PER = El<T>::PER, ROWS = El<T>::TILE, UNITS = DP / PER, KF = UNITS / 2;
-  static constexpr int BYTES = ROWS * DP * sizeof(T), LOADS = ROWS * UNITS / 256;
+// Tiles of ROWS x DP of two tensors in LDS, BUFS times.  Unit u (16 bytes) of a row
+// lies at u ^ mix(row): rows read together by a wave's 16-lane groups fall on
+// different banks.
+template <typename T_, int DP_, int ROWS_ = El<T_>::TILE, int BUFS_ = 2> struct Tile {
+  using T = T_;
+  static constexpr int DP = DP_, ROWS = ROWS_, BUFS = BUFS_;
+  static constexpr int PER = El<T>::PER, UNITS = DP / PER, KF = UNITS / 2, PITCH = UNITS * 16;
+  static constexpr int BYTES = ROWS * PITCH, PAIR = 2 * BYTES, LOADS = ROWS * UNITS / 256;
   static __device__ __forceinline__ int mix(int row) {
     return UNITS == 8 ? ((row >> 1 & 1) << 2 | (row >> 2 & 3)) : ((row & 3) << 2 | (row >> 2 & 3));
   }
-  static __device__ __forceinline__ int at(int row, int unit) { return row * UNITS * 16 + ((unit ^ mix(row)) << 4); }
+  static __device__ __forceinline__ int at(int row, int unit) { return row * PITCH + ((unit ^ mix(row)) << 4); }
 };
+
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+constexpr uint32_t kNowhere = 0x7fffffffu;  // an offset past any buffer's end
 
 // Rows of a tensor [.., rows, heads, D] for one sequence and head.
 struct Rows {
   const char* base;     // the sequence's first row, the head's first channel
-  int64_t pitch;        // bytes between rows
-  int64_t n;            // rows of the sequence
+  uint32_t pitch;       // bytes between rows
+  int n, bytes;         // rows of the sequence; bytes of a row
+  // Rows row0 .. row0 + count - 1 as a buffer: what lies past the sequence's end
+  // reads as zero.
+  __device__ __forceinline__ rsrc_t buffer(int row0, int count) const {
+    const int left = max(0, min(n - row0, count));
+    const int64_t at = uniform(reinterpret_cast<int64_t>(base) + static_cast<int64_t>(min(row0, n)) * pitch);
+    const int size = uniform(left ? (left - 1) * static_cast<int>(pitch) + bytes : 0);
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(at), 0, size, 0x00020000);
+  }
 };
 template <typename T>
-__device__ __forceinline__ Rows rows_of(const void* p, int64_t start, int64_t n, int64_t row, int head, int D) {
+__device__ __forceinline__ Rows rows_of(const void* p, int64_t start, int n, int64_t row, int head, int D) {
   return {static_cast<const char*>(p) + (start * row + static_cast<int64_t>(head) * D) * sizeof(T),
-          row * static_cast<int64_t>(sizeof(T)), n};
-}
-
-typedef __amdgpu_buffer_rsrc_t rsrc_t;
-// Rows row0 .. row0 + count - 1 as a buffer: what lies past the sequence's end
-// reads as zero.
-__device__ __forceinline__ rsrc_t buffer(const Rows& r, int64_t row0, int count, int bytes) {
-  const int64_t left = max(int64_t(0), min(r.n - row0, static_cast<int64_t>(count)));
-  const int64_t first = min(row0, r.n);
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(r.base) + first * r.pitch, 0,
-                                           left ? static_cast<int>((left - 1) * r.pitch + bytes) : 0, 0x00020000);
+          static_cast<uint32_t>(row * sizeof(T)), n, D * static_cast<int>(sizeof(T))};
 }
 __device__ __forceinline__ u32x4 load16(rsrc_t b, uint32_t at) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, static_cast<int>(at), 0, 0));
 }
 
-// A tile on its way to LDS through registers.
-template <typename T, int DP> struct Staged {
-  using L = Tile<T, DP>;
+// A tile on its way to LDS through registers; the offsets are formed once.
+template <typename L> struct Staged {
   u32x4 x[L::LOADS];
-  __device__ __forceinline__ void load(const Rows& r, int64_t row0, int D) {
-    const rsrc_t b = buffer(r, row0, L::ROWS, D * static_cast<int>(sizeof(T)));
+  uint32_t from[L::LOADS];
+  __device__ __forceinline__ void init(const Rows& r) {
 #pragma unroll
     for (int i = 0; i < L::LOADS; ++i) {
       const int idx = threadIdx.x + 256 * i, row = idx / L::UNITS, u = idx % L::UNITS;
-      x[i] = load16(b, u * L::PER < D ? static_cast<uint32_t>(row * r.pitch + u * 16) : 0x7fffffffu);
+      from[i] = u * 16 < r.bytes ? row * r.pitch + u * 16 : kNowhere;
     }
+  }
+  __device__ __forceinline__ void load(const Rows& r, int row0) {
+    const rsrc_t b = r.buffer(row0, L::ROWS);
+#pragma unroll
+    for (int i = 0; i < L::LOADS; ++i) x[i] = load16(b, from[i]);
   }
   __device__ __forceinline__ void store(char* lds) const {
 #pragma unroll
@@ -113,14 +132,13 @@ template <typename T, int DP> struct Staged {
 };
 
 // A wave's held rows as the second operand: lane (row lane % 32, units 2 i + lane / 32).
-template <typename T, int DP>
-__device__ __forceinline__ void load_held(const Rows& r, int64_t row0, int D, u32x4 (&f)[Tile<T, DP>::KF]) {
-  using L = Tile<T, DP>;
-  const rsrc_t b = buffer(r, row0, kHeld, D * static_cast<int>(sizeof(T)));
+template <typename L>
+__device__ __forceinline__ void load_held(const Rows& r, int row0, u32x4 (&f)[L::KF]) {
+  const rsrc_t b = r.buffer(row0, kHeld);
   const int row = lane_id() & 31, h = lane_id() >> 5;
 #pragma unroll
   for (int i = 0; i < L::KF; ++i)
-    f[i] = load16(b, (2 * i + h) * L::PER < D ? static_cast<uint32_t>(row * r.pitch + (2 * i + h) * 16) : 0x7fffffffu);
+    f[i] = load16(b, (2 * i + h) * 16 < r.bytes ? row * r.pitch + (2 * i + h) * 16 : kNowhere);
 }
 
 template <typename T>
@@ -143,19 +161,47 @@ __device__ __forceinline__ f32x16 zero16() {
   return z;
 }
 
+// A lane's places in a tile, formed once: of by_rows' units, and of by_columns' runs
+// of 4 channels (rows 4 h .. + 3, and 8 rows on).  Units 16 apart lie 256 bytes
+// apart, rows 16 apart 16 rows: constants of the reads.  flip() goes to the other
+// buffer.
+template <typename L> struct Lane {
+  static constexpr int NR = L::KF < 8 ? L::KF : 8, NC = L::PER == 4 ? 0 : L::DP / 32 < 4 ? L::DP / 32 : 4;
+  int row[NR], col[NC ? NC : 1][2], one;
+  __device__ __forceinline__ Lane(int row0) {
+    const int lane = lane_id(), h = lane >> 5, q = lane & 15, side = lane >> 4 & 1;
+    one = row0 * L::PITCH;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) row[i] = one + L::at(lane & 31, 2 * i + h);
+#pragma unroll
+    for (int t = 0; t < NC; ++t)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        col[t][k] = one + L::at(4 * h + (q >> 2) + 8 * k, 4 * t + 2 * side + (q >> 1 & 1)) + (q & 1) * 8;
+  }
+  __device__ __forceinline__ void flip() {
+    if constexpr (L::BUFS == 1) return;
+    one ^= L::PAIR;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) row[i] ^= L::PAIR;
+#pragma unroll
+    for (int t = 0; t < NC; ++t) col[t][0] ^= L::PAIR, col[t][1] ^= L::PAIR;
+  }
+};
+
 // (rows row0 .. + 31 of the tile) x (held rows): lane (held row lane % 32) holds
 // tile rows row0 + 8 (i / 4) + 4 (lane / 32) + i % 4.
-template <typename T, int DP>
-__device__ __forceinline__ f32x16 by_rows(const char* lds, int row0, const u32x4 (&held)[Tile<T, DP>::KF]) {
-  using L = Tile<T, DP>;
-  const int row = lane_id() & 31, h = lane_id() >> 5;
+template <typename L>
+__device__ __forceinline__ f32x16 by_rows(const Lane<L>& at, const char* lds, int row0, const u32x4 (&held)[L::KF]) {
   f32x16 c = zero16();
 #pragma unroll
   for (int i = 0; i < L::KF; ++i)
-    c = mma<T>(*reinterpret_cast<const u32x4*>(lds + row0 * L::UNITS * 16 + L::at(row, 2 * i + h)), held[i], c);
+    c = mma<typename L::T>(*reinterpret_cast<const u32x4*>(lds + at.row[i & 7] + (row0 * L::PITCH + (i >> 3) * 256)),
+                           held[i], c);
   return c;
 }
-__device__ __forceinline__ int walked(int i) { return 8 * (i >> 2) + 4 * (lane_id() >> 5) + (i & 3); }
+// Of element i, the tile row less 4 (lane / 32).
+__device__ constexpr int walked(int i) { return 8 * (i >> 2) + (i & 3); }
 
 // NP bf16 parts of eight values, most significant first.
 template <int NP>
@@ -173,28 +219,25 @@ __device__ __forceinline__ void split(const float* p, bf16x8 (&out)[NP]) {
 }
 
 // acc[t] += (channels 32 t .. + 31 of tile rows row0 .. + 31)^T x p, p as by_rows
-// gives it: lane (held row) then has channels 32 t + walked(i).  With MORE, more
-// += the same of y, as one bf16 operand.
-template <typename T, int DP, int NP, bool MORE = false>
-__device__ __forceinline__ void by_columns(f32x16 (&acc)[DP / 32], const char* lds, int row0, const float (&p)[16],
-                                           f32x16* more = nullptr, const float* y = nullptr) {
-  using L = Tile<T, DP>;
-  const int lane = lane_id(), h = lane >> 5;
-  if constexpr (sizeof(T) == 2) {
-    const int q = lane & 15, side = lane >> 4 & 1;
+// gives it: lane (held row) then has channels 32 t + 4 (lane / 32) + walked(i).  With
+// MORE, more += the same of y, as one bf16 operand.
+template <typename L, int NP, bool MORE = false>
+__device__ __forceinline__ void by_columns(f32x16 (&acc)[L::DP / 32], const Lane<L>& at, const char* lds, int row0,
+                                           const float (&p)[16], f32x16* more = nullptr, const float* y = nullptr) {
+  constexpr int NT = L::DP / 32;
+  if constexpr (L::PER == 8) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       bf16x8 f[NP], g[1];
       split<NP>(p + 8 * k, f);
       if constexpr (MORE) split<1>(y + 8 * k, g);
 #pragma unroll
-      for (int t = 0; t < DP / 32; ++t) {
-        const int unit = 4 * t + 2 * side + (q >> 1 & 1), row = 4 * h + (q >> 2);
-        const char* at = lds + (row0 + 16 * k) * L::UNITS * 16 + (q & 1) * 8;
+      for (int t = 0; t < NT; ++t) {
+        const char* from = lds + ((row0 + 16 * k) * L::PITCH + (t >> 2) * 256);
         const bf16x4 a = __builtin_bit_cast(
-            bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + L::at(row, unit))));
+            bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(from + at.col[t & 3][0])));
         const bf16x4 b = __builtin_bit_cast(
-            bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + L::at(row + 8, unit))));
+            bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(from + at.col[t & 3][1])));
         const bf16x8 x{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 #pragma unroll
         for (int n = NP - 1; n >= 0; --n)
@@ -203,131 +246,189 @@ __device__ __forceinline__ void by_columns(f32x16 (&acc)[DP / 32], const char* l
       }
     }
   } else {
-    const int d = lane & 31;
+    const int d = lane_id() & 31, h = lane_id() >> 5;
 #pragma unroll
     for (int i = 0; i < 16; ++i)
 #pragma unroll
-      for (int t = 0; t < DP / 32; ++t) {
-        const float x = *reinterpret_cast<const float*>(lds + row0 * L::UNITS * 16 + L::at(walked(i), 8 * t + (d >> 2)) +
-                                                        (d & 3) * 4);
+      for (int t = 0; t < NT; ++t) {
+        const int r = walked(i) + 4 * h;
+        const float x = *reinterpret_cast<const float*>(
+            lds + at.one + row0 * L::PITCH + r * L::PITCH + (((8 * t + (d >> 2)) ^ L::mix(r)) << 4) + (d & 3) * 4);
         acc[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(x, p[i], acc[t], 0, 0, 0);
         if constexpr (MORE) more[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(x, y[i], more[t], 0, 0, 0);
       }
   }
 }
 
+// Four results; bf16 by the conversion instruction (to nearest, ties to even).
+template <typename TO>
+__device__ __forceinline__ void store4(TO* at, const float (&x)[4]) {
+  if constexpr (sizeof(TO) == 2) {
+    *reinterpret_cast<bf16x4*>(at) = bf16x4{static_cast<__bf16>(x[0]), static_cast<__bf16>(x[1]),
+                                            static_cast<__bf16>(x[2]), static_cast<__bf16>(x[3])};
+  } else {
+    st4<TO>(at, x);
+  }
+}
+
 // A wave's held rows, channels 32 t + walked(i) each, times f, to rows of `out`.
-template <typename TO, int DP>
-__device__ __forceinline__ void store_held(TO* out, int64_t pitch, const f32x16 (&acc)[DP / 32], float f, int D) {
+template <typename TO, int NT>
+__device__ __forceinline__ void store_held(TO* out, int64_t pitch, const f32x16 (&acc)[NT], float f, int D) {
   TO* at = out + static_cast<int64_t>(lane_id() & 31) * pitch + 4 * (lane_id() >> 5);
 #pragma unroll
-  for (int t = 0; t < DP / 32; ++t)
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       if (32 * t + 8 * b + 4 * (lane_id() >> 5) >= D) continue;
       const float x[4] = {acc[t][4 * b] * f, acc[t][4 * b + 1] * f, acc[t][4 * b + 2] * f, acc[t][4 * b + 3] * f};
-      st4<TO>(at + 32 * t + 8 * b, x);
+      store4<TO>(at + 32 * t + 8 * b, x);
     }
 }
 
 // A sequence of the batch: its first row and its length.
 struct Span {
-  int64_t start, n;
+  int64_t start;
+  int n;
 };
 __device__ __forceinline__ Span span(const AttnArgs& a, int64_t b) {
-  if (!a.cu) return {b * a.T, a.T};
+  if (!a.cu) return {b * a.T, static_cast<int>(a.T)};
   const int64_t lo = a.cu[b];
-  return {lo, max(int64_t(0), min(a.cu[b + 1] - lo, a.T))};
+  return {lo, static_cast<int>(max(int64_t(0), min(a.cu[b + 1] - lo, a.T)))};
 }
 
 // Visible: j <= i and (no window, or i - j < window, or j < sinks).
 struct Mask {
-  int64_t window, sinks;
-  __device__ __forceinline__ bool sees(int64_t i, int64_t j) const {
+  int window, sinks;
+  __device__ __forceinline__ Mask(const AttnArgs& a) : window(static_cast<int>(a.window)), sinks(static_cast<int>(a.sinks)) {}
+  __device__ __forceinline__ bool sees(int i, int j) const {
     return j <= i && (window == 0 || i - j < window || j < sinks);
   }
   // all pairs of i0 .. i1 and j0 .. j1; none of them
-  __device__ __forceinline__ bool all(int64_t i0, int64_t i1, int64_t j0, int64_t j1) const {
+  __device__ __forceinline__ bool all(int i0, int i1, int j0, int j1) const {
     return j1 <= i0 && (window == 0 || i1 - j0 < window || j1 < sinks);
   }
-  __device__ __forceinline__ bool none(int64_t i0, int64_t i1, int64_t j0, int64_t j1) const {
+  __device__ __forceinline__ bool none(int i0, int i1, int j0, int j1) const {
     return j0 > i1 || (window != 0 && i0 - j1 >= window && j0 >= sinks);
   }
 };
+// Keeps what follows in a branch: the compiler would mask every tile, not the few
+// that need it.
+__device__ __forceinline__ void rarely() { asm volatile(""); }
 
 // Key tiles that queries q0 .. q1 see, as a list: sinks, then the window.
 struct KeyTiles {
-  int64_t head, skip, count;
-  __device__ __forceinline__ KeyTiles(const Mask& m, int64_t q0, int64_t q1, int tile) {
-    const int64_t first = m.window == 0 ? 0 : max(int64_t(0), q0 - m.window + 1) / tile;
+  int head, skip, count;
+  __device__ __forceinline__ KeyTiles(const Mask& m, int q0, int q1, int tile) {
+    const int first = m.window == 0 ? 0 : max(0, q0 - m.window + 1) / tile;
     head = m.window == 0 ? 0 : min((m.sinks + tile - 1) / tile, first);
     skip = first - head;
     count = q1 / tile + 1 - skip;
   }
-  __device__ __forceinline__ int64_t operator[](int64_t i) const { return i < head ? i : i + skip; }
+  __device__ __forceinline__ int operator[](int i) const { return i < head ? i : i + skip; }
 };
 
-template <typename T, typename TO, int DP, int NP>
-__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_fwd_kernel(AttnArgs a) {
-  using L = Tile<T, DP>;
-  __shared__ __align__(16) char lk[2][L::BYTES];
-  __shared__ __align__(16) char lv[2][L::BYTES];
-  const int h = blockIdx.x, kh = h / (a.Hq / a.Hk), lane = lane_id(), wave = threadIdx.x >> 6;
-  const Span s = span(a, blockIdx.z);
-  const int64_t block0 = static_cast<int64_t>(gridDim.y - 1 - blockIdx.y) * kBlock;  // long rows first
-  if (block0 >= s.n) return;
-  const Mask mask{a.window, a.sinks};
-  const int64_t block1 = min(block0 + kBlock, s.n) - 1;
-  const KeyTiles tiles(mask, block0, block1, L::ROWS);
-  const Rows kr = rows_of<T>(a.k, s.start, s.n, a.k_row, kh, a.D);
-  const Rows vr = rows_of<T>(a.v, s.start, s.n, a.v_row, kh, a.D);
-  const int64_t q0 = block0 + wave * kHeld, q1 = q0 + kHeld - 1, qi = q0 + (lane & 31);
-  u32x4 qf[L::KF];
-  load_held<T, DP>(rows_of<T>(a.q, s.start, s.n, a.q_row, h, a.D), q0, a.D, qf);
-  f32x16 acc[DP / 32];
+// The layout of the kernels that hold queries.  WIDE: each wave holds 32 queries of
+// its own and walks all rows of a tile.  Otherwise all four hold the same 32, and
+// each takes 32 rows of a tile of 128, for grids that do not fill the card: four
+// times the workgroups, each a quarter as long, joined at its end.
+template <typename T, int DP, bool WIDE>
+using QTile = Tile<T, DP, WIDE ? El<T>::TILE : 128, WIDE || 512 * DP * sizeof(T) <= (128 << 10) ? 2 : 1>;
+
+// What the waves of a workgroup hold of the same queries, added: wave w is left with
+// the sums of channels 32 t, t = w, w + 4, ..
+template <int NT>
+__device__ __forceinline__ void add_waves(f32x16 (&acc)[NT], char* lds) {
+  float* at = reinterpret_cast<float*>(lds) + lane_id();
+  const int wave = wave_id();
 #pragma unroll
-  for (int t = 0; t < DP / 32; ++t) acc[t] = zero16();
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) at[((wave * NT + t) * 16 + i) * 64] = acc[t][i];
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    if (t % kWaves != wave) continue;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float x = at[(t * 16 + i) * 64];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) x += at[((w * NT + t) * 16 + i) * 64];
+      acc[t][i] = x;
+    }
+  }
+}
+template <typename TO, int NT>
+__device__ __forceinline__ void store_own(TO* out, int64_t pitch, const f32x16 (&acc)[NT], float f, int D) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+    if (t % kWaves == wave_id()) {
+      const f32x16 one[1] = {acc[t]};
+      store_held<TO, 1>(out + 32 * t, pitch, one, f, D - 32 * t);
+    }
+}
+
+template <typename T, typename TO, int DP, int NP, bool WIDE>
+__global__ __launch_bounds__(256, WIDE && DP <= 128 ? 2 : 1) void attn_fwd_kernel(AttnArgs a) {
+  using L = QTile<T, DP, WIDE>;
+  constexpr int NT = DP / 32, BLOCK = WIDE ? kBlock : kHeld, SUB = WIDE ? L::ROWS / 32 : 1;
+  __shared__ __align__(16) char lds[L::BUFS * L::PAIR];
+  __shared__ float stat[WIDE ? 1 : kWaves][2][32];
+  const int h = blockIdx.x, kh = h / (a.Hq / a.Hk), lane = lane_id(), wave = wave_id();
+  const Span s = span(a, blockIdx.z);
+  const int block0 = static_cast<int>(gridDim.y - 1 - blockIdx.y) * BLOCK;  // long rows first
+  if (block0 >= s.n) return;
+  const Mask mask(a);
+  const KeyTiles tiles(mask, block0, min(block0 + BLOCK, s.n) - 1, L::ROWS);
+  const Rows kr = rows_of<T>(a.k, s.start, s.n, a.k_row, kh, a.D), vr = rows_of<T>(a.v, s.start, s.n, a.v_row, kh, a.D);
+  const int q0 = block0 + (WIDE ? wave * kHeld : 0), q1 = q0 + kHeld - 1, qi = q0 + (lane & 31);
+  const int mine0 = WIDE ? 0 : 32 * wave;  // the wave's rows of a tile
+  Staged<L> ks, vs;
+  ks.init(kr), vs.init(vr);
+  ks.load(kr, tiles[0] * L::ROWS), vs.load(vr, tiles[0] * L::ROWS);
+  u32x4 qf[L::KF];
+  load_held<L>(rows_of<T>(a.q, s.start, s.n, a.q_row, h, a.D), q0, qf);
+  f32x16 acc[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) acc[t] = zero16();
   float m = -INFINITY, l = 0.f;
   const float c2 = a.scale * kLog2e;
-
-  Staged<T, DP> ks, vs;
-  ks.load(kr, tiles[0] * L::ROWS, a.D);
-  vs.load(vr, tiles[0] * L::ROWS, a.D);
-  ks.store(lk[0]);
-  vs.store(lv[0]);
-  for (int64_t it = 0; it < tiles.count; ++it) {
-    const int buf = it & 1;
+  const int count = uniform(tiles.count);
+  Lane<L> at(mine0);
+  int fill = 0;  // where the next tile goes
+  ks.store(lds), vs.store(lds + L::BYTES);
+  for (int it = 0; it < count; ++it) {
     __syncthreads();
-    const bool more = it + 1 < tiles.count;
-    if (more) {
-      ks.load(kr, tiles[it + 1] * L::ROWS, a.D);
-      vs.load(vr, tiles[it + 1] * L::ROWS, a.D);
-    }
-    const int64_t j0 = tiles[it] * L::ROWS;
-    if (!mask.none(q0, q1, j0, j0 + L::ROWS - 1)) {
-      constexpr int SUB = L::ROWS / 32;
+    if (it + 1 < count) ks.load(kr, tiles[it + 1] * L::ROWS), vs.load(vr, tiles[it + 1] * L::ROWS);
+    if constexpr (L::BUFS == 2) fill ^= L::PAIR;
+    const int j0 = tiles[it] * L::ROWS + mine0, j1 = j0 + 32 * SUB - 1;
+    if (!mask.none(q0, q1, j0, j1)) {
       float x[SUB][16];
-      float top = -INFINITY;
-      const bool all = mask.all(q0, q1, j0, j0 + L::ROWS - 1);
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
-        const f32x16 c = by_rows<T, DP>(lk[buf], 32 * u, qf);
+        const f32x16 c = by_rows<L>(at, lds, 32 * u, qf);
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[u][i] = c[i];
-        if (!all)
+      }
+      if (!mask.all(q0, q1, j0, j1)) {
+        rarely();
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (!mask.sees(qi, j0 + 32 * u + walked(i))) x[u][i] = -INFINITY;
+            if (!mask.sees(qi, j0 + 4 * (lane >> 5) + 32 * u + walked(i))) x[u][i] = -INFINITY;
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, x[u][i]);
-      }
       top = fmaxf(top, __shfl_xor(top, 32, 64));
       if (__any(top > m)) {
         top = fmaxf(top, m);
         const float f = m == -INFINITY ? 0.f : exp2f((m - top) * c2);
         l *= f;
 #pragma unroll
-        for (int t = 0; t < DP / 32; ++t) acc[t] *= f;
+        for (int t = 0; t < NT; ++t) acc[t] *= f;
         m = top;
       }
       const float mc = m == -INFINITY ? 0.f : m * c2;
@@ -338,19 +439,40 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_fwd_kernel(AttnAr
           x[u][i] = __builtin_amdgcn_exp2f(fmaf(x[u][i], c2, -mc));
           l += x[u][i];
         }
-        by_columns<T, DP, NP>(acc, lv[buf], 32 * u, x[u]);
+        by_columns<L, NP>(acc, at, lds + L::BYTES, 32 * u, x[u]);
       }
     }
-    if (more) {
-      ks.store(lk[buf ^ 1]);
-      vs.store(lv[buf ^ 1]);
-    }
+    if constexpr (L::BUFS == 1) __syncthreads();
+    if (it + 1 < count) ks.store(lds + fill), vs.store(lds + fill + L::BYTES);
+    at.flip();
   }
   l += __shfl_xor(l, 32, 64);
-  if (qi >= s.n) return;
   const int64_t pitch = static_cast<int64_t>(a.Hq) * a.D;
-  store_held<TO, DP>(static_cast<TO*>(a.o) + (s.start + q0) * pitch + static_cast<int64_t>(h) * a.D, pitch, acc,
-                     1.f / l, a.D);
+  TO* out = static_cast<TO*>(a.o) + (s.start + q0) * pitch + static_cast<int64_t>(h) * a.D;
+  if constexpr (!WIDE) {
+    if (lane < 32) stat[wave][0][lane] = m, stat[wave][1][lane] = l;
+    __syncthreads();  // also: the tiles are read
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stat[w][0][lane & 31]);
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float mw = stat[w][0][lane & 31];
+      l += stat[w][1][lane & 31] * (mw == -INFINITY ? 0.f : exp2f((mw - top) * c2));
+    }
+    const float f = m == -INFINITY ? 0.f : exp2f((m - top) * c2);
+    m = top;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t] *= f;
+    add_waves(acc, lds);
+    if (qi >= s.n) return;
+    store_own<TO, NT>(out, pitch, acc, 1.f / l, a.D);
+    if (wave > 0) return;
+  } else {
+    if (qi >= s.n) return;
+    store_held<TO, NT>(out, pitch, acc, 1.f / l, a.D);
+  }
   if (lane < 32) a.lse[(s.start + qi) * a.Hq + h] = fmaf(m, a.scale, log2f(l) * kLn2);
 }
 
@@ -361,27 +483,29 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_fwd_kernel(AttnAr
 // dS over the keys, which is 0 for the right delta, is what delta is off by (e):
 // dQ has e (P K) taken off (K^T is in registers for dS; one bf16 operand for P is
 // enough, as e is small), and the delta that is passed on has e added.
-template <typename T, typename TO, int DP, int NP>
+template <typename T, typename TO, int DP, int NP, bool WIDE>
 __global__ __launch_bounds__(256, 1) void attn_dq_kernel(AttnArgs a) {
-  using L = Tile<T, DP>;
-  __shared__ __align__(16) char lk[L::BYTES];
-  __shared__ __align__(16) char lv[L::BYTES];
-  const int h = blockIdx.x, kh = h / (a.Hq / a.Hk), lane = lane_id(), wave = threadIdx.x >> 6;
+  using L = QTile<T, DP, WIDE>;
+  constexpr int NT = DP / 32, BLOCK = WIDE ? kBlock : kHeld, SUB = WIDE ? L::ROWS / 32 : 1;
+  constexpr bool FIX = sizeof(TO) == 2;
+  __shared__ __align__(16) char lds[L::BUFS * L::PAIR];
+  __shared__ float stat[WIDE ? 1 : kWaves][32];
+  const int h = blockIdx.x, kh = h / (a.Hq / a.Hk), lane = lane_id(), wave = wave_id();
   const Span s = span(a, blockIdx.z);
-  const int64_t block0 = static_cast<int64_t>(gridDim.y - 1 - blockIdx.y) * kBlock;
+  const int block0 = static_cast<int>(gridDim.y - 1 - blockIdx.y) * BLOCK;
   if (block0 >= s.n) return;
-  const Mask mask{a.window, a.sinks};
-  const KeyTiles tiles(mask, block0, min(block0 + kBlock, s.n) - 1, L::ROWS);
-  const Rows kr = rows_of<T>(a.k, s.start, s.n, a.k_row, kh, a.D);
-  const Rows vr = rows_of<T>(a.v, s.start, s.n, a.v_row, kh, a.D);
-  const int64_t q0 = block0 + wave * kHeld, q1 = q0 + kHeld - 1, qi = q0 + (lane & 31);
+  const Mask mask(a);
+  const KeyTiles tiles(mask, block0, min(block0 + BLOCK, s.n) - 1, L::ROWS);
+  const Rows kr = rows_of<T>(a.k, s.start, s.n, a.k_row, kh, a.D), vr = rows_of<T>(a.v, s.start, s.n, a.v_row, kh, a.D);
+  const int q0 = block0 + (WIDE ? wave * kHeld : 0), q1 = q0 + kHeld - 1, qi = q0 + (lane & 31);
+  const int mine0 = WIDE ? 0 : 32 * wave;
   const int64_t pitch = static_cast<int64_t>(a.Hq) * a.D;
-  Staged<T, DP> ks, vs;
-  ks.load(kr, tiles[0] * L::ROWS, a.D);
-  vs.load(vr, tiles[0] * L::ROWS, a.D);
+  Staged<L> ks, vs;
+  ks.init(kr), vs.init(vr);
+  ks.load(kr, tiles[0] * L::ROWS), vs.load(vr, tiles[0] * L::ROWS);
   u32x4 qf[L::KF], df[L::KF];
-  load_held<T, DP>(rows_of<T>(a.q, s.start, s.n, a.q_row, h, a.D), q0, a.D, qf);
-  load_held<T, DP>(rows_of<T>(a.dout, s.start, s.n, pitch, h, a.D), q0, a.D, df);
+  load_held<L>(rows_of<T>(a.q, s.start, s.n, a.q_row, h, a.D), q0, qf);
+  load_held<L>(rows_of<T>(a.dout, s.start, s.n, pitch, h, a.D), q0, df);
   float lse2 = 0.f, delta = 0.f;
   if (qi < s.n) {
     lse2 = a.lse_in[(s.start + qi) * a.Hq + h] * kLog2e;
@@ -405,243 +529,419 @@ __global__ __launch_bounds__(256, 1) void attn_dq_kernel(AttnArgs a) {
     }
   }
   delta += __shfl_xor(delta, 32, 64);
-  constexpr bool FIX = sizeof(TO) == 2;
-  f32x16 acc[DP / 32], pk[FIX ? DP / 32 : 1];
+  f32x16 acc[NT], pk[FIX ? NT : 1];
 #pragma unroll
-  for (int t = 0; t < DP / 32; ++t) {
+  for (int t = 0; t < NT; ++t) {
     acc[t] = zero16();
     if constexpr (FIX) pk[t] = zero16();
   }
   float off = 0.f;
   const float c2 = a.scale * kLog2e;
-  for (int64_t it = 0; it < tiles.count; ++it) {
-    ks.store(lk);
-    vs.store(lv);
+  const int count = uniform(tiles.count);
+  Lane<L> at(mine0);
+  int fill = 0;
+  ks.store(lds), vs.store(lds + L::BYTES);
+  for (int it = 0; it < count; ++it) {
     __syncthreads();
-    if (it + 1 < tiles.count) {
-      ks.load(kr, tiles[it + 1] * L::ROWS, a.D);
-      vs.load(vr, tiles[it + 1] * L::ROWS, a.D);
-    }
+    if (it + 1 < count) ks.load(kr, tiles[it + 1] * L::ROWS), vs.load(vr, tiles[it + 1] * L::ROWS);
+    if constexpr (L::BUFS == 2) fill ^= L::PAIR;
+    const int j0 = tiles[it] * L::ROWS + mine0;
+    const bool all = mask.all(q0, q1, j0, j0 + 32 * SUB - 1);
 #pragma unroll
-    for (int u = 0; u < L::ROWS / 32; ++u) {
-      const int64_t j0 = tiles[it] * L::ROWS + 32 * u;
-      if (mask.none(q0, q1, j0, j0 + 31)) continue;
-      const bool all = mask.all(q0, q1, j0, j0 + 31);
-      const f32x16 c = by_rows<T, DP>(lk, 32 * u, qf);
-      const f32x16 dp = by_rows<T, DP>(lv, 32 * u, df);
+    for (int u = 0; u < SUB; ++u) {
+      const f32x16 c = by_rows<L>(at, lds, 32 * u, qf);
+      const f32x16 dp = by_rows<L>(at, lds + L::BYTES, 32 * u, df);
       float x[16], p[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         p[i] = __builtin_amdgcn_exp2f(fmaf(c[i], c2, -lse2));
         x[i] = p[i] * (dp[i] - delta);
-        if (!all && !mask.sees(qi, j0 + walked(i))) x[i] = 0.f, p[i] = 0.f;
-        off += x[i];
       }
-      by_columns<T, DP, NP, FIX>(acc, lk, 32 * u, x, pk, p);
+      if (!all) {
+        rarely();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (!mask.sees(qi, j0 + 4 * (lane >> 5) + 32 * u + walked(i))) x[i] = 0.f, p[i] = 0.f;
+      }
+      if constexpr (FIX)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) off += x[i];
+      by_columns<L, NP, FIX>(acc, at, lds, 32 * u, x, pk, p);
     }
-    __syncthreads();
+    if constexpr (L::BUFS == 1) __syncthreads();
+    if (it + 1 < count) ks.store(lds + fill), vs.store(lds + fill + L::BYTES);
+    at.flip();
+  }
+  if constexpr (FIX) off += __shfl_xor(off, 32, 64);
+  if constexpr (!WIDE) {
+    if (FIX && lane < 32) stat[wave][lane] = off;
+    __syncthreads();  // also: the tiles are read
+    if constexpr (FIX) {
+      off = stat[0][lane & 31];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) off += stat[w][lane & 31];
+    }
   }
   if constexpr (FIX) {
-    off += __shfl_xor(off, 32, 64);
     delta += off;
 #pragma unroll
-    for (int t = 0; t < DP / 32; ++t) acc[t] -= off * pk[t];
+    for (int t = 0; t < NT; ++t) acc[t] -= off * pk[t];
   }
-  if (qi >= s.n) return;
+  TO* out = static_cast<TO*>(a.dq) + (s.start + q0) * pitch + static_cast<int64_t>(h) * a.D;
+  if constexpr (!WIDE) {
+    add_waves(acc, lds);
+    if (qi >= s.n) return;
+    store_own<TO, NT>(out, pitch, acc, a.scale, a.D);
+    if (wave > 0) return;
+  } else {
+    if (qi >= s.n) return;
+    store_held<TO, NT>(out, pitch, acc, a.scale, a.D);
+  }
   if (lane < 32) reinterpret_cast<float*>(a.ws)[(s.start + qi) * a.Hq + h] = delta;
-  store_held<TO, DP>(static_cast<TO*>(a.dq) + (s.start + q0) * pitch + static_cast<int64_t>(h) * a.D, pitch, acc,
-                     a.scale, a.D);
 }
 
-// How the queries that a key tile is seen by are cut: `parts` for each tile, and
-// `first` for the first `sink_tiles` tiles under a window.
-struct Cut {
-  int tiles, sink_tiles, parts, first;
+// The work of dK and dV: steps (a tile of queries of one head, against a tile of
+// kBlock keys), for a sequence and key head key tile by key tile, in each head by
+// head.  Key tile t is seen by query tiles from its own on: to the sequence's end
+// (no window, or first tokens in it), else `reach` of them.
+template <int R>  // rows of a query tile
+struct Steps {
+  static constexpr int PER = kBlock / R;  // query tiles of a key tile's length
+  int group, tiles, queries, sinks, reach;
+  __host__ __device__ __forceinline__ Steps(int64_t n, int group, int64_t window, int64_t sink)
+      : group(group), tiles(static_cast<int>((n + kBlock - 1) / kBlock)), queries(static_cast<int>((n + R - 1) / R)),
+        sinks(window ? static_cast<int>((sink + kBlock - 1) / kBlock) : tiles),
+        reach(static_cast<int>((kBlock - 2 + window) / R + 1)) {
+    if (sinks > tiles) sinks = tiles;
+  }
+  // query tiles that see key tile t
+  __host__ __device__ __forceinline__ int seen(int t) const {
+    const int all = queries - PER * t;
+    return t < sinks || all < reach ? all : reach;
+  }
+  // steps of the key tiles before t
+  __host__ __device__ __forceinline__ int64_t before(int64_t t) const {
+    const auto full = [&](int64_t x) { return x * queries - PER * (x * (x - 1) / 2); };
+    if (t <= sinks) return group * full(t);
+    int64_t cut = queries >= reach ? (queries - reach) / PER + 1 : 0;  // from here on the end is nearer
+    cut = cut < sinks ? sinks : cut > t ? t : cut;
+    return group * (full(sinks) + (cut - sinks) * reach + full(t) - full(cut));
+  }
+  // the key tile of a step
+  __device__ __forceinline__ int tile_of(int64_t step) const {
+    int lo = 0, hi = tiles - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (before(mid) <= step) lo = mid;
+      else hi = mid - 1;
+    }
+    return lo;
+  }
 };
-// Partial sums: [part][row][Hk][D] of dK, then of dV; of the first tiles'
-// [part][sequence][row][Hk][D] likewise.
+
+// All steps of a batch, cut into one share for each workgroup.
+template <int R>
+__device__ __forceinline__ Steps<R> steps_of(const AttnArgs& a, int64_t b) {
+  return Steps<R>(span(a, b).n, a.Hq / a.Hk, a.window, a.sinks);
+}
+template <int R>
+__device__ __forceinline__ int64_t steps_all(const AttnArgs& a, int64_t b) {
+  const Steps<R> s = steps_of<R>(a, b);
+  return s.before(s.tiles) * a.Hk;
+}
+__device__ __forceinline__ int64_t shfl64(int64_t x, int lane) {
+  const uint32_t lo = __shfl(static_cast<int>(x), lane, 64), hi = __shfl(static_cast<int>(x >> 32), lane, 64);
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+// Inclusive sums over the lanes.
+__device__ __forceinline__ int64_t sums64(int64_t x) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int64_t y = shfl64(x, lane_id() - d < 0 ? 0 : lane_id() - d);
+    if (lane_id() >= d) x += y;
+  }
+  return x;
+}
+// A step's place: its sequence (B: past the last), key head, key tile, and step in the
+// tile.
+template <int R> struct Place {
+  int64_t b, step;
+  int kh, tile;
+  __device__ __forceinline__ Place(const AttnArgs& a, int64_t x) : b(0), step(0), kh(0), tile(0) {
+    if (!a.cu) {
+      const int64_t each = steps_all<R>(a, 0);
+      b = x / each;
+      x -= b * each;
+    } else {
+      for (;; b += 64) {
+        if (b >= a.B) {
+          b = a.B;
+          return;
+        }
+        const int64_t own = b + lane_id() < a.B ? steps_all<R>(a, b + lane_id()) : 0, upto = sums64(own);
+        const uint64_t past = __ballot(upto > x);
+        if (past) {
+          const int at = __builtin_ctzll(past);
+          b += at;
+          x -= shfl64(upto - own, at);
+          break;
+        }
+        x -= shfl64(upto, 63);
+      }
+    }
+    const Steps<R> s = steps_of<R>(a, b);
+    const int64_t head = s.before(s.tiles);
+    kh = static_cast<int>(x / head);
+    x -= kh * head;
+    tile = s.tile_of(x);
+    step = x - s.before(tile);
+  }
+};
+template <int R>
+__device__ __forceinline__ int64_t share_of(const AttnArgs& a, int shares) {
+  int64_t all = 0;
+  if (!a.cu) {
+    all = steps_all<R>(a, 0) * a.B;
+  } else {
+    for (int64_t b = 0; b < a.B; b += 64) all += shfl64(sums64(b + lane_id() < a.B ? steps_all<R>(a, b + lane_id()) : 0), 63);
+  }
+  return max(int64_t(1), (all + shares - 1) / shares);
+}
+
+// Partial sums of key tiles that several shares have a part of: a share has at most
+// two, the tile that it begins in the middle of and the one that it ends in.
 struct Parts {
-  float *delta, *rest, *first;
+  float *delta, *sums;
 };
+template <int DP>
+__device__ __forceinline__ float* part_of(const Parts& p, int64_t share, bool end) {
+  return p.sums + (2 * share + end) * (2 * kBlock * DP);
+}
 
 template <typename T, typename TO, int DP, int NP>
-__global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs a, Cut cut, Parts parts) {
+__global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs a, Parts parts) {
   using L = Tile<T, DP>;
-  __shared__ __align__(16) char lq[L::BYTES];
-  __shared__ __align__(16) char ld[L::BYTES];
-  __shared__ __align__(16) float stat[2][L::ROWS];
-  const int kh = blockIdx.y, group = a.Hq / a.Hk, lane = lane_id(), wave = threadIdx.x >> 6;
-  const Span s = span(a, blockIdx.z);
-  const bool early = static_cast<int>(blockIdx.x) < cut.sink_tiles * cut.first;
-  const int job = early ? blockIdx.x : blockIdx.x - cut.sink_tiles * cut.first;
-  const int of = early ? cut.first : cut.parts, part = job % of;
-  const int64_t block0 = static_cast<int64_t>(job / of + (early ? 0 : cut.sink_tiles)) * kBlock;
-  if (block0 >= s.n) return;
-  const Mask mask{a.window, a.sinks};
-  const int64_t j0 = block0 + wave * kHeld, j1 = j0 + kHeld - 1, kj = j0 + (lane & 31);
-  // query tiles that see the keys, for each head of the group
-  const int64_t last = mask.window == 0 || block0 < mask.sinks ? s.n - 1
-                                                               : min(s.n - 1, block0 + kBlock - 1 + mask.window - 1);
-  const int64_t tile0 = block0 / L::ROWS, per = last / L::ROWS - tile0 + 1, total = per * group;
-  const int64_t it0 = total * part / of, it1 = total * (part + 1) / of;
-
-  u32x4 kf[L::KF], vf[L::KF];
-  load_held<T, DP>(rows_of<T>(a.k, s.start, s.n, a.k_row, kh, a.D), j0, a.D, kf);
-  load_held<T, DP>(rows_of<T>(a.v, s.start, s.n, a.v_row, kh, a.D), j0, a.D, vf);
-  f32x16 dk[DP / 32], dv[DP / 32];
-#pragma unroll
-  for (int t = 0; t < DP / 32; ++t) dk[t] = zero16(), dv[t] = zero16();
+  constexpr int NT = DP / 32, R = L::ROWS;
+  __shared__ __align__(16) char lds[2 * L::PAIR];
+  __shared__ __align__(16) float stat[2][2][R];
+  const int group = a.Hq / a.Hk, lane = lane_id(), wave = wave_id();
+  const int64_t share = uniform(share_of<R>(a, gridDim.x));
+  int64_t x = share * blockIdx.x;
+  Place<R> at(a, x);
+  const Mask mask(a);
   const float c2 = a.scale * kLog2e;
-  const int64_t pitch = static_cast<int64_t>(a.Hq) * a.D;
-  Staged<T, DP> qs, ds;
-  float st = 0.f;
-  auto load = [&](int64_t it) {
-    const int g = static_cast<int>(it / per);
-    const int64_t i0 = (tile0 + it - g * per) * L::ROWS;
-    const int h = kh * group + g;
-    qs.load(rows_of<T>(a.q, s.start, s.n, a.q_row, h, a.D), i0, a.D);
-    ds.load(rows_of<T>(a.dout, s.start, s.n, pitch, h, a.D), i0, a.D);
-    if (threadIdx.x < 2 * L::ROWS) {
-      const int64_t i = i0 + threadIdx.x % L::ROWS;
-      const bool lse = threadIdx.x < L::ROWS;
-      st = i < s.n ? (lse ? a.lse_in : parts.delta)[(s.start + i) * a.Hq + h] * (lse ? kLog2e : 1.f) : 0.f;
-    }
-  };
-  if (it0 < it1) load(it0);
-  for (int64_t it = it0; it < it1; ++it) {
-    qs.store(lq);
-    ds.store(ld);
-    if (threadIdx.x < 2 * L::ROWS) stat[threadIdx.x / L::ROWS][threadIdx.x % L::ROWS] = st;
-    __syncthreads();
-    if (it + 1 < it1) load(it + 1);
-#pragma unroll
-    for (int u = 0; u < L::ROWS / 32; ++u) {
-      const int64_t i0 = (tile0 + it % per) * L::ROWS + 32 * u;
-      if (mask.none(i0, i0 + 31, j0, j1)) continue;
-      const bool all = mask.all(i0, i0 + 31, j0, j1);
-      const f32x16 c = by_rows<T, DP>(lq, 32 * u, kf);
-      const f32x16 dp = by_rows<T, DP>(ld, 32 * u, vf);
-      float p[16], x[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int r = 32 * u + walked(i);
-        p[i] = __builtin_amdgcn_exp2f(fmaf(c[i], c2, -stat[0][r]));
-        x[i] = p[i] * (dp[i] - stat[1][r]);
-        if (!all && !mask.sees(i0 + walked(i), kj)) p[i] = 0.f, x[i] = 0.f;
+  const int64_t pitch = static_cast<int64_t>(a.Hq) * a.D, kp = static_cast<int64_t>(a.Hk) * a.D;
+  for (int64_t left = share; left > 0;) {
+    const int64_t b = uniform(at.b);
+    if (b >= a.B) return;
+    const Span s{uniform(span(a, b).start), uniform(span(a, b).n)};
+    const Steps<R> steps(s.n, group, a.window, a.sinks);
+    const int kh = uniform(at.kh), kt = uniform(at.tile), block0 = kt * kBlock;
+    const int per = steps.seen(kt);
+    const int64_t total = static_cast<int64_t>(per) * group, first = uniform(at.step);
+    const int count = uniform(static_cast<int>(min(left, total - first)));
+    left -= count;
+    const bool whole = count == total, begun = first > 0;
+    // the next share's place
+    at.step = 0;
+    if (first + count == total && ++at.tile == steps.tiles) {
+      at.tile = 0;
+      if (++at.kh == a.Hk) {
+        at.kh = 0;
+        while (++at.b < a.B && span(a, at.b).n == 0) {}
       }
-      by_columns<T, DP, NP>(dv, ld, 32 * u, p);
-      by_columns<T, DP, NP>(dk, lq, 32 * u, x);
     }
-    __syncthreads();
+
+    const int j0 = block0 + wave * kHeld, j1 = j0 + kHeld - 1, kj = j0 + (lane & 31);
+    int g = uniform(static_cast<int>(first / per));  // the head and tile that are loaded next
+    int tile = uniform(block0 / R + static_cast<int>(first - static_cast<int64_t>(g) * per));
+    const int tile_end = block0 / R + per;
+    Staged<L> qs, ds;
+    Rows qr = rows_of<T>(a.q, s.start, s.n, a.q_row, kh * group + g, a.D);
+    Rows dr = rows_of<T>(a.dout, s.start, s.n, pitch, kh * group + g, a.D);
+    qs.init(qr), ds.init(dr);
+    float st = 0.f;
+    auto load = [&]() {
+      const int i0 = tile * R;
+      qs.load(qr, i0), ds.load(dr, i0);
+      if (threadIdx.x < 2 * R) {
+        const int i = i0 + threadIdx.x % R;
+        const bool lse = threadIdx.x < R;
+        st = i < s.n ? (lse ? a.lse_in : parts.delta)[(s.start + i) * a.Hq + kh * group + g] * (lse ? kLog2e : 1.f) : 0.f;
+      }
+      if (++tile == tile_end) {
+        tile = block0 / R, ++g;
+        qr.base += a.D * sizeof(T), dr.base += a.D * sizeof(T);
+      }
+    };
+    int fill = 0;
+    auto store = [&](int buf) {
+      qs.store(lds + fill), ds.store(lds + fill + L::BYTES);
+      if (threadIdx.x < 2 * R) stat[buf][threadIdx.x / R][threadIdx.x % R] = st;
+    };
+    int next0 = tile * R;
+    load();
+    u32x4 kf[L::KF], vf[L::KF];
+    load_held<L>(rows_of<T>(a.k, s.start, s.n, a.k_row, kh, a.D), j0, kf);
+    load_held<L>(rows_of<T>(a.v, s.start, s.n, a.v_row, kh, a.D), j0, vf);
+    f32x16 dk[NT], dv[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) dk[t] = zero16(), dv[t] = zero16();
+    Lane<L> mine(0);
+    store(0);
+    for (int it = 0; it < count; ++it) {
+      const int i0 = next0;
+      next0 = tile * R;
+      __syncthreads();
+      if (it + 1 < count) load();
+      fill ^= L::PAIR;
+      const bool all = mask.all(i0, i0 + R - 1, j0, j1);
+      const float* lse = stat[it & 1][0] + 4 * (lane >> 5);
+#pragma unroll
+      for (int u = 0; u < R / 32; ++u) {
+        const f32x16 c = by_rows<L>(mine, lds, 32 * u, kf);
+        const f32x16 dp = by_rows<L>(mine, lds + L::BYTES, 32 * u, vf);
+        float p[16], y[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          p[i] = __builtin_amdgcn_exp2f(fmaf(c[i], c2, -lse[32 * u + walked(i)]));
+          y[i] = p[i] * (dp[i] - lse[R + 32 * u + walked(i)]);
+        }
+        if (!all) {
+          rarely();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (!mask.sees(i0 + 4 * (lane >> 5) + 32 * u + walked(i), kj)) p[i] = 0.f, y[i] = 0.f;
+        }
+        by_columns<L, NP>(dv, mine, lds + L::BYTES, 32 * u, p);
+        by_columns<L, NP>(dk, mine, lds, 32 * u, y);
+      }
+      if (it + 1 < count) store(it + 1 & 1);
+      mine.flip();
+    }
+    __syncthreads();  // the tiles are read
+    if (!whole) {
+      float* to = part_of<DP>(parts, blockIdx.x, !begun) + wave * kHeld * DP;
+      store_held<float, NT>(to, DP, dk, a.scale, DP);
+      store_held<float, NT>(to + kBlock * DP, DP, dv, 1.f, DP);
+    } else if (kj < s.n) {
+      const int64_t to = (s.start + j0) * kp + static_cast<int64_t>(kh) * a.D;
+      store_held<TO, NT>(static_cast<TO*>(a.dk) + to, kp, dk, a.scale, a.D);
+      store_held<TO, NT>(static_cast<TO*>(a.dv) + to, kp, dv, 1.f, a.D);
+    }
   }
-  if (kj >= s.n) return;
-  const int64_t kp = static_cast<int64_t>(a.Hk) * a.D, at = static_cast<int64_t>(kh) * a.D;
-  if (of == 1) {
-    store_held<TO, DP>(static_cast<TO*>(a.dk) + (s.start + j0) * kp + at, kp, dk, a.scale, a.D);
-    store_held<TO, DP>(static_cast<TO*>(a.dv) + (s.start + j0) * kp + at, kp, dv, 1.f, a.D);
-    return;
-  }
-  const int64_t rows = early ? a.B * cut.sink_tiles * kBlock : a.rows;
-  const int64_t row = early ? static_cast<int64_t>(blockIdx.z) * cut.sink_tiles * kBlock + j0 : s.start + j0;
-  float* to = (early ? parts.first : parts.rest) + (part * rows + row) * kp + at;
-  store_held<float, DP>(to, kp, dk, a.scale, a.D);
-  store_held<float, DP>(to + of * rows * kp, kp, dv, 1.f, a.D);
 }
 
-// The parts of a key tile added, in their order.
-template <typename TO>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Cut cut, Parts parts) {
-  const Span s = span(a, blockIdx.z);
-  const int64_t tile = blockIdx.x, block0 = tile * kBlock;
-  const bool early = tile < cut.sink_tiles;
-  const int of = early ? cut.first : cut.parts;
-  if (block0 >= s.n || of == 1) return;
-  const int64_t kp = static_cast<int64_t>(a.Hk) * a.D, at = static_cast<int64_t>(blockIdx.y) * a.D;
-  const int64_t rows = early ? a.B * cut.sink_tiles * kBlock : a.rows;
-  const int64_t row = early ? static_cast<int64_t>(blockIdx.z) * cut.sink_tiles * kBlock + block0 : s.start + block0;
-  const float* from = (early ? parts.first : parts.rest) + row * kp + at;
-  const int n = static_cast<int>(min(s.n - block0, static_cast<int64_t>(kBlock))), units = a.D / 4;
-  for (int x = threadIdx.x; x < 2 * n * units; x += 256) {
-    const int which = x / (n * units), r = x / units % n, d = x % units * 4;
-    const float* p = from + which * of * rows * kp + r * kp + d;
-    float sum[4] = {};
+// A key tile that begins in share blockIdx.x and goes on in the next ones: its parts
+// added in their order.  blockIdx.y: 16 keys of dK or of dV.
+template <typename T, typename TO, int DP>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Parts parts) {
+  constexpr int R = El<T>::TILE, UNITS = DP / 4, KEYS = 16;
+  const int64_t share = share_of<R>(a, gridDim.x), end = share * (blockIdx.x + 1);
+  const Place<R> at(a, end - 1);
+  if (at.b >= a.B) return;
+  const Span s = span(a, at.b);
+  const int64_t total = static_cast<int64_t>(Steps<R>(s.n, a.Hq / a.Hk, a.window, a.sinks).seen(at.tile)) * (a.Hq / a.Hk);
+  const int64_t begin = end - 1 - at.step;
+  if (begin < end - share || begin + total <= end) return;
+  const int more = static_cast<int>((begin + total - end + share - 1) / share);
+  const int which = blockIdx.y / (kBlock / KEYS), key0 = blockIdx.y % (kBlock / KEYS) * KEYS;
+  const int64_t kp = static_cast<int64_t>(a.Hk) * a.D;
+  for (int x = threadIdx.x; x < KEYS * UNITS; x += 256) {
+    const int key = key0 + x / UNITS, d = x % UNITS * 4;
+    if (at.tile * kBlock + key >= s.n || d >= a.D) continue;
+    const int64_t from = (static_cast<int64_t>(which) * kBlock + key) * DP + d;
+    float sum[4];
+    ld4<float>(part_of<DP>(parts, blockIdx.x, true) + from, sum);
 #pragma unroll 4
-    for (int i = 0; i < of; ++i) {
+    for (int i = 1; i <= more; ++i) {
       float y[4];
-      ld4<float>(p + i * rows * kp, y);
+      ld4<float>(part_of<DP>(parts, blockIdx.x + i, false) + from, y);
 #pragma unroll
       for (int k = 0; k < 4; ++k) sum[k] += y[k];
     }
-    st4<TO>(static_cast<TO*>(which ? a.dv : a.dk) + (s.start + block0 + r) * kp + at + d, sum);
+    store4<TO>(static_cast<TO*>(which ? a.dv : a.dk) + (s.start + at.tile * kBlock + key) * kp +
+                   static_cast<int64_t>(at.kh) * a.D + d,
+               sum);
   }
 }
 
 int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
 
-constexpr int64_t kFill = 512;  // workgroups that fill the card
-constexpr int kMaxParts = 64;
-Cut cut_of(const AttnArgs& a) {
-  const int tile = a.io_bf16 ? El<bf16_t>::TILE : El<float>::TILE;
-  Cut c{};
-  c.tiles = static_cast<int>(ceil_div(a.T, kBlock));
-  c.sink_tiles = a.window ? static_cast<int>(std::min<int64_t>(ceil_div(a.sinks, kBlock), c.tiles)) : 0;
-  const int64_t reach = a.window ? std::min(a.T, a.window + kBlock) : a.T;
-  const int64_t group = a.Hq / a.Hk, steps = ceil_div(reach, tile) * group, all = ceil_div(a.T, tile) * group;
-  const int64_t blocks = std::max<int64_t>(1, a.B * a.Hk * c.tiles);
-  c.parts = static_cast<int>(std::max<int64_t>(1, std::min({ceil_div(kFill, blocks), ceil_div(steps, 4),
-                                                            static_cast<int64_t>(kMaxParts)})));
-  // the first tiles' queries are cut as finely as the others', while there are few
-  // such tiles
-  const int64_t firsts = std::max<int64_t>(1, a.B * a.Hk * c.sink_tiles);
-  c.first = static_cast<int>(std::max<int64_t>(
-      1, std::min({ceil_div(c.parts * all, steps), ceil_div(2 * kFill, firsts), static_cast<int64_t>(kMaxParts)})));
-  return c;
+// Workgroups of the (dK, dV) kernel: as many as the card holds at once, each with
+// kLeast steps or more.
+constexpr int64_t kHold = 256, kLeast = 2;
+int shares_of(const AttnArgs& a) {
+  // a ragged batch has no more steps than its rows as sequences of the longest length
+  const int64_t n = std::min(a.T, a.rows), seqs = std::min(a.B, ceil_div(a.rows, n) + 1);
+  int64_t each;
+  if (a.io_bf16) {
+    const Steps<El<bf16_t>::TILE> s(n, a.Hq / a.Hk, a.window, a.sinks);
+    each = s.before(s.tiles);
+  } else {
+    const Steps<El<float>::TILE> s(n, a.Hq / a.Hk, a.window, a.sinks);
+    each = s.before(s.tiles);
+  }
+  return static_cast<int>(std::max<int64_t>(1, std::min(kHold, each * a.Hk * seqs / kLeast)));
 }
-size_t parts_of(const AttnArgs& a, const Cut& c, char* ws, Parts* p) {
-  const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t kp = static_cast<size_t>(a.Hk) * a.D * sizeof(float);
-  size_t at = 0;
-  p->delta = reinterpret_cast<float*>(ws);
-  at += up(static_cast<size_t>(a.rows) * a.Hq * sizeof(float));
-  p->rest = reinterpret_cast<float*>(ws + at);
-  if (c.parts > 1 && c.tiles > c.sink_tiles) at += up(2 * kp * c.parts * a.rows);
-  p->first = reinterpret_cast<float*>(ws + at);
-  if (c.first > 1 && c.sink_tiles) at += up(2 * kp * c.first * a.B * c.sink_tiles * kBlock);
-  return at;
+int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+size_t parts_of(const AttnArgs& a, int shares, Parts* p) {
+  const size_t delta = (static_cast<size_t>(a.rows) * a.Hq * sizeof(float) + 255) / 256 * 256;
+  p->delta = reinterpret_cast<float*>(a.ws);
+  p->sums = reinterpret_cast<float*>(a.ws + delta);
+  return delta + (shares > 1 ? static_cast<size_t>(shares) * 4 * kBlock * padded(a.D) * sizeof(float) : 0);
 }
 
-template <typename T, typename TO, int DP>
+// Whether the kernels that hold queries give each wave 32 of its own: where that
+// fills the card, or the other layout's tiles do not fit LDS.
+template <typename T, int DP>
+bool wide(const AttnArgs& a) {
+  return 256 * DP * sizeof(T) > (128 << 10) || a.B * a.Hq * ceil_div(a.T, kBlock) > kWideFrom;
+}
+
+template <typename T, typename TO, int DP, bool WIDE>
 hipError_t fwd(const AttnArgs& a, hipStream_t st) {
   constexpr int NP = sizeof(TO) == 2 ? 2 : 3;
   ProfScope prof("attention", st);
-  const dim3 grid(a.Hq, static_cast<unsigned>(ceil_div(a.T, kBlock)), static_cast<unsigned>(a.B));
-  attn_fwd_kernel<T, TO, DP, NP><<<grid, 256, 0, st>>>(a);
+  const dim3 grid(a.Hq, static_cast<unsigned>(ceil_div(a.T, WIDE ? kBlock : kHeld)), static_cast<unsigned>(a.B));
+  attn_fwd_kernel<T, TO, DP, NP, WIDE><<<grid, 256, 0, st>>>(a);
   return hipGetLastError();
 }
+template <typename T, typename TO, int DP>
+hipError_t fwd(const AttnArgs& a, hipStream_t st) {
+  if constexpr (256 * DP * sizeof(T) <= (128 << 10))
+    if (!wide<T, DP>(a)) return fwd<T, TO, DP, false>(a, st);
+  return fwd<T, TO, DP, true>(a, st);
+}
 
+template <typename T, typename TO, int DP, bool WIDE>
+hipError_t dq(const AttnArgs& a, hipStream_t st) {
+  constexpr int NP = sizeof(TO) == 2 ? 2 : 3;
+  ProfScope prof("attention_dq", st);
+  const dim3 grid(a.Hq, static_cast<unsigned>(ceil_div(a.T, WIDE ? kBlock : kHeld)), static_cast<unsigned>(a.B));
+  attn_dq_kernel<T, TO, DP, NP, WIDE><<<grid, 256, 0, st>>>(a);
+  return hipGetLastError();
+}
 template <typename T, typename TO, int DP>
 hipError_t bwd(const AttnArgs& a, hipStream_t st) {
   constexpr int NP = sizeof(TO) == 2 ? 2 : 3;
-  const Cut cut = cut_of(a);
+  hipError_t e;
+  if constexpr (256 * DP * sizeof(T) <= (128 << 10))
+    e = wide<T, DP>(a) ? dq<T, TO, DP, true>(a, st) : dq<T, TO, DP, false>(a, st);
+  else
+    e = dq<T, TO, DP, true>(a, st);
+  if (e != hipSuccess) return e;
+  const int shares = shares_of(a);
   Parts parts;
-  parts_of(a, cut, a.ws, &parts);
-  {
-    ProfScope prof("attention_dq", st);
-    const dim3 grid(a.Hq, static_cast<unsigned>(cut.tiles), static_cast<unsigned>(a.B));
-    attn_dq_kernel<T, TO, DP, NP><<<grid, 256, 0, st>>>(a);
-    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  }
+  parts_of(a, shares, &parts);
   {
     ProfScope prof("attention_dkv", st);
-    const dim3 grid(cut.sink_tiles * cut.first + (cut.tiles - cut.sink_tiles) * cut.parts, a.Hk,
-                    static_cast<unsigned>(a.B));
-    attn_dkv_kernel<T, TO, DP, NP><<<grid, 256, 0, st>>>(a, cut, parts);
-    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    attn_dkv_kernel<T, TO, DP, NP><<<dim3(shares), 256, 0, st>>>(a, parts);
+    if (e = hipGetLastError(); e != hipSuccess) return e;
   }
-  const int joined = cut.parts > 1 ? cut.tiles : cut.first > 1 ? cut.sink_tiles : 0;
-  if (!joined) return hipSuccess;
+  if (shares == 1) return hipSuccess;
   ProfScope prof("attention_join", st);
-  attn_join_kernel<TO><<<dim3(joined, a.Hk, static_cast<unsigned>(a.B)), 256, 0, st>>>(a, cut, parts);
+  attn_join_kernel<T, TO, DP><<<dim3(shares, 2 * kBlock / 16), 256, 0, st>>>(a, parts);
   return hipGetLastError();
 }
 
@@ -665,7 +965,7 @@ hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t st) {
 
 size_t attn_bwd_workspace(const AttnArgs& a) {
   Parts p;
-  return parts_of(a, cut_of(a), nullptr, &p);
+  return parts_of(a, shares_of(a), &p);
 }
 
 hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t st) {
