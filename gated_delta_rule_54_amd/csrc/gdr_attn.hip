@@ -192,30 +192,49 @@ template <typename L> struct Lane {
 // (rows row0 .. + 31 of the tile) x (held rows): lane (held row lane % 32) holds
 // tile rows row0 + 8 (i / 4) + 4 (lane / 32) + i % 4.
 template <typename L>
+__device__ __forceinline__ u32x4 unit(const Lane<L>& at, const char* lds, int row0, int i) {
+  return *reinterpret_cast<const u32x4*>(lds + at.row[i & 7] + (row0 * L::PITCH + (i >> 3) * 256));
+}
+template <typename L>
 __device__ __forceinline__ f32x16 by_rows(const Lane<L>& at, const char* lds, int row0, const u32x4 (&held)[L::KF]) {
   f32x16 c = zero16();
 #pragma unroll
-  for (int i = 0; i < L::KF; ++i)
-    c = mma<typename L::T>(*reinterpret_cast<const u32x4*>(lds + at.row[i & 7] + (row0 * L::PITCH + (i >> 3) * 256)),
-                           held[i], c);
+  for (int i = 0; i < L::KF; ++i) c = mma<typename L::T>(unit<L>(at, lds, row0, i), held[i], c);
   return c;
+}
+// Two such products in turn: each waits for its own last one, not for the other's.
+template <typename L>
+__device__ __forceinline__ void by_rows2(const Lane<L>& at, const char* lds0, const char* lds1, int row0, int row1,
+                                         const u32x4 (&held0)[L::KF], const u32x4 (&held1)[L::KF], f32x16& c0,
+                                         f32x16& c1) {
+  c0 = zero16(), c1 = zero16();
+#pragma unroll
+  for (int i = 0; i < L::KF; ++i) {
+    c0 = mma<typename L::T>(unit<L>(at, lds0, row0, i), held0[i], c0);
+    c1 = mma<typename L::T>(unit<L>(at, lds1, row1, i), held1[i], c1);
+  }
 }
 // Of element i, the tile row less 4 (lane / 32).
 __device__ constexpr int walked(int i) { return 8 * (i >> 2) + (i & 3); }
 
-// NP bf16 parts of eight values, most significant first.
+// NP bf16 parts of eight values, most significant first; converted in pairs.
 template <int NP>
 __device__ __forceinline__ void split(const float* p, bf16x8 (&out)[NP]) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  u32x4 w[NP];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float r = p[i];
+  for (int i = 0; i < 4; ++i) {
+    f32x2 r{p[2 * i], p[2 * i + 1]};
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
-      const __bf16 x = static_cast<__bf16>(r);
-      out[k][i] = x;
-      r -= static_cast<float>(x);
+      w[k][i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(r, bf16x2));
+      r[0] -= __uint_as_float(w[k][i] << 16);
+      r[1] -= __uint_as_float(w[k][i] & 0xffff0000u);
     }
   }
+#pragma unroll
+  for (int k = 0; k < NP; ++k) out[k] = __builtin_bit_cast(bf16x8, w[k]);
 }
 
 // acc[t] += (channels 32 t .. + 31 of tile rows row0 .. + 31)^T x p, p as by_rows
@@ -231,6 +250,7 @@ __device__ __forceinline__ void by_columns(f32x16 (&acc)[L::DP / 32], const Lane
       bf16x8 f[NP], g[1];
       split<NP>(p + 8 * k, f);
       if constexpr (MORE) split<1>(y + 8 * k, g);
+      bf16x8 x[NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const char* from = lds + ((row0 + 16 * k) * L::PITCH + (t >> 2) * 256);
@@ -238,12 +258,18 @@ __device__ __forceinline__ void by_columns(f32x16 (&acc)[L::DP / 32], const Lane
             bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(from + at.col[t & 3][0])));
         const bf16x4 b = __builtin_bit_cast(
             bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(from + at.col[t & 3][1])));
-        const bf16x8 x{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-#pragma unroll
-        for (int n = NP - 1; n >= 0; --n)
-          acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, f[n], acc[t], 0, 0, 0);
-        if constexpr (MORE) more[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, g[0], more[t], 0, 0, 0);
+        x[t] = bf16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
       }
+      // a sum's products one after another would wait for each other
+#pragma unroll
+      for (int n = NP - 1; n >= 0; --n)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[t], f[n], acc[t], 0, 0, 0);
+      if constexpr (MORE)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          more[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[t], g[0], more[t], 0, 0, 0);
     }
   } else {
     const int d = lane_id() & 31, h = lane_id() >> 5;
@@ -403,11 +429,15 @@ __global__ __launch_bounds__(256, WIDE && DP <= 128 ? 2 : 1) void attn_fwd_kerne
     const int j0 = tiles[it] * L::ROWS + mine0, j1 = j0 + 32 * SUB - 1;
     if (!mask.none(q0, q1, j0, j1)) {
       float x[SUB][16];
+      if constexpr (SUB == 2) {
+        f32x16 c, d;
+        by_rows2<L>(at, lds, lds, 0, 32, qf, qf, c, d);
 #pragma unroll
-      for (int u = 0; u < SUB; ++u) {
-        const f32x16 c = by_rows<L>(at, lds, 32 * u, qf);
+        for (int i = 0; i < 16; ++i) x[0][i] = c[i], x[1][i] = d[i];
+      } else {
+        const f32x16 c = by_rows<L>(at, lds, 0, qf);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[u][i] = c[i];
+        for (int i = 0; i < 16; ++i) x[0][i] = c[i];
       }
       if (!mask.all(q0, q1, j0, j1)) {
         rarely();
@@ -549,8 +579,8 @@ __global__ __launch_bounds__(256, 1) void attn_dq_kernel(AttnArgs a) {
     const bool all = mask.all(q0, q1, j0, j0 + 32 * SUB - 1);
 #pragma unroll
     for (int u = 0; u < SUB; ++u) {
-      const f32x16 c = by_rows<L>(at, lds, 32 * u, qf);
-      const f32x16 dp = by_rows<L>(at, lds + L::BYTES, 32 * u, df);
+      f32x16 c, dp;
+      by_rows2<L>(at, lds, lds + L::BYTES, 32 * u, 32 * u, qf, df, c, dp);
       float x[16], p[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -799,8 +829,8 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs a, Parts part
       const float* lse = stat[it & 1][0] + 4 * (lane >> 5);
 #pragma unroll
       for (int u = 0; u < R / 32; ++u) {
-        const f32x16 c = by_rows<L>(mine, lds, 32 * u, kf);
-        const f32x16 dp = by_rows<L>(mine, lds + L::BYTES, 32 * u, vf);
+        f32x16 c, dp;
+        by_rows2<L>(mine, lds, lds + L::BYTES, 32 * u, 32 * u, kf, vf, c, dp);
         float p[16], y[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
