@@ -353,19 +353,32 @@ struct KeyTiles {
   __device__ __forceinline__ int operator[](int i) const { return i < head ? i : i + skip; }
 };
 
-// The layout of the kernels that hold queries.  WIDE: each wave holds 32 queries of
-// its own and walks all rows of a tile.  Otherwise all four hold the same 32, and
-// each takes 32 rows of a tile of 128, for grids that do not fill the card: four
-// times the workgroups, each a quarter as long, joined at its end.
-template <typename T, int DP, bool WIDE>
-using QTile = Tile<T, DP, WIDE ? El<T>::TILE : 128, WIDE || 512 * DP * sizeof(T) <= (128 << 10) ? 2 : 1>;
+// The VJP's kernels have two sums for their held rows (dV and dK; dS K and P K).
+// One wave forms both, for each of four blocks of 32 rows; where its registers do not
+// hold them (256 channels in bf16) two waves do, one sum each, for each of two blocks.
+// That costs the scores twice, but 2 x 2048 tokens of 16 heads of 256 take 0.96 ms
+// instead of 1.90, of which spilled registers were the most.  At 128 channels two waves
+// for each block, all eight on a compute unit, took the same time (1.24 ms for the
+// training step of 2 x 4096 tokens), and fp32 up to a quarter more.
+template <typename T, int DP> constexpr bool kApart = sizeof(T) == 2 && DP > 128;
+template <typename T, int DP> constexpr int kBlocks = kApart<T, DP> ? 2 : 4;
+// Workgroups of these kernels on a compute unit.
+template <typename T, int DP> constexpr int kResident = sizeof(T) == 2 && DP <= 64 ? 2 : 1;
+constexpr int kBoth = 0, kFirst = 1, kSecond = 2;  // what a wave forms
+
+// The layout of the kernels that hold queries.  WIDE: each of N waves holds 32
+// queries of its own and walks all rows of a tile.  Otherwise all hold the same 32, and
+// each takes 32 rows of a tile of 32 N, for grids that do not fill the card: N times
+// the workgroups, each an N-th as long, joined at its end.
+template <typename T, int DP, int N, bool WIDE>
+using QTile = Tile<T, DP, WIDE ? El<T>::TILE : 32 * N,
+                   WIDE || 128 * N * DP * sizeof(T) <= (128 << 10) ? 2 : 1>;
 
 // What the waves of a workgroup hold of the same queries, added: wave w is left with
-// the sums of channels 32 t, t = w, w + 4, ..
-template <int NT>
-__device__ __forceinline__ void add_waves(f32x16 (&acc)[NT], char* lds) {
+// the sums of channels 32 t, t = w, w + N, ..
+template <int N, int NT>
+__device__ __forceinline__ void add_waves(f32x16 (&acc)[NT], int wave, char* lds) {
   float* at = reinterpret_cast<float*>(lds) + lane_id();
-  const int wave = wave_id();
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -373,21 +386,21 @@ __device__ __forceinline__ void add_waves(f32x16 (&acc)[NT], char* lds) {
   __syncthreads();
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    if (t % kWaves != wave) continue;
+    if (t % N != wave) continue;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float x = at[(t * 16 + i) * 64];
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) x += at[((w * NT + t) * 16 + i) * 64];
+      for (int w = 1; w < N; ++w) x += at[((w * NT + t) * 16 + i) * 64];
       acc[t][i] = x;
     }
   }
 }
-template <typename TO, int NT>
-__device__ __forceinline__ void store_own(TO* out, int64_t pitch, const f32x16 (&acc)[NT], float f, int D) {
+template <typename TO, int N, int NT>
+__device__ __forceinline__ void store_own(TO* out, int64_t pitch, const f32x16 (&acc)[NT], int wave, float f, int D) {
 #pragma unroll
   for (int t = 0; t < NT; ++t)
-    if (t % kWaves == wave_id()) {
+    if (t % N == wave) {
       const f32x16 one[1] = {acc[t]};
       store_held<TO, 1>(out + 32 * t, pitch, one, f, D - 32 * t);
     }
@@ -395,7 +408,7 @@ __device__ __forceinline__ void store_own(TO* out, int64_t pitch, const f32x16 (
 
 template <typename T, typename TO, int DP, int NP, bool WIDE>
 __global__ __launch_bounds__(256, WIDE && DP <= 128 ? 2 : 1) void attn_fwd_kernel(AttnArgs a) {
-  using L = QTile<T, DP, WIDE>;
+  using L = QTile<T, DP, kWaves, WIDE>;
   constexpr int NT = DP / 32, BLOCK = WIDE ? kBlock : kHeld, SUB = WIDE ? L::ROWS / 32 : 1;
   __shared__ __align__(16) char lds[L::BUFS * L::PAIR];
   __shared__ float stat[WIDE ? 1 : kWaves][2][32];
@@ -495,9 +508,9 @@ __global__ __launch_bounds__(256, WIDE && DP <= 128 ? 2 : 1) void attn_fwd_kerne
     m = top;
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[t] *= f;
-    add_waves(acc, lds);
+    add_waves<kWaves>(acc, wave, lds);
     if (qi >= s.n) return;
-    store_own<TO, NT>(out, pitch, acc, 1.f / l, a.D);
+    store_own<TO, kWaves>(out, pitch, acc, wave, 1.f / l, a.D);
     if (wave > 0) return;
   } else {
     if (qi >= s.n) return;
@@ -513,19 +526,25 @@ __global__ __launch_bounds__(256, WIDE && DP <= 128 ? 2 : 1) void attn_fwd_kerne
 // dS over the keys, which is 0 for the right delta, is what delta is off by (e):
 // dQ has e (P K) taken off (K^T is in registers for dS; one bf16 operand for P is
 // enough, as e is small), and the delta that is passed on has e added.
+template <typename T, typename TO, int DP, bool WIDE> struct Dq {
+  static constexpr bool FIX = sizeof(TO) == 2, APART = FIX && kApart<T, DP>;
+  static constexpr int N = APART ? 2 : 4, BLOCK = kHeld * (WIDE ? N : 1);
+  using L = QTile<T, DP, N, WIDE>;
+};
 template <typename T, typename TO, int DP, int NP, bool WIDE>
-__global__ __launch_bounds__(256, 1) void attn_dq_kernel(AttnArgs a) {
-  using L = QTile<T, DP, WIDE>;
-  constexpr int NT = DP / 32, BLOCK = WIDE ? kBlock : kHeld, SUB = WIDE ? L::ROWS / 32 : 1;
-  constexpr bool FIX = sizeof(TO) == 2;
+__global__ __launch_bounds__(256, (kResident<T, DP>)) void attn_dq_kernel(AttnArgs a) {
+  using C = Dq<T, TO, DP, WIDE>;
+  using L = typename C::L;
+  constexpr int NT = DP / 32, N = C::N, SUB = WIDE ? L::ROWS / 32 : 1;
   __shared__ __align__(16) char lds[L::BUFS * L::PAIR];
-  __shared__ float stat[WIDE ? 1 : kWaves][32];
-  const int h = blockIdx.x, kh = h / (a.Hq / a.Hk), lane = lane_id(), wave = wave_id();
+  __shared__ float stat[N][32];
+  const int h = blockIdx.x, kh = h / (a.Hq / a.Hk), lane = lane_id();
+  const int wave = wave_id() % N;
   const Span s = span(a, blockIdx.z);
-  const int block0 = static_cast<int>(gridDim.y - 1 - blockIdx.y) * BLOCK;
+  const int block0 = static_cast<int>(gridDim.y - 1 - blockIdx.y) * C::BLOCK;
   if (block0 >= s.n) return;
   const Mask mask(a);
-  const KeyTiles tiles(mask, block0, min(block0 + BLOCK, s.n) - 1, L::ROWS);
+  const KeyTiles tiles(mask, block0, min(block0 + C::BLOCK, s.n) - 1, L::ROWS);
   const Rows kr = rows_of<T>(a.k, s.start, s.n, a.k_row, kh, a.D), vr = rows_of<T>(a.v, s.start, s.n, a.v_row, kh, a.D);
   const int q0 = block0 + (WIDE ? wave * kHeld : 0), q1 = q0 + kHeld - 1, qi = q0 + (lane & 31);
   const int mine0 = WIDE ? 0 : 32 * wave;
@@ -533,115 +552,155 @@ __global__ __launch_bounds__(256, 1) void attn_dq_kernel(AttnArgs a) {
   Staged<L> ks, vs;
   ks.init(kr), vs.init(vr);
   ks.load(kr, tiles[0] * L::ROWS), vs.load(vr, tiles[0] * L::ROWS);
-  u32x4 qf[L::KF], df[L::KF];
-  load_held<L>(rows_of<T>(a.q, s.start, s.n, a.q_row, h, a.D), q0, qf);
-  load_held<L>(rows_of<T>(a.dout, s.start, s.n, pitch, h, a.D), q0, df);
-  float lse2 = 0.f, delta = 0.f;
-  if (qi < s.n) {
-    lse2 = a.lse_in[(s.start + qi) * a.Hq + h] * kLog2e;
-    const TO* o = static_cast<const TO*>(a.out) + (s.start + qi) * pitch + static_cast<int64_t>(h) * a.D;
-#pragma unroll
-    for (int i = 0; i < L::KF; ++i) {
-      const int d = (2 * i + (lane >> 5)) * L::PER;
-      if (d >= a.D) continue;
-#pragma unroll
-      for (int e = 0; e < L::PER; e += 4) {
-        float y[4];
-        ld4<TO>(o + d + e, y);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float x = sizeof(T) == 4 ? __uint_as_float(df[i][k])
-                          : k & 1        ? __uint_as_float(df[i][(e + k) / 2] & 0xffff0000u)
-                                         : __uint_as_float(df[i][(e + k) / 2] << 16);
-          delta += x * y[k];
-        }
-      }
-    }
-  }
-  delta += __shfl_xor(delta, 32, 64);
-  f32x16 acc[NT], pk[FIX ? NT : 1];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    acc[t] = zero16();
-    if constexpr (FIX) pk[t] = zero16();
-  }
-  float off = 0.f;
+  float lse2 = 0.f;
+  if (qi < s.n) lse2 = a.lse_in[(s.start + qi) * a.Hq + h] * kLog2e;
   const float c2 = a.scale * kLog2e;
   const int count = uniform(tiles.count);
-  Lane<L> at(mine0);
-  int fill = 0;
-  ks.store(lds), vs.store(lds + L::BYTES);
-  for (int it = 0; it < count; ++it) {
-    __syncthreads();
-    if (it + 1 < count) ks.load(kr, tiles[it + 1] * L::ROWS), vs.load(vr, tiles[it + 1] * L::ROWS);
-    if constexpr (L::BUFS == 2) fill ^= L::PAIR;
-    const int j0 = tiles[it] * L::ROWS + mine0;
-    const bool all = mask.all(q0, q1, j0, j0 + 32 * SUB - 1);
-#pragma unroll
-    for (int u = 0; u < SUB; ++u) {
-      f32x16 c, dp;
-      by_rows2<L>(at, lds, lds + L::BYTES, 32 * u, 32 * u, qf, df, c, dp);
-      float x[16], p[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        p[i] = __builtin_amdgcn_exp2f(fmaf(c[i], c2, -lse2));
-        x[i] = p[i] * (dp[i] - delta);
-      }
-      if (!all) {
-        rarely();
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (!mask.sees(qi, j0 + 4 * (lane >> 5) + 32 * u + walked(i))) x[i] = 0.f, p[i] = 0.f;
-      }
-      if constexpr (FIX)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) off += x[i];
-      by_columns<L, NP, FIX>(acc, at, lds, 32 * u, x, pk, p);
-    }
-    if constexpr (L::BUFS == 1) __syncthreads();
-    if (it + 1 < count) ks.store(lds + fill), vs.store(lds + fill + L::BYTES);
-    at.flip();
-  }
-  if constexpr (FIX) off += __shfl_xor(off, 32, 64);
-  if constexpr (!WIDE) {
-    if (FIX && lane < 32) stat[wave][lane] = off;
-    __syncthreads();  // also: the tiles are read
-    if constexpr (FIX) {
-      off = stat[0][lane & 31];
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) off += stat[w][lane & 31];
-    }
-  }
-  if constexpr (FIX) {
-    delta += off;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t] -= off * pk[t];
-  }
   TO* out = static_cast<TO*>(a.dq) + (s.start + q0) * pitch + static_cast<int64_t>(h) * a.D;
-  if constexpr (!WIDE) {
-    add_waves(acc, lds);
-    if (qi >= s.n) return;
-    store_own<TO, NT>(out, pitch, acc, a.scale, a.D);
-    if (wave > 0) return;
+  // e (P K) on its way to the wave that has dS K
+  float* const meet = reinterpret_cast<float*>(lds) + wave * (NT * 16 * 64) + lane;
+  // all tiles of a wave, which forms dS K, P K (the second sum) or both
+  auto walk = [&](auto what) {
+    constexpr int WHAT = decltype(what)::value;
+    constexpr bool SECOND = WHAT == kSecond, PK = C::FIX && WHAT == kBoth;
+    u32x4 qf[L::KF], df[SECOND ? 1 : L::KF];
+    load_held<L>(rows_of<T>(a.q, s.start, s.n, a.q_row, h, a.D), q0, qf);
+    float delta = 0.f;
+    if constexpr (!SECOND) {
+      load_held<L>(rows_of<T>(a.dout, s.start, s.n, pitch, h, a.D), q0, df);
+      if (qi < s.n) {
+        const TO* o = static_cast<const TO*>(a.out) + (s.start + qi) * pitch + static_cast<int64_t>(h) * a.D;
+#pragma unroll
+        for (int i = 0; i < L::KF; ++i) {
+          const int d = (2 * i + (lane >> 5)) * L::PER;
+          if (d >= a.D) continue;
+#pragma unroll
+          for (int e = 0; e < L::PER; e += 4) {
+            float y[4];
+            ld4<TO>(o + d + e, y);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float x = sizeof(T) == 4 ? __uint_as_float(df[i][k])
+                              : k & 1        ? __uint_as_float(df[i][(e + k) / 2] & 0xffff0000u)
+                                             : __uint_as_float(df[i][(e + k) / 2] << 16);
+              delta += x * y[k];
+            }
+          }
+        }
+      }
+      delta += __shfl_xor(delta, 32, 64);
+    }
+    f32x16 acc[NT], pk[PK ? NT : 1];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      acc[t] = zero16();
+      if constexpr (PK) pk[t] = zero16();
+    }
+    float off = 0.f;
+    Lane<L> at(mine0);
+    int fill = 0;
+    ks.store(lds), vs.store(lds + L::BYTES);
+    for (int it = 0; it < count; ++it) {
+      __syncthreads();
+      if (it + 1 < count) ks.load(kr, tiles[it + 1] * L::ROWS), vs.load(vr, tiles[it + 1] * L::ROWS);
+      if constexpr (L::BUFS == 2) fill ^= L::PAIR;
+      const int j0 = tiles[it] * L::ROWS + mine0;
+      const bool all = mask.all(q0, q1, j0, j0 + 32 * SUB - 1);
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+        f32x16 c, dp;
+        float x[16], p[16];
+        if constexpr (SECOND) {
+          c = by_rows<L>(at, lds, 32 * u, qf);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = __builtin_amdgcn_exp2f(fmaf(c[i], c2, -lse2));
+        } else {
+          by_rows2<L>(at, lds, lds + L::BYTES, 32 * u, 32 * u, qf, df, c, dp);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            p[i] = __builtin_amdgcn_exp2f(fmaf(c[i], c2, -lse2));
+            x[i] = p[i] * (dp[i] - delta);
+          }
+        }
+        if (!all) {
+          rarely();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (!mask.sees(qi, j0 + 4 * (lane >> 5) + 32 * u + walked(i))) x[i] = 0.f, p[i] = 0.f;
+        }
+        if constexpr (C::FIX && !SECOND)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) off += x[i];
+        by_columns<L, SECOND ? 1 : NP, PK>(acc, at, lds, 32 * u, x, pk, p);
+      }
+      if constexpr (L::BUFS == 1) __syncthreads();
+      if (it + 1 < count) ks.store(lds + fill), vs.store(lds + fill + L::BYTES);
+      at.flip();
+    }
+    if constexpr (C::FIX) {
+      if constexpr (!SECOND) {
+        off += __shfl_xor(off, 32, 64);
+        if (lane < 32) stat[wave][lane] = off;
+      }
+      __syncthreads();  // also: the tiles are read
+      off = stat[WIDE ? wave : 0][lane & 31];
+      if constexpr (!WIDE)
+#pragma unroll
+        for (int w = 1; w < N; ++w) off += stat[w][lane & 31];
+      delta += off;
+      if constexpr (PK) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[t] -= off * pk[t];
+      } else {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if constexpr (SECOND) meet[(t * 16 + i) * 64] = off * acc[t][i];
+        __syncthreads();
+        if constexpr (!SECOND)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[t][i] -= meet[(t * 16 + i) * 64];
+      }
+    }
+    if constexpr (!WIDE) {
+      __syncthreads();
+      if constexpr (SECOND) {
+        __syncthreads();  // add_waves has one
+        return;
+      }
+      add_waves<N>(acc, wave, lds);
+      if (qi >= s.n) return;
+      store_own<TO, N>(out, pitch, acc, wave, a.scale, a.D);
+      if (wave > 0) return;
+    } else {
+      if (SECOND || qi >= s.n) return;
+      store_held<TO, NT>(out, pitch, acc, a.scale, a.D);
+    }
+    if (lane < 32) reinterpret_cast<float*>(a.ws)[(s.start + qi) * a.Hq + h] = delta;
+  };
+  if constexpr (C::APART) {
+    if (wave_id() < N) walk(std::integral_constant<int, kFirst>{});
+    else walk(std::integral_constant<int, kSecond>{});
   } else {
-    if (qi >= s.n) return;
-    store_held<TO, NT>(out, pitch, acc, a.scale, a.D);
+    walk(std::integral_constant<int, kBoth>{});
   }
-  if (lane < 32) reinterpret_cast<float*>(a.ws)[(s.start + qi) * a.Hq + h] = delta;
 }
 
 // The work of dK and dV: steps (a tile of queries of one head, against a tile of
-// kBlock keys), for a sequence and key head key tile by key tile, in each head by
+// BLOCK keys), for a sequence and key head key tile by key tile, in each head by
 // head.  Key tile t is seen by query tiles from its own on: to the sequence's end
 // (no window, or first tokens in it), else `reach` of them.
-template <int R>  // rows of a query tile
+template <int R, int BLOCK>  // rows of a query tile and of a key tile
 struct Steps {
-  static constexpr int PER = kBlock / R;  // query tiles of a key tile's length
+  static constexpr int PER = BLOCK / R;  // query tiles of a key tile's length
   int group, tiles, queries, sinks, reach;
   __host__ __device__ __forceinline__ Steps(int64_t n, int group, int64_t window, int64_t sink)
-      : group(group), tiles(static_cast<int>((n + kBlock - 1) / kBlock)), queries(static_cast<int>((n + R - 1) / R)),
-        sinks(window ? static_cast<int>((sink + kBlock - 1) / kBlock) : tiles),
-        reach(static_cast<int>((kBlock - 2 + window) / R + 1)) {
+      : group(group), tiles(static_cast<int>((n + BLOCK - 1) / BLOCK)), queries(static_cast<int>((n + R - 1) / R)),
+        sinks(window ? static_cast<int>((sink + BLOCK - 1) / BLOCK) : tiles),
+        reach(static_cast<int>((BLOCK - 2 + window) / R + 1)) {
     if (sinks > tiles) sinks = tiles;
   }
   // query tiles that see key tile t
@@ -670,13 +729,13 @@ struct Steps {
 };
 
 // All steps of a batch, cut into one share for each workgroup.
-template <int R>
-__device__ __forceinline__ Steps<R> steps_of(const AttnArgs& a, int64_t b) {
-  return Steps<R>(span(a, b).n, a.Hq / a.Hk, a.window, a.sinks);
+template <int R, int BLOCK>
+__device__ __forceinline__ Steps<R, BLOCK> steps_of(const AttnArgs& a, int64_t b) {
+  return Steps<R, BLOCK>(span(a, b).n, a.Hq / a.Hk, a.window, a.sinks);
 }
-template <int R>
+template <int R, int BLOCK>
 __device__ __forceinline__ int64_t steps_all(const AttnArgs& a, int64_t b) {
-  const Steps<R> s = steps_of<R>(a, b);
+  const Steps<R, BLOCK> s = steps_of<R, BLOCK>(a, b);
   return s.before(s.tiles) * a.Hk;
 }
 __device__ __forceinline__ int64_t shfl64(int64_t x, int lane) {
@@ -694,12 +753,12 @@ __device__ __forceinline__ int64_t sums64(int64_t x) {
 }
 // A step's place: its sequence (B: past the last), key head, key tile, and step in the
 // tile.
-template <int R> struct Place {
+template <int R, int BLOCK> struct Place {
   int64_t b, step;
   int kh, tile;
   __device__ __forceinline__ Place(const AttnArgs& a, int64_t x) : b(0), step(0), kh(0), tile(0) {
     if (!a.cu) {
-      const int64_t each = steps_all<R>(a, 0);
+      const int64_t each = steps_all<R, BLOCK>(a, 0);
       b = x / each;
       x -= b * each;
     } else {
@@ -708,7 +767,7 @@ template <int R> struct Place {
           b = a.B;
           return;
         }
-        const int64_t own = b + lane_id() < a.B ? steps_all<R>(a, b + lane_id()) : 0, upto = sums64(own);
+        const int64_t own = b + lane_id() < a.B ? steps_all<R, BLOCK>(a, b + lane_id()) : 0, upto = sums64(own);
         const uint64_t past = __ballot(upto > x);
         if (past) {
           const int at = __builtin_ctzll(past);
@@ -719,7 +778,7 @@ template <int R> struct Place {
         x -= shfl64(upto, 63);
       }
     }
-    const Steps<R> s = steps_of<R>(a, b);
+    const Steps<R, BLOCK> s = steps_of<R, BLOCK>(a, b);
     const int64_t head = s.before(s.tiles);
     kh = static_cast<int>(x / head);
     x -= kh * head;
@@ -727,13 +786,13 @@ template <int R> struct Place {
     step = x - s.before(tile);
   }
 };
-template <int R>
+template <int R, int BLOCK>
 __device__ __forceinline__ int64_t share_of(const AttnArgs& a, int shares) {
   int64_t all = 0;
   if (!a.cu) {
-    all = steps_all<R>(a, 0) * a.B;
+    all = steps_all<R, BLOCK>(a, 0) * a.B;
   } else {
-    for (int64_t b = 0; b < a.B; b += 64) all += shfl64(sums64(b + lane_id() < a.B ? steps_all<R>(a, b + lane_id()) : 0), 63);
+    for (int64_t b = 0; b < a.B; b += 64) all += shfl64(sums64(b + lane_id() < a.B ? steps_all<R, BLOCK>(a, b + lane_id()) : 0), 63);
   }
   return max(int64_t(1), (all + shares - 1) / shares);
 }
@@ -743,21 +802,21 @@ __device__ __forceinline__ int64_t share_of(const AttnArgs& a, int shares) {
 struct Parts {
   float *delta, *sums;
 };
-template <int DP>
+template <int DP, int BLOCK>
 __device__ __forceinline__ float* part_of(const Parts& p, int64_t share, bool end) {
-  return p.sums + (2 * share + end) * (2 * kBlock * DP);
+  return p.sums + (2 * share + end) * (2 * BLOCK * DP);
 }
 
 template <typename T, typename TO, int DP, int NP>
-__global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs a, Parts parts) {
+__global__ __launch_bounds__(256, (kResident<T, DP>)) void attn_dkv_kernel(AttnArgs a, Parts parts) {
+  constexpr int N = kBlocks<T, DP>, BLOCK = kHeld * N;
   using L = Tile<T, DP>;
   constexpr int NT = DP / 32, R = L::ROWS;
   __shared__ __align__(16) char lds[2 * L::PAIR];
   __shared__ __align__(16) float stat[2][2][R];
-  const int group = a.Hq / a.Hk, lane = lane_id(), wave = wave_id();
-  const int64_t share = uniform(share_of<R>(a, gridDim.x));
-  int64_t x = share * blockIdx.x;
-  Place<R> at(a, x);
+  const int group = a.Hq / a.Hk, lane = lane_id(), wave = wave_id() % N;
+  const int64_t share = uniform(share_of<R, BLOCK>(a, gridDim.x));
+  Place<R, BLOCK> at(a, share * blockIdx.x);
   const Mask mask(a);
   const float c2 = a.scale * kLog2e;
   const int64_t pitch = static_cast<int64_t>(a.Hq) * a.D, kp = static_cast<int64_t>(a.Hk) * a.D;
@@ -765,8 +824,8 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs a, Parts part
     const int64_t b = uniform(at.b);
     if (b >= a.B) return;
     const Span s{uniform(span(a, b).start), uniform(span(a, b).n)};
-    const Steps<R> steps(s.n, group, a.window, a.sinks);
-    const int kh = uniform(at.kh), kt = uniform(at.tile), block0 = kt * kBlock;
+    const Steps<R, BLOCK> steps(s.n, group, a.window, a.sinks);
+    const int kh = uniform(at.kh), kt = uniform(at.tile), block0 = kt * BLOCK;
     const int per = steps.seen(kt);
     const int64_t total = static_cast<int64_t>(per) * group, first = uniform(at.step);
     const int count = uniform(static_cast<int>(min(left, total - first)));
@@ -811,53 +870,68 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs a, Parts part
     };
     int next0 = tile * R;
     load();
-    u32x4 kf[L::KF], vf[L::KF];
-    load_held<L>(rows_of<T>(a.k, s.start, s.n, a.k_row, kh, a.D), j0, kf);
-    load_held<L>(rows_of<T>(a.v, s.start, s.n, a.v_row, kh, a.D), j0, vf);
-    f32x16 dk[NT], dv[NT];
+    // all steps of a wave, which forms dV, dK (the second sum) or both
+    auto walk = [&](auto what) {
+      constexpr int WHAT = decltype(what)::value;
+      constexpr bool VALUES = WHAT != kSecond, KEYS = WHAT != kFirst;
+      u32x4 kf[L::KF], vf[KEYS ? L::KF : 1];
+      load_held<L>(rows_of<T>(a.k, s.start, s.n, a.k_row, kh, a.D), j0, kf);
+      if constexpr (KEYS) load_held<L>(rows_of<T>(a.v, s.start, s.n, a.v_row, kh, a.D), j0, vf);
+      f32x16 dk[KEYS ? NT : 1], dv[VALUES ? NT : 1];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) dk[t] = zero16(), dv[t] = zero16();
-    Lane<L> mine(0);
-    store(0);
-    for (int it = 0; it < count; ++it) {
-      const int i0 = next0;
-      next0 = tile * R;
-      __syncthreads();
-      if (it + 1 < count) load();
-      fill ^= L::PAIR;
-      const bool all = mask.all(i0, i0 + R - 1, j0, j1);
-      const float* lse = stat[it & 1][0] + 4 * (lane >> 5);
-#pragma unroll
-      for (int u = 0; u < R / 32; ++u) {
-        f32x16 c, dp;
-        by_rows2<L>(mine, lds, lds + L::BYTES, 32 * u, 32 * u, kf, vf, c, dp);
-        float p[16], y[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          p[i] = __builtin_amdgcn_exp2f(fmaf(c[i], c2, -lse[32 * u + walked(i)]));
-          y[i] = p[i] * (dp[i] - lse[R + 32 * u + walked(i)]);
-        }
-        if (!all) {
-          rarely();
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (!mask.sees(i0 + 4 * (lane >> 5) + 32 * u + walked(i), kj)) p[i] = 0.f, y[i] = 0.f;
-        }
-        by_columns<L, NP>(dv, mine, lds + L::BYTES, 32 * u, p);
-        by_columns<L, NP>(dk, mine, lds, 32 * u, y);
+      for (int t = 0; t < NT; ++t) {
+        if constexpr (KEYS) dk[t] = zero16();
+        if constexpr (VALUES) dv[t] = zero16();
       }
-      if (it + 1 < count) store(it + 1 & 1);
-      mine.flip();
-    }
-    __syncthreads();  // the tiles are read
-    if (!whole) {
-      float* to = part_of<DP>(parts, blockIdx.x, !begun) + wave * kHeld * DP;
-      store_held<float, NT>(to, DP, dk, a.scale, DP);
-      store_held<float, NT>(to + kBlock * DP, DP, dv, 1.f, DP);
-    } else if (kj < s.n) {
-      const int64_t to = (s.start + j0) * kp + static_cast<int64_t>(kh) * a.D;
-      store_held<TO, NT>(static_cast<TO*>(a.dk) + to, kp, dk, a.scale, a.D);
-      store_held<TO, NT>(static_cast<TO*>(a.dv) + to, kp, dv, 1.f, a.D);
+      Lane<L> mine(0);
+      store(0);
+      for (int it = 0; it < count; ++it) {
+        const int i0 = next0;
+        next0 = tile * R;
+        __syncthreads();
+        if (it + 1 < count) load();
+        fill ^= L::PAIR;
+        const bool all = mask.all(i0, i0 + R - 1, j0, j1);
+        const float* lse = stat[it & 1][0] + 4 * (lane >> 5);
+#pragma unroll
+        for (int u = 0; u < R / 32; ++u) {
+          f32x16 c, dp;
+          float p[16], y[16];
+          if constexpr (KEYS) by_rows2<L>(mine, lds, lds + L::BYTES, 32 * u, 32 * u, kf, vf, c, dp);
+          else c = by_rows<L>(mine, lds, 32 * u, kf);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            p[i] = __builtin_amdgcn_exp2f(fmaf(c[i], c2, -lse[32 * u + walked(i)]));
+            if constexpr (KEYS) y[i] = p[i] * (dp[i] - lse[R + 32 * u + walked(i)]);
+          }
+          if (!all) {
+            rarely();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (!mask.sees(i0 + 4 * (lane >> 5) + 32 * u + walked(i), kj)) p[i] = 0.f, y[i] = 0.f;
+          }
+          if constexpr (VALUES) by_columns<L, NP>(dv, mine, lds + L::BYTES, 32 * u, p);
+          if constexpr (KEYS) by_columns<L, NP>(dk, mine, lds, 32 * u, y);
+        }
+        if (it + 1 < count) store(it + 1 & 1);
+        mine.flip();
+      }
+      __syncthreads();  // the tiles are read
+      if (!whole) {
+        float* to = part_of<DP, BLOCK>(parts, blockIdx.x, !begun) + wave * kHeld * DP;
+        if constexpr (KEYS) store_held<float, NT>(to, DP, dk, a.scale, DP);
+        if constexpr (VALUES) store_held<float, NT>(to + BLOCK * DP, DP, dv, 1.f, DP);
+      } else if (kj < s.n) {
+        const int64_t to = (s.start + j0) * kp + static_cast<int64_t>(kh) * a.D;
+        if constexpr (KEYS) store_held<TO, NT>(static_cast<TO*>(a.dk) + to, kp, dk, a.scale, a.D);
+        if constexpr (VALUES) store_held<TO, NT>(static_cast<TO*>(a.dv) + to, kp, dv, 1.f, a.D);
+      }
+    };
+    if constexpr (kApart<T, DP>) {
+      if (wave_id() < N) walk(std::integral_constant<int, kFirst>{});
+      else walk(std::integral_constant<int, kSecond>{});
+    } else {
+      walk(std::integral_constant<int, kBoth>{});
     }
   }
 }
@@ -866,31 +940,31 @@ __global__ __launch_bounds__(256, 1) void attn_dkv_kernel(AttnArgs a, Parts part
 // added in their order.  blockIdx.y: 16 keys of dK or of dV.
 template <typename T, typename TO, int DP>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Parts parts) {
-  constexpr int R = El<T>::TILE, UNITS = DP / 4, KEYS = 16;
-  const int64_t share = share_of<R>(a, gridDim.x), end = share * (blockIdx.x + 1);
-  const Place<R> at(a, end - 1);
+  constexpr int R = El<T>::TILE, BLOCK = kHeld * kBlocks<T, DP>, UNITS = DP / 4, KEYS = 16;
+  const int64_t share = share_of<R, BLOCK>(a, gridDim.x), end = share * (blockIdx.x + 1);
+  const Place<R, BLOCK> at(a, end - 1);
   if (at.b >= a.B) return;
   const Span s = span(a, at.b);
-  const int64_t total = static_cast<int64_t>(Steps<R>(s.n, a.Hq / a.Hk, a.window, a.sinks).seen(at.tile)) * (a.Hq / a.Hk);
+  const int64_t total = static_cast<int64_t>(Steps<R, BLOCK>(s.n, a.Hq / a.Hk, a.window, a.sinks).seen(at.tile)) * (a.Hq / a.Hk);
   const int64_t begin = end - 1 - at.step;
   if (begin < end - share || begin + total <= end) return;
   const int more = static_cast<int>((begin + total - end + share - 1) / share);
-  const int which = blockIdx.y / (kBlock / KEYS), key0 = blockIdx.y % (kBlock / KEYS) * KEYS;
+  const int which = blockIdx.y / (BLOCK / KEYS), key0 = blockIdx.y % (BLOCK / KEYS) * KEYS;
   const int64_t kp = static_cast<int64_t>(a.Hk) * a.D;
   for (int x = threadIdx.x; x < KEYS * UNITS; x += 256) {
     const int key = key0 + x / UNITS, d = x % UNITS * 4;
-    if (at.tile * kBlock + key >= s.n || d >= a.D) continue;
-    const int64_t from = (static_cast<int64_t>(which) * kBlock + key) * DP + d;
+    if (at.tile * BLOCK + key >= s.n || d >= a.D) continue;
+    const int64_t from = (static_cast<int64_t>(which) * BLOCK + key) * DP + d;
     float sum[4];
-    ld4<float>(part_of<DP>(parts, blockIdx.x, true) + from, sum);
+    ld4<float>(part_of<DP, BLOCK>(parts, blockIdx.x, true) + from, sum);
 #pragma unroll 4
     for (int i = 1; i <= more; ++i) {
       float y[4];
-      ld4<float>(part_of<DP>(parts, blockIdx.x + i, false) + from, y);
+      ld4<float>(part_of<DP, BLOCK>(parts, blockIdx.x + i, false) + from, y);
 #pragma unroll
       for (int k = 0; k < 4; ++k) sum[k] += y[k];
     }
-    store4<TO>(static_cast<TO*>(which ? a.dv : a.dk) + (s.start + at.tile * kBlock + key) * kp +
+    store4<TO>(static_cast<TO*>(which ? a.dv : a.dk) + (s.start + at.tile * BLOCK + key) * kp +
                    static_cast<int64_t>(at.kh) * a.D + d,
                sum);
   }
@@ -900,33 +974,27 @@ int64_t ceil_div(int64_t x, int64_t y) { return (x + y - 1) / y; }
 
 // Workgroups of the (dK, dV) kernel: as many as the card holds at once, each with
 // kLeast steps or more.
-constexpr int64_t kHold = 256, kLeast = 2;
-int shares_of(const AttnArgs& a) {
+constexpr int64_t kLeast = 2;
+template <typename T, int DP>
+int shares_for(const AttnArgs& a) {
   // a ragged batch has no more steps than its rows as sequences of the longest length
   const int64_t n = std::min(a.T, a.rows), seqs = std::min(a.B, ceil_div(a.rows, n) + 1);
-  int64_t each;
-  if (a.io_bf16) {
-    const Steps<El<bf16_t>::TILE> s(n, a.Hq / a.Hk, a.window, a.sinks);
-    each = s.before(s.tiles);
-  } else {
-    const Steps<El<float>::TILE> s(n, a.Hq / a.Hk, a.window, a.sinks);
-    each = s.before(s.tiles);
-  }
-  return static_cast<int>(std::max<int64_t>(1, std::min(kHold, each * a.Hk * seqs / kLeast)));
+  const Steps<El<T>::TILE, kHeld * kBlocks<T, DP>> s(n, a.Hq / a.Hk, a.window, a.sinks);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(256 * kResident<T, DP>, s.before(s.tiles) * a.Hk * seqs / kLeast)));
 }
-int padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+template <typename T, int DP>
 size_t parts_of(const AttnArgs& a, int shares, Parts* p) {
   const size_t delta = (static_cast<size_t>(a.rows) * a.Hq * sizeof(float) + 255) / 256 * 256;
   p->delta = reinterpret_cast<float*>(a.ws);
   p->sums = reinterpret_cast<float*>(a.ws + delta);
-  return delta + (shares > 1 ? static_cast<size_t>(shares) * 4 * kBlock * padded(a.D) * sizeof(float) : 0);
+  return delta + (shares > 1 ? static_cast<size_t>(shares) * 4 * kHeld * kBlocks<T, DP> * DP * sizeof(float) : 0);
 }
 
 // Whether the kernels that hold queries give each wave 32 of its own: where that
-// fills the card, or the other layout's tiles do not fit LDS.
-template <typename T, int DP>
+// fills the card, or where 128 rows of both tensors do not fit LDS.
+template <typename T, int DP> constexpr bool kNarrow = 256 * DP * sizeof(T) <= (128 << 10);
 bool wide(const AttnArgs& a) {
-  return 256 * DP * sizeof(T) > (128 << 10) || a.B * a.Hq * ceil_div(a.T, kBlock) > kWideFrom;
+  return a.B * a.Hq * ceil_div(a.T, kBlock) > kWideFrom;
 }
 
 template <typename T, typename TO, int DP, bool WIDE>
@@ -939,8 +1007,8 @@ hipError_t fwd(const AttnArgs& a, hipStream_t st) {
 }
 template <typename T, typename TO, int DP>
 hipError_t fwd(const AttnArgs& a, hipStream_t st) {
-  if constexpr (256 * DP * sizeof(T) <= (128 << 10))
-    if (!wide<T, DP>(a)) return fwd<T, TO, DP, false>(a, st);
+  if constexpr (kNarrow<T, DP>)
+    if (!wide(a)) return fwd<T, TO, DP, false>(a, st);
   return fwd<T, TO, DP, true>(a, st);
 }
 
@@ -948,7 +1016,8 @@ template <typename T, typename TO, int DP, bool WIDE>
 hipError_t dq(const AttnArgs& a, hipStream_t st) {
   constexpr int NP = sizeof(TO) == 2 ? 2 : 3;
   ProfScope prof("attention_dq", st);
-  const dim3 grid(a.Hq, static_cast<unsigned>(ceil_div(a.T, WIDE ? kBlock : kHeld)), static_cast<unsigned>(a.B));
+  using C = Dq<T, TO, DP, WIDE>;
+  const dim3 grid(a.Hq, static_cast<unsigned>(ceil_div(a.T, C::BLOCK)), static_cast<unsigned>(a.B));
   attn_dq_kernel<T, TO, DP, NP, WIDE><<<grid, 256, 0, st>>>(a);
   return hipGetLastError();
 }
@@ -956,14 +1025,12 @@ template <typename T, typename TO, int DP>
 hipError_t bwd(const AttnArgs& a, hipStream_t st) {
   constexpr int NP = sizeof(TO) == 2 ? 2 : 3;
   hipError_t e;
-  if constexpr (256 * DP * sizeof(T) <= (128 << 10))
-    e = wide<T, DP>(a) ? dq<T, TO, DP, true>(a, st) : dq<T, TO, DP, false>(a, st);
-  else
-    e = dq<T, TO, DP, true>(a, st);
+  if constexpr (kNarrow<T, DP>) e = wide(a) ? dq<T, TO, DP, true>(a, st) : dq<T, TO, DP, false>(a, st);
+  else e = dq<T, TO, DP, true>(a, st);
   if (e != hipSuccess) return e;
-  const int shares = shares_of(a);
+  const int shares = shares_for<T, DP>(a);
   Parts parts;
-  parts_of(a, shares, &parts);
+  parts_of<T, DP>(a, shares, &parts);
   {
     ProfScope prof("attention_dkv", st);
     attn_dkv_kernel<T, TO, DP, NP><<<dim3(shares), 256, 0, st>>>(a, parts);
@@ -971,7 +1038,7 @@ hipError_t bwd(const AttnArgs& a, hipStream_t st) {
   }
   if (shares == 1) return hipSuccess;
   ProfScope prof("attention_join", st);
-  attn_join_kernel<T, TO, DP><<<dim3(shares, 2 * kBlock / 16), 256, 0, st>>>(a, parts);
+  attn_join_kernel<T, TO, DP><<<dim3(shares, 2 * kHeld * kBlocks<T, DP> / 16), 256, 0, st>>>(a, parts);
   return hipGetLastError();
 }
 
@@ -986,6 +1053,16 @@ hipError_t bwd_dim(const AttnArgs& a, hipStream_t st) {
   return a.D <= 128 ? bwd<T, TO, 128>(a, st) : bwd<T, TO, 256>(a, st);
 }
 
+template <typename T, int DP>
+size_t workspace(const AttnArgs& a) {
+  Parts p;
+  return parts_of<T, DP>(a, shares_for<T, DP>(a), &p);
+}
+template <typename T>
+size_t workspace_dim(const AttnArgs& a) {
+  return a.D <= 64 ? workspace<T, 64>(a) : a.D <= 128 ? workspace<T, 128>(a) : workspace<T, 256>(a);
+}
+
 }  // namespace
 
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t st) {
@@ -994,8 +1071,7 @@ hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t st) {
 }
 
 size_t attn_bwd_workspace(const AttnArgs& a) {
-  Parts p;
-  return parts_of(a, shares_of(a), &p);
+  return a.io_bf16 ? workspace_dim<bf16_t>(a) : workspace_dim<float>(a);
 }
 
 hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t st) {
