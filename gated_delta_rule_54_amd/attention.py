@@ -164,7 +164,7 @@ def _cache(k_cache, v_cache, table, lengths, dev):
     st = k_cache.stride()
     if st != v_cache.stride():
         raise ValueError(f"k_cache and v_cache must have the same strides, got {st} and {v_cache.stride()}")
-    if st[3] != 1 or any(s == 0 and n > 1 for s, n in zip(st, k_cache.shape)):
+    if st[3] != 1 or (0 in st and any(s == 0 and n > 1 for s, n in zip(st, k_cache.shape))):
         raise ValueError(f"a cache must have dense channels and no expanded axes, got strides {st}")
     if table.dim() != 2 or table.dtype != torch.int32:
         raise TypeError("table must be a 2-d int32 device tensor")

@@ -23,8 +23,8 @@ gdr_status done(hipError_t e) { return e == hipSuccess ? GDR_OK : gdr::record_hi
 constexpr int64_t kMaxRows = 0x7fffffffLL;
 constexpr int64_t kMaxLen = int64_t(1) << 30;  // tokens of a sequence in a cache
 
-// A row distance: 0 (dense), or at least the row, in whole 16-byte units; 64 rows
-// of it lie within 2^30 bytes, which 32-bit offsets reach.
+// A row distance: 0 (dense), or at least the row, in whole 16-byte units; the 128
+// rows of a tile lie within 2^31 bytes, which 32-bit offsets reach.
 constexpr int64_t kMaxRow = int64_t(1) << 22;
 gdr_status check_row(int64_t stride, int64_t dense, int32_t dtype) {
   if (dense > kMaxRow) return GDR_ERR_UNSUPPORTED;

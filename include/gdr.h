@@ -480,7 +480,8 @@ gdr_status gdr_cache_append_varlen(const gdr_append_problem* p, const int64_t* c
  * Lengths are read on the device; they are clamped to [0, max_len], and max_len
  * (0: max_pages * page_size, which it may not exceed) sizes the workspace and
  * the launch, so a captured call serves all lengths up to it (at most 2^30).  B *
- * Hq is at most 2^22, scale > 0, window and sinks >= 0. */
+ * Hq is at most 2^22, scale > 0, window and sinks >= 0.  Outputs must not alias
+ * inputs. */
 typedef struct gdr_cache_attention_problem {
   int64_t B;
   int32_t Hq;
@@ -504,7 +505,8 @@ gdr_status gdr_cache_attention(const gdr_cache_attention_problem* p, const void*
  * that share a key head, in a fixed order.  bf16 outputs are rounded once: the
  * probabilities (and in the VJP their gradients) enter the matrix cores as two
  * bf16 operands, as three for fp32 outputs; fp32 io is fp32 throughout.  varlen:
- * cu_seqlens as for gdr_forward_varlen.  NaN and Inf propagate: scores that are
+ * cu_seqlens as for gdr_forward_varlen.  Outputs must not alias inputs.  NaN and
+ * Inf propagate: scores that are
  * +Inf, or all -Inf, give NaN; an Inf in v or dout may come out as NaN, and Inf or
  * NaN in a token's v, k, q or dout may reach tokens of its sequence that are
  * masked from it but share a tile of 64 with ones that are not.  B and Hq are at
