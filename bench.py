@@ -440,6 +440,55 @@ def bench_linear_attention(torch, gdr, steps=10):
     return out
 
 
+def bench_attention_layer(torch, gdr, steps=5):
+    """The attention layer at the step's tokens: rotary positions and causal
+    attention under a window with sinks, its VJP through both, and one token
+    for each sequence appended to a paged cache and attended to; time per call
+    from events around back-to-back calls, bf16 in and out."""
+    gen = torch.Generator(device="cuda").manual_seed(10)
+    rn = lambda *s: torch.randn(*s, device="cuda", generator=gen).to(bf)
+    bf = torch.bfloat16
+    hq, hk, page, window = HV, HV // 4, 64, 1024
+    x, do = rn(B, T, hq + 2 * hk, D), rn(B, T, hq, D)
+    q, k, v = x[:, :, :hq], x[:, :, hq:hq + hk], x[:, :, hq + hk:]
+    pos = torch.arange(T, device="cuda").expand(B, T).contiguous()
+    freq = torch.pow(10000.0, -2.0 * torch.arange(D // 2, device="cuda") / D)
+    how = dict(window=window, sinks=4)
+
+    def forward():
+        qr, kr = gdr.gdr_rotary_forward(q, k, pos, freq, out_dtype=bf)
+        return (qr, kr) + gdr.gdr_attention_forward(qr, kr, v, out_dtype=bf, **how)
+
+    qr, kr, o, lse = forward()
+
+    def vjp():
+        dq, dk, _ = gdr.gdr_attention_backward(qr, kr, v, o, lse, do, **how)
+        gdr.gdr_rotary_backward(dq, dk, pos, freq, dq=dq, dk=dk)
+
+    table = torch.arange(B * (T // page), dtype=torch.int32, device="cuda").reshape(B, -1)
+    kc, vc = (rn(B * (T // page), page, hk, D) for _ in "kv")
+    lengths = torch.full((B,), T, device="cuda")
+
+    def token():
+        qs = gdr.gdr_cache_append(k[:, -1:], v[:, -1:], kc, vc, table, lengths, freq, q=q[:, -1:])
+        gdr.gdr_cache_attention(qs, kc, vc, table, lengths, out_dtype=bf)
+
+    out = {}
+    for name, call, reps in (("forward", forward, steps), ("vjp", vjp, steps), ("token", token, 20 * steps)):
+        for _ in range(3):
+            call()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        for _ in range(reps):
+            call()
+        e1.record()
+        torch.cuda.synchronize()
+        out[f"{name}_us"] = round(1000.0 * e0.elapsed_time(e1) / reps, 2)
+    out["config"] = (f"B={B} T={T} Hq={hq} Hk={hk} D={D}, bf16, all channels turned, window {window} and 4 sinks; token: "
+                     f"{B} sequences of {T} tokens in pages of {page}, all visible")
+    return out
+
+
 def bench_channelwise_decode(torch, gdr, t_prefill=2048, steps=128):
     """Channelwise gate: a B=1 prefill of t_prefill tokens (chunked), then
     `steps` single-token steps carrying the state in place (Hk=16, Hv=32,
@@ -662,7 +711,7 @@ def _cpu_model():
 def variants(torch, gdr, args, tokens):
     """The other measured legs: the same step with fused gates and with the
     stateless VJP, the channelwise prefill and decode, the ragged prefill, the
-    backward sweep, and linear attention with its norm."""
+    backward sweep, linear attention with its norm, and the attention layer."""
     fms, _, _ = bench_chunked(torch, gdr, args.steps, args.warmup, fused_gates=True)
     sms, _, skern = bench_chunked(torch, gdr, args.steps, args.warmup, saved=False)
     return {
@@ -677,6 +726,7 @@ def variants(torch, gdr, args, tokens):
         "ragged_prefill": bench_ragged(torch, gdr),
         "vjp_sweep": bench_vjp_sweep(torch, gdr),
         "linear_attention": bench_linear_attention(torch, gdr),
+        "attention_layer": bench_attention_layer(torch, gdr),
     }
 
 

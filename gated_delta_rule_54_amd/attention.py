@@ -58,6 +58,26 @@ class GdrAttentionProblem(ctypes.Structure):
                 ("q_row", ctypes.c_int64), ("k_row", ctypes.c_int64), ("v_row", ctypes.c_int64)]
 
 
+# A call for a few tokens is bound by the host.  What a call works out from its
+# operands' shapes, strides, types and devices, and from its options, is kept by these
+# (never by a tensor or its address): the checks that passed, the problem, the
+# workspace's size.
+_plans = {}
+_MOST = 4096
+
+
+def _meta(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+
+
+def _plan(key, make):
+    plan = make()
+    if len(_plans) >= _MOST:
+        _plans.clear()
+    _plans[key] = plan
+    return plan
+
+
 # ---- rotary positions -----------------------------------------------------
 
 def _rotary(freq, section, adjacent, cycled, dev):
@@ -98,6 +118,24 @@ def _turn(entry, q, k, pos, freq, section, adjacent, cycled, out_dtype, q_out, k
     if not _here(dev, stream):
         with _on(dev, stream):
             return _turn(entry, q, k, pos, freq, section, adjacent, cycled, out_dtype, q_out, k_out, None)
+    section = None if section is None else tuple(section)
+    key = (entry, _meta(q), _meta(k), _meta(pos), _meta(freq), _meta(q_out), _meta(k_out), section, adjacent, cycled,
+           out_dtype)
+    plan = _plans.get(key) or _plan(key, lambda: _turn_plan(q, k, pos, freq, section, adjacent, cycled, out_dtype,
+                                                            q_out, k_out, dev))
+    ref, q_shape, k_shape = plan
+    if q_out is None:
+        q_out = torch.empty(q_shape, dtype=out_dtype, device=dev)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k_shape, dtype=out_dtype, device=dev)
+    st = getattr(lib(), entry)(ref, q.data_ptr(), _ptr(k), _ptr(pos), _ptr(freq), q_out.data_ptr(), _ptr(k_out),
+                               _raw_stream(dev.index))
+    if st:
+        _check_status(st, entry)
+    return q_out, k_out
+
+
+def _turn_plan(q, k, pos, freq, section, adjacent, cycled, out_dtype, q_out, k_out, dev):
     rows, Hq, D = _heads(q, "q")
     Hk = 0
     if k is not None:
@@ -109,25 +147,19 @@ def _turn(entry, q, k, pos, freq, section, adjacent, cycled, out_dtype, q_out, k
     if rot.R and pos is None:
         raise ValueError("pos is required")
     _positions(pos, rot, rows, dev)
-    out = []
-    for t, to, name, H in ((q, q_out, "q_out", Hq), (k, k_out, "k_out", Hk)):
-        if t is not None and to is None:
-            to = torch.empty(rows + (H, D), dtype=out_dtype, device=dev)
-        elif t is not None:
-            _want(to, name, rows + (H, D), to.dtype, dev, False)
-        out.append(to)
-    qo, ko = out
-    if ko is not None and ko.dtype != qo.dtype:
-        raise TypeError(f"q_out is {qo.dtype}, k_out {ko.dtype}")
+    dt = out_dtype if q_out is None else q_out.dtype
+    for t, name, H in ((q_out, "q_out", Hq), (k_out, "k_out", Hk)):
+        if t is not None:
+            _want(t, name, rows + (H, D), t.dtype, dev, False)
+    if k is not None and (out_dtype if k_out is None else k_out.dtype) != dt:
+        raise TypeError(f"q_out is {dt}, k_out {out_dtype if k_out is None else k_out.dtype}")
     n = 1
     for s in rows:
         n *= s
-    prob = GdrRotaryProblem(n, Hq, Hk, D, _dtype(q.dtype, "q"), _dtype(qo.dtype, "q_out"), rot, _row_stride(q, "q"),
-                            0 if k is None else _row_stride(k, "k"), _row_stride(qo, "q_out"),
-                            0 if ko is None else _row_stride(ko, "k_out"))
-    _check_status(getattr(lib(), entry)(ctypes.byref(prob), _ptr(q), _ptr(k), _ptr(pos), _ptr(freq), _ptr(qo),
-                                        _ptr(ko), _raw_stream(dev.index)), entry)
-    return qo, ko
+    strides = [0 if t is None else _row_stride(t, name)
+               for t, name in ((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out"))]
+    prob = GdrRotaryProblem(n, Hq, Hk, D, _dtype(q.dtype, "q"), _dtype(dt, "q_out"), rot, *strides)
+    return ctypes.byref(prob), rows + (Hq, D), rows + (Hk, D)
 
 
 def gdr_rotary_forward(q, k, pos, freq, *, section=None, adjacent=False, cycled=False, out_dtype=torch.float32,
@@ -200,6 +232,28 @@ def gdr_cache_append(k, v, k_cache, v_cache, table, lengths, freq=None, pos=None
                                     max_seqlen=max_seqlen)
     if k.dim() != 4:
         raise ValueError("k must be [B, T, Hk, D]")
+    dims = k.shape[:2] if cu_seqlens is None else _ragged_dims(k, cu_seqlens, max_seqlen)
+    section = None if section is None else tuple(section)
+    key = ("append", _meta(k), _meta(v), _meta(k_cache), _meta(v_cache), _meta(table), _meta(lengths), _meta(freq),
+           _meta(pos), _meta(q), _meta(q_out), _meta(cu_seqlens), dims, section, adjacent, cycled)
+    plan = _plans.get(key) or _plan(key, lambda: _append_plan(k, v, k_cache, v_cache, table, lengths, freq, pos, q,
+                                                              section, adjacent, cycled, q_out, cu_seqlens, dims, dev))
+    ref, shape = plan
+    if q is not None and q_out is None:
+        q_out = torch.empty(shape, dtype=k_cache.dtype, device=dev)
+    args = (lengths.data_ptr(), table.data_ptr(), _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(pos), _ptr(freq),
+            _ptr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), _raw_stream(dev.index))
+    if cu_seqlens is not None:
+        st = lib().gdr_cache_append_varlen(ref, cu_seqlens.data_ptr(), *args)
+    else:
+        st = lib().gdr_cache_append(ref, *args)
+    if st:
+        _check_status(st, "gdr_cache_append")
+    return q_out
+
+
+def _append_plan(k, v, k_cache, v_cache, table, lengths, freq, pos, q, section, adjacent, cycled, q_out, cu_seqlens,
+                 dims, dev):
     cache = _cache(k_cache, v_cache, table, lengths, dev)
     rows = tuple(k.shape[:2])
     _want(k, "k", rows + (cache.Hk, cache.D), k.dtype, dev, False)
@@ -208,31 +262,21 @@ def gdr_cache_append(k, v, k_cache, v_cache, table, lengths, freq=None, pos=None
     if q is not None:
         Hq = q.shape[2] if q.dim() == 4 else 0
         _want(q, "q", rows + (Hq, cache.D), k.dtype, dev, False)
-        if q_out is None:
-            q_out = torch.empty(rows + (Hq, cache.D), dtype=k_cache.dtype, device=dev)
-        else:
-            _want(q_out, "q_out", rows + (Hq, cache.D), k_cache.dtype, dev)
+        _want(q_out, "q_out", rows + (Hq, cache.D), k_cache.dtype, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
     rot = _rotary(freq, section, adjacent, cycled, dev)
     if rot.axes > 1 and pos is None:
         raise ValueError("pos is required where there are several axes")
     _positions(pos, rot, rows, dev)
-    B, T = rows if cu_seqlens is None else _ragged_dims(k, cu_seqlens, max_seqlen)
+    B, T = dims
     if cu_seqlens is not None and not cu_seqlens.is_contiguous():
         raise ValueError("cu_seqlens must be contiguous")
     if B != table.shape[0]:
         raise ValueError(f"table has {table.shape[0]} sequences, the batch {B}")
     prob = GdrAppendProblem(B, min(T, rows[1]), rows[0] * rows[1], Hq, _dtype(k.dtype, "k"), rot, cache,
                             0 if q is None else _row_stride(q, "q"), _row_stride(k, "k"), _row_stride(v, "v"))
-    args = (_ptr(lengths), _ptr(table), _ptr(q), _ptr(k), _ptr(v), _ptr(pos), _ptr(freq), _ptr(q_out),
-            _ptr(k_cache), _ptr(v_cache), _raw_stream(dev.index))
-    if cu_seqlens is not None:
-        st = lib().gdr_cache_append_varlen(ctypes.byref(prob), _ptr(cu_seqlens), *args)
-    else:
-        st = lib().gdr_cache_append(ctypes.byref(prob), *args)
-    _check_status(st, "gdr_cache_append")
-    return q_out
+    return ctypes.byref(prob), rows + (Hq, cache.D)
 
 
 def gdr_cache_attention_workspace(prob):
@@ -268,37 +312,47 @@ def gdr_cache_attention(q, k_cache, v_cache, table, lengths, *, scale=None, wind
         with _on(dev, stream):
             return gdr_cache_attention(q, k_cache, v_cache, table, lengths, scale=scale, window=window, sinks=sinks,
                                        max_len=max_len, out_dtype=out_dtype, o=o, lse=lse)
+    key = ("cache", _meta(q), _meta(k_cache), _meta(v_cache), _meta(table), _meta(lengths), _meta(o),
+           lse if lse is None or lse is True else _meta(lse), scale, window, sinks, max_len, out_dtype)
+    plan = _plans.get(key) or _plan(key, lambda: _cache_attention_plan(
+        q, k_cache, v_cache, table, lengths, scale, window, sinks, max_len, out_dtype, o, lse, dev))
+    ref, shape, nws = plan
+    if o is None:
+        o = torch.empty(shape, dtype=out_dtype, device=dev)
+    if lse is True:
+        lse = torch.empty(shape[:3], dtype=torch.float32, device=dev)
+    ws = _workspace(nws, dev)
+    st = lib().gdr_cache_attention(ref, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(),
+                                   lengths.data_ptr(), o.data_ptr(), _ptr(lse), _ptr(ws), nws, _raw_stream(dev.index))
+    if st:
+        _check_status(st, "gdr_cache_attention")
+    return o, lse
+
+
+def _cache_attention_plan(q, k_cache, v_cache, table, lengths, scale, window, sinks, max_len, out_dtype, o, lse, dev):
     if q.dim() != 4:
         raise ValueError("q must be [B, 1, Hq, D]")
     cache = _cache(k_cache, v_cache, table, lengths, dev)
     shape = (table.shape[0], 1, q.shape[2], cache.D)
     _want(q, "q", shape, k_cache.dtype, dev, False)
-    if o is None:
-        o = torch.empty(shape, dtype=out_dtype, device=dev)
-    else:
+    if o is not None:
         _want(o, "o", shape, o.dtype, dev)
-    if lse is True:
-        lse = torch.empty(shape[:3], dtype=torch.float32, device=dev)
-    else:
+    if lse is not True:
         _want(lse, "lse", shape[:3], torch.float32, dev)
     span = _span(window, sinks)
     if max_len is None:
         max_len = 0
     elif max_len < 1:
         raise ValueError("max_len must be at least 1")
-    prob = GdrCacheAttentionProblem(shape[0], shape[2], _dtype(o.dtype, "o"), cache, _row_stride(q, "q"), max_len,
-                                    span, sinks, cache.D ** -0.5 if scale is None else scale)
-    ws = _workspace(gdr_cache_attention_workspace(prob), dev)
-    _check_status(lib().gdr_cache_attention(ctypes.byref(prob), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(table),
-                                            _ptr(lengths), _ptr(o), _ptr(lse), _ptr(ws),
-                                            0 if ws is None else ws.numel(), _raw_stream(dev.index)),
-                  "gdr_cache_attention")
-    return o, lse
+    prob = GdrCacheAttentionProblem(shape[0], shape[2], _dtype(out_dtype if o is None else o.dtype, "out_dtype"), cache,
+                                    _row_stride(q, "q"), max_len, span, sinks,
+                                    cache.D ** -0.5 if scale is None else scale)
+    return ctypes.byref(prob), shape, gdr_cache_attention_workspace(prob)
 
 
 # ---- attention over whole sequences ---------------------------------------
 
-def _attention_problem(q, k, v, scale, window, sinks, out_dtype, cu_seqlens, max_seqlen):
+def _attention_problem(q, k, v, scale, window, sinks, out_dtype, cu_seqlens, dims):
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q, k, v must be [B, T, heads, dim]")
     dev = _device(q, "q")
@@ -307,7 +361,7 @@ def _attention_problem(q, k, v, scale, window, sinks, out_dtype, cu_seqlens, max
     Hk = k.shape[2]
     _want(k, "k", rows + (Hk, D), q.dtype, dev, False)
     _want(v, "v", rows + (Hk, D), q.dtype, dev, False)
-    B, T = rows if cu_seqlens is None else _ragged_dims(q, cu_seqlens, max_seqlen)
+    B, T = rows if cu_seqlens is None else dims
     if cu_seqlens is not None:
         if not cu_seqlens.is_contiguous():
             raise ValueError("cu_seqlens must be contiguous")
@@ -330,19 +384,26 @@ def gdr_attention_forward(q, k, v, *, scale=None, window=None, sinks=0, out_dtyp
         with _on(dev, stream):
             return gdr_attention_forward(q, k, v, scale=scale, window=window, sinks=sinks, out_dtype=out_dtype, o=o,
                                          cu_seqlens=cu_seqlens, max_seqlen=max_seqlen)
-    prob = _attention_problem(q, k, v, scale, window, sinks, out_dtype if o is None else o.dtype, cu_seqlens,
-                              max_seqlen)
+    dims = None if cu_seqlens is None else _ragged_dims(q, cu_seqlens, max_seqlen)
+    key = ("forward", _meta(q), _meta(k), _meta(v), _meta(o), _meta(cu_seqlens), dims, scale, window, sinks, out_dtype)
+
+    def make():
+        if o is not None:
+            _want(o, "o", tuple(q.shape), o.dtype, dev)
+        return ctypes.byref(_attention_problem(q, k, v, scale, window, sinks, out_dtype if o is None else o.dtype,
+                                               cu_seqlens, dims)), tuple(q.shape)
+
+    ref, shape = _plans.get(key) or _plan(key, make)
     if o is None:
-        o = torch.empty(q.shape, dtype=out_dtype, device=dev)
-    else:
-        _want(o, "o", tuple(q.shape), o.dtype, dev)
-    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
-    args = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _raw_stream(dev.index))
+        o = torch.empty(shape, dtype=out_dtype, device=dev)
+    lse = torch.empty(shape[:3], dtype=torch.float32, device=dev)
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), _raw_stream(dev.index))
     if cu_seqlens is not None:
-        st = lib().gdr_attention_forward_varlen(ctypes.byref(prob), _ptr(cu_seqlens), *args)
+        st = lib().gdr_attention_forward_varlen(ref, cu_seqlens.data_ptr(), *args)
     else:
-        st = lib().gdr_attention_forward(ctypes.byref(prob), *args)
-    _check_status(st, "gdr_attention_forward")
+        st = lib().gdr_attention_forward(ref, *args)
+    if st:
+        _check_status(st, "gdr_attention_forward")
     return o, lse
 
 
@@ -364,20 +425,29 @@ def gdr_attention_backward(q, k, v, o, lse, dout, *, scale=None, window=None, si
         with _on(dev, stream):
             return gdr_attention_backward(q, k, v, o, lse, dout, scale=scale, window=window, sinks=sinks,
                                           cu_seqlens=cu_seqlens, max_seqlen=max_seqlen)
-    prob = _attention_problem(q, k, v, scale, window, sinks, o.dtype, cu_seqlens, max_seqlen)
-    _want(o, "o", tuple(q.shape), o.dtype, dev)
-    _want(lse, "lse", tuple(q.shape[:3]), torch.float32, dev)
-    _want(dout, "dout", tuple(q.shape), q.dtype, dev)
+    dims = None if cu_seqlens is None else _ragged_dims(q, cu_seqlens, max_seqlen)
+    key = ("backward", _meta(q), _meta(k), _meta(v), _meta(o), _meta(lse), _meta(dout), _meta(cu_seqlens), dims, scale,
+           window, sinks)
+
+    def make():
+        prob = _attention_problem(q, k, v, scale, window, sinks, o.dtype, cu_seqlens, dims)
+        _want(o, "o", tuple(q.shape), o.dtype, dev)
+        _want(lse, "lse", tuple(q.shape[:3]), torch.float32, dev)
+        _want(dout, "dout", tuple(q.shape), q.dtype, dev)
+        rows = q.shape[0] * q.shape[1]
+        return ctypes.byref(prob), rows, gdr_attention_backward_workspace(prob, rows)
+
+    ref, rows, nws = _plans.get(key) or _plan(key, make)
     dq = torch.empty(q.shape, dtype=o.dtype, device=dev)
     dk = torch.empty(k.shape, dtype=o.dtype, device=dev)
     dv = torch.empty(v.shape, dtype=o.dtype, device=dev)
-    rows = q.shape[0] * q.shape[1]
-    ws = _workspace(gdr_attention_backward_workspace(prob, rows), dev)
-    args = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws),
-            0 if ws is None else ws.numel(), _raw_stream(dev.index))
+    ws = _workspace(nws, dev)
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dout.data_ptr(), dq.data_ptr(),
+            dk.data_ptr(), dv.data_ptr(), _ptr(ws), nws, _raw_stream(dev.index))
     if cu_seqlens is not None:
-        st = lib().gdr_attention_backward_varlen(ctypes.byref(prob), rows, _ptr(cu_seqlens), *args)
+        st = lib().gdr_attention_backward_varlen(ref, rows, cu_seqlens.data_ptr(), *args)
     else:
-        st = lib().gdr_attention_backward(ctypes.byref(prob), *args)
-    _check_status(st, "gdr_attention_backward")
+        st = lib().gdr_attention_backward(ref, *args)
+    if st:
+        _check_status(st, "gdr_attention_backward")
     return dq, dk, dv

@@ -23,14 +23,16 @@ gdr_status done(hipError_t e) { return e == hipSuccess ? GDR_OK : gdr::record_hi
 constexpr int64_t kMaxRows = 0x7fffffffLL;
 constexpr int64_t kMaxLen = int64_t(1) << 30;  // tokens of a sequence in a cache
 
-// A row distance: 0 (dense), or at least the row, in whole 16-byte units; the 128
-// rows of a tile lie within 2^31 bytes, which 32-bit offsets reach.
-constexpr int64_t kMaxRow = int64_t(1) << 22;
-gdr_status check_row(int64_t stride, int64_t dense, int32_t dtype) {
+// A row distance: 0 (dense), or at least the row, in whole 16-byte units.  Where tiles
+// of rows are loaded, the 128 rows of one lie within 2^31 bytes, which 32-bit offsets
+// reach; where rows are addressed one by one (in 64 bits) they may lie further apart,
+// as one token of each of a batch's long sequences does.
+constexpr int64_t kMaxRow = int64_t(1) << 22, kFarRow = int64_t(1) << 40;
+gdr_status check_row(int64_t stride, int64_t dense, int32_t dtype, int64_t most = kFarRow) {
   if (dense > kMaxRow) return GDR_ERR_UNSUPPORTED;
   if (stride == 0) return GDR_OK;
   if (stride < dense) return GDR_ERR_BAD_SHAPE;
-  if (stride > kMaxRow) return GDR_ERR_UNSUPPORTED;
+  if (stride > most) return GDR_ERR_UNSUPPORTED;
   return stride % per16(dtype) ? GDR_ERR_BAD_ALIGNMENT : GDR_OK;
 }
 gdr_status first_of(std::initializer_list<gdr_status> all) {
@@ -212,8 +214,8 @@ gdr_status check(const gdr_attention_problem* p, int64_t rows) {
   // a launch has at most 2^32 threads
   if (p->B * p->Hq * ((p->T + 127) / 128) > (1 << 23)) return GDR_ERR_UNSUPPORTED;
   const int64_t q = static_cast<int64_t>(p->Hq) * p->D, k = static_cast<int64_t>(p->Hk) * p->D;
-  return first_of({check_row(p->q_row, q, p->io_dtype), check_row(p->k_row, k, p->io_dtype),
-                   check_row(p->v_row, k, p->io_dtype)});
+  return first_of({check_row(p->q_row, q, p->io_dtype, kMaxRow), check_row(p->k_row, k, p->io_dtype, kMaxRow),
+                   check_row(p->v_row, k, p->io_dtype, kMaxRow)});
 }
 // B * T, where it is no larger than it may be
 int64_t dense_rows(const gdr_attention_problem* p) {

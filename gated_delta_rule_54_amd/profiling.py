@@ -41,7 +41,8 @@ eight SQ counters a run)
     python -m gated_delta_rule_54_amd.profiling sq DIR_S1/s_results.db DIR_S2/s_results.db --md profiles/<name>.md
 
 give each kernel's wave time split by what its waves were doing.  ``trace`` and
-``sq`` take ``--operators`` for profiles of linear attention and the group norm.
+``sq`` take ``--operators`` for profiles of linear attention and the group norm,
+``--attention`` for those of the attention layer.
 """
 
 import argparse
@@ -89,6 +90,13 @@ OPERATORS = [
     (r"norm_fwd_kernel", "norm_fwd"),
     (r"norm_bwd_kernel", "norm_bwd"),
     (r"norm_params_kernel", "norm_params"),
+    (r"attn_fwd_kernel", "attention"),
+    (r"attn_dq_kernel", "attention_dq"),
+    (r"attn_dkv_kernel", "attention_dkv"),
+    (r"attn_join_kernel", "attention_join"),
+    (r"cache_attn_kernel", "cache_attention"),
+    (r"cache_join_kernel", "cache_join"),
+    (r"rotary_kernel", "rotary"),
 ]
 COPY_PATTERN = r"calib_copy_kernel"
 
@@ -275,7 +283,7 @@ def sq(args):
         ins = [d.get(k) for k in ("SQ_INSTS_VALU", "SQ_INSTS_LDS", "SQ_INSTS_MFMA", "SQ_INSTS_SALU")]
         row.append(" / ".join(f"{x[0] / 1e6:.1f}" if x else "-" for x in ins))
         lines.append("| " + " | ".join(row) + " |")
-    lines += ["", f"Kernel sources digest: `{src_digest(args.operators)}`", ""]
+    lines += ["", f"Kernel sources digest: `{src_digest(args.operators, args.attention)}`", ""]
     text = "\n".join(lines)
     if args.md:
         with open(args.md, "w") as fh:
@@ -316,7 +324,7 @@ def trace(args):
               "|---|---|---:|---:|---:|---:|"]
     for (lab, gx, gy, gz, wx), (n, tot, least) in sorted(acc.items(), key=lambda kv: (kv[0][0], -kv[1][0])):
         lines.append(f"| {lab} | {gx} x {gy} x {gz} | {wx} | {n} | {tot / n / 1000.0:.2f} | {least / 1000.0:.2f} |")
-    lines += ["", f"Kernel sources digest: `{src_digest(args.operators)}`", ""]
+    lines += ["", f"Kernel sources digest: `{src_digest(args.operators, args.attention)}`", ""]
     text = "\n".join(lines)
     if args.md:
         with open(args.md, "w") as fh:
@@ -351,6 +359,8 @@ def main():
     for s in (k, q):
         s.add_argument("--operators", action="store_true",
                        help="the profile is of linear attention and the group norm: their sources' digest")
+        s.add_argument("--attention", action="store_true",
+                       help="the profile is of the attention layer: its sources' digest")
     args = ap.parse_args()
     {"traffic": traffic, "trace": trace, "mfma": mfma, "sq": sq}[args.cmd](args)
 

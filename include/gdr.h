@@ -411,8 +411,9 @@ typedef struct gdr_rotary_problem {
 /* q [rows, Hq, D] and k [rows, Hk, D] turned into q_out and k_out.  An output
  * may be its own input (same dtype and row distance: in place) and must not
  * overlap an input otherwise.  backward is the VJP: the outputs' gradients in,
- * the inputs' out (the opposite turn); freq and pos have no gradients.  Rows
- * and row distances as for gdr_linear_forward; at most 2^31 - 1 rows. */
+ * the inputs' out (the opposite turn); freq and pos have no gradients.  A row
+ * holds at most 2^22 elements; rows lie at most 2^40 apart, in whole 16-byte
+ * units; at most 2^31 - 1 rows. */
 gdr_status gdr_rotary_forward(const gdr_rotary_problem* p, const void* q, const void* k, const int64_t* pos,
                               const float* freq, void* q_out, void* k_out, void* hip_stream);
 gdr_status gdr_rotary_backward(const gdr_rotary_problem* p, const void* dq_out, const void* dk_out,
@@ -447,8 +448,9 @@ typedef struct gdr_cache {
  * append to one page): one of them, or a mixture, would remain.  varlen:
  * sequence b's new tokens are rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of
  * `rows` rows, its last ones; p->T bounds their number, tokens past it are not
- * stored; rows that no sequence covers are neither read nor written.  B is at
- * most 65535, B * T and rows at most 2^31 - 1. */
+ * stored; rows that no sequence covers are neither read nor written.  Row
+ * distances as for gdr_rotary_forward; B is at most 65535, B * T and rows at most
+ * 2^31 - 1. */
 typedef struct gdr_append_problem {
   int64_t B, T;                /* sequences; new tokens of each (or a bound)  */
   int64_t rows;                /* varlen: rows of q, k, v                     */

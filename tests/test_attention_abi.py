@@ -97,7 +97,7 @@ def test_bad_turns(bad, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(rows=-1), 2), (dict(Hq=0), 2), (dict(Hk=-1), 2), (dict(D=0), 2), (dict(D=40), 3), (dict(D=272), 3),
     (dict(io_dtype=2), 3), (dict(out_dtype=-1), 3), (dict(rows=1 << 31), 3), (dict(q_row=248), 2), (dict(k_row=132), 4),
-    (dict(qo_row=260), 4), (dict(ko_row=-8), 2), (dict(q_row=(1 << 22) + 8), 3), (dict(Hq=1 << 17), 3),
+    (dict(qo_row=260), 4), (dict(ko_row=-8), 2), (dict(q_row=(1 << 40) + 8), 3), (dict(Hq=1 << 17), 3),
 ])
 def test_bad_rotary(kw, status):
     assert rotary(rot(**kw), q=None) == status and rotary(rot(**kw), back=True, ko=None) == status

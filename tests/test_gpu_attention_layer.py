@@ -151,3 +151,62 @@ def test_beside_a_recurrent_layer():
         want = step(*b)
         torch.cuda.synchronize()
         assert all(torch.equal(p, w) for p, w in zip(res, want)), i
+
+
+@pytest.mark.parametrize("io", [BF, F])
+def test_last_tokens_of_long_projections(io):
+    """One token of each sequence of a long projection: rows far apart."""
+    B, T, Hk, D = 3, 9000, 2, 64
+    x = torch.randn(B, T, 8, D, device="cuda").to(io)
+    kc, vc = (torch.zeros(B * 2, 16, Hk, D, device="cuda", dtype=io) for _ in "kv")
+    table = torch.arange(B * 2, dtype=torch.int32, device="cuda").reshape(B, 2)
+    n = torch.tensor([17, 3, 32], device="cuda")
+    f, last = dev(freqs(D)), x[:, -1:]
+    assert last.stride(0) > 1 << 22
+    one = [t.clone() for t in (kc, vc)]
+    q = gdr.gdr_cache_append(last[:, :, 4:6], last[:, :, 6:], kc, vc, table, n, f, q=last[:, :, :4])
+    d = last.contiguous()
+    q1 = gdr.gdr_cache_append(d[:, :, 4:6].contiguous(), d[:, :, 6:].contiguous(), *one, table, n, f,
+                              q=d[:, :, :4].contiguous())
+    assert torch.equal(q, q1) and torch.equal(kc, one[0]) and torch.equal(vc, one[1])
+    for a, b in zip(gdr.gdr_cache_attention(last[:, :, :4], kc, vc, table, n),
+                    gdr.gdr_cache_attention(d[:, :, :4].contiguous(), kc, vc, table, n)):
+        assert torch.equal(a, b)
+    y, _ = gdr.gdr_rotary_forward(last[:, :, :4], None, (n - 1)[:, None], f, out_dtype=io)
+    assert torch.equal(y, q)
+
+
+def test_calls_alike_but_for_one_thing():
+    """Calls that differ in one shape, stride, type or option, in turn and again: each
+    is what it is alone (what a call keeps goes by all of them)."""
+    r = torch.Generator(device="cuda").manual_seed(5)
+    rn = lambda *s: torch.randn(*s, device="cuda", generator=r)
+    q, k, v, do = rn(1, 40, 4, 32), rn(1, 40, 2, 32), rn(1, 40, 2, 32), rn(1, 40, 4, 32)
+    wide = rn(1, 40, 3, 32)
+    cases = [dict(), dict(window=5), dict(window=5, sinks=1), dict(scale=0.3), dict(sinks=1)]
+    seen = []
+    for turn in range(2):
+        got = []
+        for how in cases:
+            for kk in (k, wide[:, :, :2]):
+                o, lse = gdr.gdr_attention_forward(q, kk, v, **how)
+                got += [o, lse, *gdr.gdr_attention_backward(q, kk, v, o, lse, do, **how)]
+            o, lse = gdr.gdr_attention_forward(q, k, v, out_dtype=BF, **how)
+            got += [o, lse, *gdr.gdr_attention_backward(q, k, v, o, lse, do, **how)]
+            assert o.dtype == BF
+        seen.append(got)
+    assert all(torch.equal(a, b) for a, b in zip(*seen))
+    for how, at in zip(cases, range(0, 75, 15)):
+        for kk, i in ((k, 0), (wide[:, :, :2], 5)):
+            x = [host(t[0]) for t in (q, kk, v)]
+            ref, _ = ao.attention(*x, how.get("scale", 32 ** -0.5), how.get("window"), how.get("sinks", 0))
+            assert np.abs(host(seen[0][at + i][0]) - ref).max() < 2.0 ** -13 * np.abs(x[2]).max()
+    with pytest.raises(ValueError):
+        gdr.gdr_attention_forward(q, k, v[:, :39])
+    f = dev(freqs(32))
+    pos = torch.arange(40, device="cuda")[None]
+    a = gdr.gdr_rotary_forward(q, k, pos, f)
+    b = gdr.gdr_rotary_forward(q, k, pos, f, adjacent=True)
+    c = gdr.gdr_rotary_backward(q, k, pos, f)
+    again = gdr.gdr_rotary_forward(q, k, pos, f)
+    assert torch.equal(a[0], again[0]) and not torch.equal(a[0], b[0]) and not torch.equal(a[0], c[0])
