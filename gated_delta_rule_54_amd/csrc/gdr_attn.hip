@@ -16,15 +16,34 @@
 // lane) and, where they are summed over, by columns (transposing reads); their
 // 16-byte units are permuted so that both kinds spread over the banks.
 //
-// dQ and (dK, dV) are formed by two kernels, each in a fixed order without
-// atomics.  dK and dV add up over the query heads that share a key head and over
-// the queries; where there are few key tiles, or where a tile's keys are seen by
-// far more queries than the others' (first tokens under a window), this axis is
-// cut and the parts are joined by a third launch.
+// dQ and (dK, dV) are formed by two kernels, each in a fixed order without atomics.
+// dK and dV add up over the query heads that share a key head and over the queries.
+// How many there are differs by tile (causality, a window, first tokens that every
+// query sees) and few tiles do not fill the card, so this work is not cut by tiles:
+// it is one list of steps (a tile of queries of one head against a tile of keys), cut
+// into equal shares, one for each workgroup that the card holds; a key tile that lies
+// in two shares or more is joined by a third launch.  By tiles, with the first ones cut
+// apart, the training step below took 1.42 ms instead of 1.31.
 //
 // Precision.  bf16 inputs are operands as they are; P and dS enter as two bf16
 // operands (16 bits) for outputs in bf16 and as three for outputs in fp32: one is
 // as coarse as the output itself.  fp32 inputs use fp32 products.
+//
+// Bound.  The matrix cores and the vector instructions beside them: of S, e^S and its
+// two operands a wave issues 6.6-8.9 vector instructions for each product of 32 x 32 x
+// 16, which takes as long as 8 of them, and a wave has no other one's to fill the gaps
+// (one on a SIMD in the VJP, two in the forward: 22-29 % of a wave's time it waits for
+// its turn to issue, 31-37 % for LDS or a barrier; no bank conflicts).  bf16, 32 query and
+// 8 key heads of 128, us (a graph of calls): forward, 4 x 4096 tokens, all earlier ones
+// visible, 835 (658 TFLOP/s of 4 D a pair; its operands make 1.5 times that: 990); the
+// training step of 2 x 4096 tokens under a window of 1024 with 4 sinks 1250 (forward 230,
+// dQ 475, dK and dV 590, joins 24).  A library product of 8192 x 8192 x 8192 reaches 1287
+// TFLOP/s on this card.  Steps that got there: buffers in scalar registers, not lane by
+// lane (dK, dV 836 -> 698 us), shares instead of tiles (-> 639), two products in turn
+// that do not wait for each other (712 -> 578 with pairs converted together), masks in a
+// branch of their own, addresses formed once.  Set aside: two waves for dV and dK at 128
+// channels (more products, the same time), the next rows read before the products (1 %),
+// one code path for each LDS buffer (spills), the compiler's interleaving hints (2 % more).
 
 #include <algorithm>
 #include <type_traits>
@@ -44,6 +63,9 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kHeld = 32, kWaves = 4, kBlock = kHeld * kWaves;  // held rows of a wave, of a workgroup
+// Blocks of 128 query rows from which on a workgroup takes such a block; fewer leave
+// compute units idle.  us, a workgroup for 128 rows : for 32: 2 x 333 tokens of 6 heads of
+// 96 in fp32 104 : 25; 777 tokens of 8 heads of 80 forward 34 : 19, dQ 46 : 20.
 constexpr int64_t kWideFrom = 256;
 
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 63; }
