@@ -312,6 +312,7 @@ def gdr_cache_attention(q, k_cache, v_cache, table, lengths, *, scale=None, wind
         with _on(dev, stream):
             return gdr_cache_attention(q, k_cache, v_cache, table, lengths, scale=scale, window=window, sinks=sinks,
                                        max_len=max_len, out_dtype=out_dtype, o=o, lse=lse)
+    scale = None if scale is None else float(scale)
     key = ("cache", _meta(q), _meta(k_cache), _meta(v_cache), _meta(table), _meta(lengths), _meta(o),
            lse if lse is None or lse is True else _meta(lse), scale, window, sinks, max_len, out_dtype)
     plan = _plans.get(key) or _plan(key, lambda: _cache_attention_plan(
@@ -385,6 +386,7 @@ def gdr_attention_forward(q, k, v, *, scale=None, window=None, sinks=0, out_dtyp
             return gdr_attention_forward(q, k, v, scale=scale, window=window, sinks=sinks, out_dtype=out_dtype, o=o,
                                          cu_seqlens=cu_seqlens, max_seqlen=max_seqlen)
     dims = None if cu_seqlens is None else _ragged_dims(q, cu_seqlens, max_seqlen)
+    scale = None if scale is None else float(scale)
     key = ("forward", _meta(q), _meta(k), _meta(v), _meta(o), _meta(cu_seqlens), dims, scale, window, sinks, out_dtype)
 
     def make():
@@ -426,6 +428,7 @@ def gdr_attention_backward(q, k, v, o, lse, dout, *, scale=None, window=None, si
             return gdr_attention_backward(q, k, v, o, lse, dout, scale=scale, window=window, sinks=sinks,
                                           cu_seqlens=cu_seqlens, max_seqlen=max_seqlen)
     dims = None if cu_seqlens is None else _ragged_dims(q, cu_seqlens, max_seqlen)
+    scale = None if scale is None else float(scale)
     key = ("backward", _meta(q), _meta(k), _meta(v), _meta(o), _meta(lse), _meta(dout), _meta(cu_seqlens), dims, scale,
            window, sinks)
 

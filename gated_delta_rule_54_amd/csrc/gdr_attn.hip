@@ -970,7 +970,9 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Parts parts)
   const int64_t total = static_cast<int64_t>(Steps<R, BLOCK>(s.n, a.Hq / a.Hk, a.window, a.sinks).seen(at.tile)) * (a.Hq / a.Hk);
   const int64_t begin = end - 1 - at.step;
   if (begin < end - share || begin + total <= end) return;
-  const int more = static_cast<int>((begin + total - end + share - 1) / share);
+  // within the workspace also where offsets changed under the call
+  const int more = static_cast<int>(min((begin + total - end + share - 1) / share,
+                                        static_cast<int64_t>(gridDim.x - 1 - blockIdx.x)));
   const int which = blockIdx.y / (BLOCK / KEYS), key0 = blockIdx.y % (BLOCK / KEYS) * KEYS;
   const int64_t kp = static_cast<int64_t>(a.Hk) * a.D;
   for (int x = threadIdx.x; x < KEYS * UNITS; x += 256) {

@@ -21,6 +21,7 @@ int per16(int32_t dtype) { return dtype == GDR_BF16 ? 8 : 4; }
 gdr_status done(hipError_t e) { return e == hipSuccess ? GDR_OK : gdr::record_hip_error(e); }
 
 constexpr int64_t kMaxRows = 0x7fffffffLL;
+constexpr int64_t kMaxT = (int64_t(1) << 22) - 128;  // tokens of a sequence
 constexpr int64_t kMaxLen = int64_t(1) << 30;  // tokens of a sequence in a cache
 
 // A row distance: 0 (dense), or at least the row, in whole 16-byte units.  Where tiles
@@ -210,9 +211,9 @@ gdr_status check(const gdr_attention_problem* p, int64_t rows) {
   if (p->Hq % p->Hk || !(p->scale > 0.f) || std::isinf(p->scale)) return GDR_ERR_BAD_SHAPE;
   if (gdr_status st = check_dim(p->D); st != GDR_OK) return st;
   if (!known(p->io_dtype) || !known(p->out_dtype)) return GDR_ERR_UNSUPPORTED;
-  if (p->B > 65535 || p->Hq > 65535 || p->T > (1 << 22) || rows > kMaxRows) return GDR_ERR_UNSUPPORTED;
-  // a launch has at most 2^32 threads
-  if (p->B * p->Hq * ((p->T + 127) / 128) > (1 << 23)) return GDR_ERR_UNSUPPORTED;
+  // a grid has less than 2^16 blocks (of 64 rows or more) and 2^32 threads
+  if (p->B > 65535 || p->Hq > 65535 || p->T > kMaxT || rows > kMaxRows) return GDR_ERR_UNSUPPORTED;
+  if (p->B * p->Hq * ((p->T + 127) / 128) > (1 << 22)) return GDR_ERR_UNSUPPORTED;
   const int64_t q = static_cast<int64_t>(p->Hq) * p->D, k = static_cast<int64_t>(p->Hk) * p->D;
   return first_of({check_row(p->q_row, q, p->io_dtype, kMaxRow), check_row(p->k_row, k, p->io_dtype, kMaxRow),
                    check_row(p->v_row, k, p->io_dtype, kMaxRow)});
@@ -220,7 +221,7 @@ gdr_status check(const gdr_attention_problem* p, int64_t rows) {
 // B * T, where it is no larger than it may be
 int64_t dense_rows(const gdr_attention_problem* p) {
   if (!p || p->B < 0 || p->T < 0) return 0;
-  return p->B > 65535 || p->T > (1 << 22) ? kMaxRows + 1 : p->B * p->T;
+  return p->B > 65535 || p->T > kMaxT ? kMaxRows + 1 : p->B * p->T;
 }
 gdr::AttnArgs args_of(const gdr_attention_problem* p, int64_t rows) {
   gdr::AttnArgs a{};

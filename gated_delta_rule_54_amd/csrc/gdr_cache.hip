@@ -443,8 +443,9 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheAttnArgs a, int pi
   const int D = a.cache.D, units = D / 4, rows = 256 / units, lane = threadIdx.x & 63;
   // a sequence without a visible token has no pieces
   const int2 mine = visible(a, b).count ? Parts(a, pieces, 0, 0).pieces[b] : make_int2(0, 0);
-  const int n = mine.y;
-  const Parts part(a, pieces, mine.x, static_cast<int>(head - b * a.Hq));
+  // within the workspace also where lengths changed under the call
+  const int n = max(0, min(mine.y, min(kMaxPieces, pieces)));
+  const Parts part(a, pieces, max(0, min(mine.x, pieces - n)), static_cast<int>(head - b * a.Hq));
   const float c2 = a.scale * kLog2e;
   float2 st[kMaxPieces / 64];
   float m = -INFINITY;

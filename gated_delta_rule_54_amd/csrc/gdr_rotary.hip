@@ -19,6 +19,8 @@
 // but 2777 rows that are still in a cache then take 15-17 instead of 12, and what is
 // stored is read next.
 
+#include <algorithm>
+
 #include "gdr_attn.h"
 #include "gdr_device.h"
 
@@ -75,14 +77,13 @@ __device__ __forceinline__ int pair_axis(const RotArgs& a, int i) {
   return x;
 }
 
+// Rows row0 .. row0 + n - 1.
 template <typename TI, typename TO>
-__global__ __launch_bounds__(256) void rotary_kernel(RotArgs a, int tokens) {
+__device__ __forceinline__ void rotary_rows(const RotArgs& a, int64_t row0, int n) {
   __shared__ float2 turn[kMaxTokens * kMaxPairs];
   __shared__ int64_t slot[kMaxTokens];  // a row's element offset in the cache; -1: none
   __shared__ int64_t place[kMaxTokens];
   __shared__ int live[kMaxTokens];
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * tokens;
-  const int n = static_cast<int>(min(static_cast<int64_t>(tokens), a.rows - row0));
   const int tid = threadIdx.x, half = a.R / 2;
 
   if (a.append) {
@@ -188,11 +189,21 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotArgs a, int tokens) {
 }
 
 template <typename TI, typename TO>
+__global__ __launch_bounds__(256) void rotary_kernel(RotArgs a, int tokens) {
+  const int64_t step = static_cast<int64_t>(gridDim.x) * tokens;
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * tokens; row0 < a.rows; row0 += step) {
+    rotary_rows<TI, TO>(a, row0, static_cast<int>(min(static_cast<int64_t>(tokens), a.rows - row0)));
+    __syncthreads();  // the rows' turns and places are read
+  }
+}
+
+template <typename TI, typename TO>
 hipError_t launch(const RotArgs& a, hipStream_t st) {
   // a step of single tokens spreads over the card, many rows share a workgroup
   const int64_t most = (a.rows + 1023) / 1024;
   const int tokens = static_cast<int>(most < kMaxTokens ? (most < 1 ? 1 : most) : kMaxTokens);
-  const int64_t blocks = (a.rows + tokens - 1) / tokens;
+  // a launch has less than 2^32 threads
+  const int64_t blocks = std::min<int64_t>((a.rows + tokens - 1) / tokens, 1 << 22);
   rotary_kernel<TI, TO><<<dim3(static_cast<unsigned>(blocks)), 256, 0, st>>>(a, tokens);
   return hipGetLastError();
 }

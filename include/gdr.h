@@ -512,8 +512,9 @@ gdr_status gdr_cache_attention(const gdr_cache_attention_problem* p, const void*
  * +Inf, or all -Inf, give NaN; an Inf in v or dout may come out as NaN, and Inf or
  * NaN in a token's v, k, q or dout may reach tokens of its sequence that are
  * masked from it but share a tile of 64 with ones that are not.  B and Hq are at
- * most 65535, T at most 2^22, a row at most 2^22 elements, B * Hq * ceil(T / 128)
- * at most 2^23, token rows at most 2^31 - 1 (else GDR_ERR_UNSUPPORTED). */
+ * most 65535, T at most 2^22 - 128, a row, with its gap, at most 2^22 elements, B *
+ * Hq * ceil(T / 128) at most 2^22, token rows at most 2^31 - 1 (else
+ * GDR_ERR_UNSUPPORTED). */
 typedef struct gdr_attention_problem {
   int64_t B, T;
   int32_t Hq, Hk, D;
@@ -528,7 +529,8 @@ gdr_status gdr_attention_forward(const gdr_attention_problem* p, const void* q, 
                                  float* lse, void* hip_stream);
 gdr_status gdr_attention_forward_varlen(const gdr_attention_problem* p, const int64_t* cu_seqlens, const void* q,
                                         const void* k, const void* v, void* o, float* lse, void* hip_stream);
-/* `rows`: token rows of q (B * T, or a ragged batch's): they size the workspace. */
+/* `rows`: token rows of q (B * T, or a ragged batch's): they size the workspace, and
+ * every offset lies in [0, rows]. */
 gdr_status gdr_attention_backward_workspace(const gdr_attention_problem* p, int64_t rows, size_t* bytes);
 gdr_status gdr_attention_backward(const gdr_attention_problem* p, const void* q, const void* k, const void* v,
                                   const void* o, const float* lse, const void* dout, void* dq, void* dk, void* dv,

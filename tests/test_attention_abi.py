@@ -206,7 +206,7 @@ def test_cache_attention_arguments():
     (dict(D=24), 3), (dict(D=288), 3), (dict(io_dtype=2), 3), (dict(out_dtype=2), 3), (dict(window=-1), 2),
     (dict(sinks=-1), 2), (dict(scale=0.0), 2), (dict(scale=float("nan")), 2), (dict(scale=float("inf")), 2),
     (dict(q_row=248), 2), (dict(k_row=132), 4), (dict(v_row=(1 << 22) + 8), 3), (dict(B=70000), 3),
-    (dict(T=(1 << 22) + 1), 3), (dict(B=1 << 62, T=1 << 62), 3), (dict(B=2048, Hq=64, T=16384), 3),
+    (dict(T=(1 << 22) - 127), 3), (dict(B=1 << 62, T=1 << 62), 3), (dict(B=512, Hq=64, T=16385), 3),
     (dict(Hq=70000, Hk=70000), 3),
 ])
 def test_bad_attention(kw, status):
@@ -240,6 +240,14 @@ def test_attention_arguments():
     assert bwd(att(), ws=None, nws=0) == 1 and bwd(att(), nws=n.value - 1) == 5
     assert B.lib().gdr_attention_backward_workspace(ctypes.byref(att()), 200, None) == 1
     assert B.lib().gdr_attention_forward(None, *[FAKE] * 5, None) == 1
+
+
+def test_the_largest_problems():
+    n = ctypes.c_size_t(0)
+    for kw in (dict(B=1, T=(1 << 22) - 128), dict(B=512, Hq=64, T=16384)):
+        p = att(**kw)
+        assert B.lib().gdr_attention_backward_workspace(ctypes.byref(p), p.B * p.T, ctypes.byref(n)) == 0
+        assert n.value >= p.B * p.T * p.Hq * 4
 
 
 def test_ragged_workspace_follows_the_rows():

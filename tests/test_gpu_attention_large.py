@@ -128,6 +128,18 @@ def test_rotary_past_32_bits():
     assert z is y and ((y[-5:].float() - x[-5:].float()).abs() <= 2.0 ** -6 * x[-5:].float().abs().amax()).all()
 
 
+def test_rotary_of_many_rows():
+    """More rows than a launch of one workgroup for each two can have."""
+    rows = 17_000_001
+    x = randn(41, rows, 1, 16)
+    pos = torch.arange(rows, device="cuda") % 1000
+    y, _ = gdr.gdr_rotary_forward(x, None, pos, dev(freqs(16)), out_dtype=BF)
+    for at in (slice(0, 9), slice(8388600, 8388620), slice(rows - 9, rows)):
+        close(y[at], host(x[at]), host(pos[at]).astype(np.int64), freqs(16), BF)
+    small, _ = gdr.gdr_rotary_forward(x[-1000:], None, pos[-1000:], dev(freqs(16)), out_dtype=BF)
+    assert torch.equal(y[-1000:], small)
+
+
 def test_two_graphs_of_one_pool():
     """Two captured training steps and a decoding step that share a memory pool,
     replayed in turn with other inputs and eager calls between."""
