@@ -7,13 +7,13 @@
 // sum O of its own keys, rescaled when m grows, and (m, l, O) of disjoint sets of
 // keys join as O = sum_i e^{m_i - m} O_i.
 //
-// Layout.  A wave takes tiles of keys (32 in bf16, 16 in fp32) for up to 16
+// Layout.  A wave takes tiles of keys (32 in bf16 up to 128 channels, else 16) for up to 16
 // query heads that share a key head, and needs no LDS for them.  Scores come out
 // transposed (keys x queries): a lane holds 4 keys of a 16-key product for one
 // query, and these are, element by element, the summed index of the product
 // with V, whose order is free.  K rows are that product's operand as they lie in
 // memory (16 bytes a lane); V's operand runs over keys, so a lane loads 16 bytes
-// of each of its rows and transposes 8 x 8 values in its registers.
+// of each of its rows and transposes up to 8 x 8 values in its registers.
 //
 // Which keys are visible is a list of places without holes (sinks, then the
 // window); a page that is not there leaves holes, masked key by key.  The lists of

@@ -132,6 +132,17 @@ def test_many_sequences():
     check(list(np.random.default_rng(9).integers(0, 90, 700)), 2, 1, 32)
 
 
+@pytest.mark.parametrize("io,D", [(BF, 64), (BF, 256), (F, 48)])
+def test_more_sequences_than_the_card_holds_pieces(io, D):
+    """Cut, with more pieces than the card holds at once; one sequence far longer than
+    the others, and empty ones."""
+    r = np.random.default_rng(12)
+    lengths = [int(n) for n in r.integers(0, 120, 290)]
+    lengths[7], lengths[8:12] = 5000, [0, 64, 65, 0]
+    check(lengths, 4, 2, D, io=io)
+    check(lengths, 4, 2, D, io=io, window=70, sinks=3)
+
+
 def test_large_scores():
     """A softmax that is nearly one key: weights over many decades."""
     check([900, 77], 4, 2, 64, scale=3.0, out=BF)
