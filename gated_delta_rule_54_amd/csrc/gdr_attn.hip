@@ -63,10 +63,6 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kHeld = 32, kWaves = 4, kBlock = kHeld * kWaves;  // held rows of a wave, of a workgroup
-// Blocks of 128 query rows from which on a workgroup takes such a block; fewer leave
-// compute units idle.  us, a workgroup for 128 rows : for 32: 2 x 333 tokens of 6 heads of
-// 96 in fp32 104 : 25; 777 tokens of 8 heads of 80 forward 34 : 19, dQ 46 : 20.
-constexpr int64_t kWideFrom = 256;
 
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 63; }
 
@@ -1014,11 +1010,19 @@ size_t parts_of(const AttnArgs& a, int shares, Parts* p) {
   return delta + (shares > 1 ? static_cast<size_t>(shares) * 4 * kHeld * kBlocks<T, DP> * DP * sizeof(float) : 0);
 }
 
-// Whether the kernels that hold queries give each wave 32 of its own: where that
-// fills the card, or where 128 rows of both tensors do not fit LDS.
+// Whether the kernels that hold queries give each wave 32 of its own: where 128 rows of
+// both tensors do not fit LDS, or from so many blocks of 128 query rows on; fewer leave
+// compute units idle.  us, 32 of its own : the same 32.  bf16, 64 channels forward: 192
+// blocks 40 : 25, 256 blocks 18.5 : 21.8; 96 channels, 256 blocks 70 : 87; 128 channels,
+// 128 blocks 39 : 30, 192 blocks 54 : 57.  256 channels (whose narrow tile has one
+// buffer): 64 blocks 44 : 49, 128 blocks 77 : 106, 256 blocks 143 : 360.  fp32, 64
+// channels: training step, 512 blocks 865 : 928, forward, 1024 blocks 351 : 515; 128
+// channels (whose wide kernel spills): 256 blocks 264 : 134, 512 blocks 538 : 446.
 template <typename T, int DP> constexpr bool kNarrow = 256 * DP * sizeof(T) <= (128 << 10);
+template <typename T, int DP> constexpr int64_t kWideFrom = sizeof(T) == 2 ? (DP <= 128 ? 256 : 64) : DP <= 64 ? 256 : 1024;
+template <typename T, int DP>
 bool wide(const AttnArgs& a) {
-  return a.B * a.Hq * ceil_div(a.T, kBlock) > kWideFrom;
+  return a.B * a.Hq * ceil_div(a.T, kBlock) >= kWideFrom<T, DP>;
 }
 
 template <typename T, typename TO, int DP, bool WIDE>
@@ -1032,7 +1036,7 @@ hipError_t fwd(const AttnArgs& a, hipStream_t st) {
 template <typename T, typename TO, int DP>
 hipError_t fwd(const AttnArgs& a, hipStream_t st) {
   if constexpr (kNarrow<T, DP>)
-    if (!wide(a)) return fwd<T, TO, DP, false>(a, st);
+    if (!wide<T, DP>(a)) return fwd<T, TO, DP, false>(a, st);
   return fwd<T, TO, DP, true>(a, st);
 }
 
@@ -1049,7 +1053,7 @@ template <typename T, typename TO, int DP>
 hipError_t bwd(const AttnArgs& a, hipStream_t st) {
   constexpr int NP = sizeof(TO) == 2 ? 2 : 3;
   hipError_t e;
-  if constexpr (kNarrow<T, DP>) e = wide(a) ? dq<T, TO, DP, true>(a, st) : dq<T, TO, DP, false>(a, st);
+  if constexpr (kNarrow<T, DP>) e = wide<T, DP>(a) ? dq<T, TO, DP, true>(a, st) : dq<T, TO, DP, false>(a, st);
   else e = dq<T, TO, DP, true>(a, st);
   if (e != hipSuccess) return e;
   const int shares = shares_for<T, DP>(a);
