@@ -257,10 +257,12 @@ __device__ __forceinline__ void split(const float* p, bf16x8 (&out)[NP]) {
 
 // acc[t] += (channels 32 t .. + 31 of tile rows row0 .. + 31)^T x p, p as by_rows
 // gives it: lane (held row) then has channels 32 t + 4 (lane / 32) + walked(i).  With
-// MORE, more += the same of y, as one bf16 operand.
+// MORE, more += the same of y, as one bf16 operand.  half: the bytes from a tile's row
+// to the one 16 rows on.
 template <typename L, int NP, bool MORE = false>
 __device__ __forceinline__ void by_columns(f32x16 (&acc)[L::DP / 32], const Lane<L>& at, const char* lds, int row0,
-                                           const float (&p)[16], f32x16* more = nullptr, const float* y = nullptr) {
+                                           const float (&p)[16], f32x16* more = nullptr, const float* y = nullptr,
+                                           int half = 16 * L::PITCH) {
   constexpr int NT = L::DP / 32;
   if constexpr (L::PER == 8) {
 #pragma unroll
@@ -271,7 +273,7 @@ __device__ __forceinline__ void by_columns(f32x16 (&acc)[L::DP / 32], const Lane
       bf16x8 x[NT];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const char* from = lds + ((row0 + 16 * k) * L::PITCH + (t >> 2) * 256);
+        const char* from = lds + (row0 * L::PITCH + k * half + (t >> 2) * 256);
         const bf16x4 a = __builtin_bit_cast(
             bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(from + at.col[t & 3][0])));
         const bf16x4 b = __builtin_bit_cast(
@@ -297,7 +299,8 @@ __device__ __forceinline__ void by_columns(f32x16 (&acc)[L::DP / 32], const Lane
       for (int t = 0; t < NT; ++t) {
         const int r = walked(i) + 4 * h;
         const float x = *reinterpret_cast<const float*>(
-            lds + at.one + row0 * L::PITCH + r * L::PITCH + (((8 * t + (d >> 2)) ^ L::mix(r)) << 4) + (d & 3) * 4);
+            lds + at.one + (row0 + (r & 15)) * L::PITCH + (i >> 3) * half +
+            (((8 * t + (d >> 2)) ^ L::mix(r)) << 4) + (d & 3) * 4);
         acc[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(x, p[i], acc[t], 0, 0, 0);
         if constexpr (MORE) more[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(x, y[i], more[t], 0, 0, 0);
       }
@@ -383,6 +386,32 @@ template <typename T, int DP> constexpr int kBlocks = kApart<T, DP> ? 2 : 4;
 // Workgroups of these kernels on a compute unit.
 template <typename T, int DP> constexpr int kResident = sizeof(T) == 2 && DP <= 64 ? 2 : 1;
 constexpr int kBoth = 0, kFirst = 1, kSecond = 2;  // what a wave forms
+
+// Rows of a tile of which a wave's mask leaves nothing: their weights are 0, but 0 times
+// an Inf or NaN in them is NaN, so they may not enter a product.  The VJP's kernels
+// branch around such 32 rows (0: no zeros), or, where a branch makes the compiler move
+// or spill sums, take zeros in their place, which lie behind the tiles: 32 rows of
+// them, or 16 that are read twice where LDS holds no more.  us, neither : branch : zeros.
+// dK, dV: fp32, 2 x 1024 tokens of 32 heads of 128 386 : 502 : 408; 700 of 16 heads of
+// 256 424 : 517 : 340; 2 x 1024 of 16 heads of 64 112 : 113 : 125; bf16, 2 x 2048 of 16
+// heads of 256 460 : 444 : 492 (in fp32 out 452 : 477 : 472).  dQ, at the first two
+// 371 : 354 : 464, 457 : 554 : 494, bf16, 777 tokens of 8 heads of 80 23.7 : 26.5 : 24.1.
+template <typename T, int DP, bool WIDE>
+constexpr int kZerosDq = sizeof(T) == 2 ? (WIDE ? 0 : 16) : DP > 128 ? 16 : 0;
+template <typename T, int DP>
+constexpr int kZerosDkv = sizeof(T) == 2 || DP <= 64 ? 0 : DP <= 128 ? 32 : 16;
+template <typename L, int ZEROS> __device__ __forceinline__ void clear_zeros(char* lds) {
+  for (int i = threadIdx.x * 16; i < ZEROS * L::PITCH; i += 256 * 16)
+    *reinterpret_cast<u32x4*>(lds + L::BUFS * L::PAIR + i) = u32x4{0, 0, 0, 0};
+}
+// Where by_columns finds rows row0 .. of a tensor's tile, or with `none` the zeros.
+template <typename L, int ZEROS>
+__device__ __forceinline__ const char* rows_or_zeros(const Lane<L>& at, const char* lds, int row0, int tensor, bool none) {
+  return ZEROS && none ? lds + (L::BUFS * L::PAIR - at.one - row0 * L::PITCH) : lds + tensor;
+}
+template <typename L, int ZEROS> __device__ __forceinline__ int half_of(bool none) {
+  return ZEROS == 16 && none ? 0 : 16 * L::PITCH;
+}
 
 // The layout of the kernels that hold queries.  WIDE: each of N waves holds 32
 // queries of its own and walks all rows of a tile.  Otherwise all hold the same 32, and
@@ -553,9 +582,10 @@ template <typename T, typename TO, int DP, int NP, bool WIDE>
 __global__ __launch_bounds__(256, (kResident<T, DP>)) void attn_dq_kernel(AttnArgs a) {
   using C = Dq<T, TO, DP, WIDE>;
   using L = typename C::L;
-  constexpr int NT = DP / 32, N = C::N, SUB = WIDE ? L::ROWS / 32 : 1;
-  __shared__ __align__(16) char lds[L::BUFS * L::PAIR];
+  constexpr int NT = DP / 32, N = C::N, SUB = WIDE ? L::ROWS / 32 : 1, ZEROS = kZerosDq<T, DP, WIDE>;
+  __shared__ __align__(16) char lds[L::BUFS * L::PAIR + ZEROS * L::PITCH];
   __shared__ float stat[N][32];
+  clear_zeros<L, ZEROS>(lds);
   const int h = blockIdx.x, kh = h / (a.Hq / a.Hk), lane = lane_id();
   const int wave = wave_id() % N;
   const Span s = span(a, blockIdx.z);
@@ -626,6 +656,8 @@ __global__ __launch_bounds__(256, (kResident<T, DP>)) void attn_dq_kernel(AttnAr
       const bool all = mask.all(q0, q1, j0, j0 + 32 * SUB - 1);
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
+        const bool none = mask.none(q0, q1, j0 + 32 * u, j0 + 32 * u + 31);
+        if (ZEROS == 0 && none) continue;
         f32x16 c, dp;
         float x[16], p[16];
         if constexpr (SECOND) {
@@ -649,7 +681,8 @@ __global__ __launch_bounds__(256, (kResident<T, DP>)) void attn_dq_kernel(AttnAr
         if constexpr (C::FIX && !SECOND)
 #pragma unroll
           for (int i = 0; i < 16; ++i) off += x[i];
-        by_columns<L, SECOND ? 1 : NP, PK>(acc, at, lds, 32 * u, x, pk, p);
+        by_columns<L, SECOND ? 1 : NP, PK>(acc, at, rows_or_zeros<L, ZEROS>(at, lds, 32 * u, 0, none), 32 * u, x, pk, p,
+                                           half_of<L, ZEROS>(none));
       }
       if constexpr (L::BUFS == 1) __syncthreads();
       if (it + 1 < count) ks.store(lds + fill), vs.store(lds + fill + L::BYTES);
@@ -829,9 +862,10 @@ template <typename T, typename TO, int DP, int NP>
 __global__ __launch_bounds__(256, (kResident<T, DP>)) void attn_dkv_kernel(AttnArgs a, Parts parts) {
   constexpr int N = kBlocks<T, DP>, BLOCK = kHeld * N;
   using L = Tile<T, DP>;
-  constexpr int NT = DP / 32, R = L::ROWS;
-  __shared__ __align__(16) char lds[2 * L::PAIR];
+  constexpr int NT = DP / 32, R = L::ROWS, ZEROS = kZerosDkv<T, DP>;
+  __shared__ __align__(16) char lds[2 * L::PAIR + ZEROS * L::PITCH];
   __shared__ __align__(16) float stat[2][2][R];
+  clear_zeros<L, ZEROS>(lds);
   const int group = a.Hq / a.Hk, lane = lane_id(), wave = wave_id() % N;
   const int64_t share = uniform(share_of<R, BLOCK>(a, gridDim.x));
   Place<R, BLOCK> at(a, share * blockIdx.x);
@@ -913,6 +947,8 @@ __global__ __launch_bounds__(256, (kResident<T, DP>)) void attn_dkv_kernel(AttnA
         const float* lse = stat[it & 1][0] + 4 * (lane >> 5);
 #pragma unroll
         for (int u = 0; u < R / 32; ++u) {
+          const bool none = mask.none(i0 + 32 * u, i0 + 32 * u + 31, j0, j1);
+          if (ZEROS == 0 && none) continue;
           f32x16 c, dp;
           float p[16], y[16];
           if constexpr (KEYS) by_rows2<L>(mine, lds, lds + L::BYTES, 32 * u, 32 * u, kf, vf, c, dp);
@@ -928,8 +964,13 @@ __global__ __launch_bounds__(256, (kResident<T, DP>)) void attn_dkv_kernel(AttnA
             for (int i = 0; i < 16; ++i)
               if (!mask.sees(i0 + 4 * (lane >> 5) + 32 * u + walked(i), kj)) p[i] = 0.f, y[i] = 0.f;
           }
-          if constexpr (VALUES) by_columns<L, NP>(dv, mine, lds + L::BYTES, 32 * u, p);
-          if constexpr (KEYS) by_columns<L, NP>(dk, mine, lds, 32 * u, y);
+          const int half = half_of<L, ZEROS>(none);
+          if constexpr (VALUES)
+            by_columns<L, NP>(dv, mine, rows_or_zeros<L, ZEROS>(mine, lds, 32 * u, L::BYTES, none), 32 * u, p, nullptr,
+                              nullptr, half);
+          if constexpr (KEYS)
+            by_columns<L, NP>(dk, mine, rows_or_zeros<L, ZEROS>(mine, lds, 32 * u, 0, none), 32 * u, y, nullptr, nullptr,
+                              half);
         }
         if (it + 1 < count) store(it + 1 & 1);
         mine.flip();
