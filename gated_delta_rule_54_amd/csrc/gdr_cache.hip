@@ -36,6 +36,7 @@
 #include <algorithm>
 
 #include "gdr_attn.h"
+#include "gdr_cache_pieces.h"
 #include "gdr_device.h"
 
 namespace gdr {
@@ -50,9 +51,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kWaves = 4;
-constexpr int kMaxPieces = 256;           // of one sequence
 constexpr int kMaxCut = 512;              // sequences of a batch that is cut
-constexpr int64_t kLeast = 64;            // keys of a piece at least
 
 // Workgroups that a compute unit holds at once (the registers that a wave needs).
 constexpr int held_workgroups(bool bf16, int D) { return D <= 64 ? 3 : D <= 128 || bf16 ? 2 : 1; }
@@ -104,9 +103,7 @@ __device__ __forceinline__ Pieces find_piece(const CacheAttnArgs& a, int f, int 
     sum += __shfl_xor(sum, s, 64);
     most = max(most, __shfl_xor(most, s, 64));
   }
-  const uint32_t even = static_cast<uint32_t>(ceil(sum / static_cast<double>(slots)));
-  uint32_t per = max(static_cast<uint32_t>(kLeast), max(even, (most + kMaxPieces - 1) / kMaxPieces));
-  per = (per + tile - 1) / tile * tile;
+  uint32_t per = piece_keys(sum, most, slots, tile);
   for (int again = 0; fit && again < 16; ++again) {
     int n = 0;
 #pragma unroll
