@@ -33,6 +33,8 @@ SYMBOLS = ("gdr_keeps_chunks", "gdr_forward_workspace", "gdr_backward_workspace"
            "gdr_attention_forward_varlen", "gdr_attention_backward_workspace", "gdr_attention_backward",
            "gdr_attention_backward_varlen", "gdr_profile_enable", "gdr_profile_read",
            "gdr_status_str", "gdr_last_hip_error", "gdr_abi_version")
+# Room for the kernels of one profile read: more than the library names.
+PROFILE_KERNELS = 128
 # Every symbol include/gdr_calib.h declares (device ceilings for the benchmark).
 CALIB_SYMBOLS = ("gdr_calib_copy", "gdr_calib_mfma")
 
@@ -206,7 +208,7 @@ def gdr_profile_enable(on=True):
 def gdr_profile_read():
     """{kernel name: (total ms, launches)} of the events recorded since the
     last read; waits for them to complete."""
-    cap = 32
+    cap = PROFILE_KERNELS
     buf = (GdrKernelTime * cap)()
     n = ctypes.c_int(0)
     st = lib().gdr_profile_read(buf, cap, ctypes.byref(n))
