@@ -10,6 +10,7 @@ the tensors' device, or ``stream``.
 """
 
 import ctypes
+import operator
 
 import torch
 
@@ -61,13 +62,22 @@ class GdrAttentionProblem(ctypes.Structure):
 # A call for a few tokens is bound by the host.  What a call works out from its
 # operands' shapes, strides, types and devices, and from its options, is kept by these
 # (never by a tensor or its address): the checks that passed, the problem, the
-# workspace's size.
+# workspace's size.  Integers are kept with their class: 4.0 equals 4, but is refused.
 _plans = {}
 _MOST = 4096
 
 
 def _meta(t):
     return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+
+
+def _whole(x, name):
+    if x is None:
+        return None
+    try:
+        return operator.index(x)
+    except TypeError:
+        raise TypeError(f"{name} must be an integer, got {x!r}") from None
 
 
 def _plan(key, make):
@@ -235,7 +245,7 @@ def gdr_cache_append(k, v, k_cache, v_cache, table, lengths, freq=None, pos=None
     dims = k.shape[:2] if cu_seqlens is None else _ragged_dims(k, cu_seqlens, max_seqlen)
     section = None if section is None else tuple(section)
     key = ("append", _meta(k), _meta(v), _meta(k_cache), _meta(v_cache), _meta(table), _meta(lengths), _meta(freq),
-           _meta(pos), _meta(q), _meta(q_out), _meta(cu_seqlens), dims, section, adjacent, cycled)
+           _meta(pos), _meta(q), _meta(q_out), _meta(cu_seqlens), dims, max_seqlen.__class__, section, adjacent, cycled)
     plan = _plans.get(key) or _plan(key, lambda: _append_plan(k, v, k_cache, v_cache, table, lengths, freq, pos, q,
                                                               section, adjacent, cycled, q_out, cu_seqlens, dims, dev))
     ref, shape = plan
@@ -269,7 +279,7 @@ def _append_plan(k, v, k_cache, v_cache, table, lengths, freq, pos, q, section, 
     if rot.axes > 1 and pos is None:
         raise ValueError("pos is required where there are several axes")
     _positions(pos, rot, rows, dev)
-    B, T = dims
+    B, T = dims[0], _whole(dims[1], "max_seqlen")
     if cu_seqlens is not None and not cu_seqlens.is_contiguous():
         raise ValueError("cu_seqlens must be contiguous")
     if B != table.shape[0]:
@@ -287,11 +297,19 @@ def gdr_cache_attention_workspace(prob):
 
 
 def _span(window, sinks):
+    """The window (0: none) and the sinks, checked."""
+    window, sinks = _whole(window, "window"), _whole(sinks, "sinks")
     if window is not None and window < 1:
         raise ValueError("window must be at least 1, or None for all tokens")
-    if sinks < 0:
+    if sinks is None or sinks < 0:
         raise ValueError("sinks must be at least 0")
-    return 0 if window is None else window
+    return 0 if window is None else window, sinks
+
+
+def _lse_meta(lse):
+    if not isinstance(lse, torch.Tensor):
+        raise TypeError(f"lse must be True, None or a tensor, got {lse!r}")
+    return _meta(lse)
 
 
 def gdr_cache_attention(q, k_cache, v_cache, table, lengths, *, scale=None, window=None, sinks=0, max_len=None,
@@ -314,7 +332,8 @@ def gdr_cache_attention(q, k_cache, v_cache, table, lengths, *, scale=None, wind
                                        max_len=max_len, out_dtype=out_dtype, o=o, lse=lse)
     scale = None if scale is None else float(scale)
     key = ("cache", _meta(q), _meta(k_cache), _meta(v_cache), _meta(table), _meta(lengths), _meta(o),
-           lse if lse is None or lse is True else _meta(lse), scale, window, sinks, max_len, out_dtype)
+           lse if lse is None or lse is True else _lse_meta(lse), scale, window, sinks, max_len, window.__class__,
+           sinks.__class__, max_len.__class__, out_dtype)
     plan = _plans.get(key) or _plan(key, lambda: _cache_attention_plan(
         q, k_cache, v_cache, table, lengths, scale, window, sinks, max_len, out_dtype, o, lse, dev))
     ref, shape, nws = plan
@@ -340,13 +359,14 @@ def _cache_attention_plan(q, k_cache, v_cache, table, lengths, scale, window, si
         _want(o, "o", shape, o.dtype, dev)
     if lse is not True:
         _want(lse, "lse", shape[:3], torch.float32, dev)
-    span = _span(window, sinks)
+    window, sinks = _span(window, sinks)
+    max_len = _whole(max_len, "max_len")
     if max_len is None:
         max_len = 0
     elif max_len < 1:
         raise ValueError("max_len must be at least 1")
     prob = GdrCacheAttentionProblem(shape[0], shape[2], _dtype(out_dtype if o is None else o.dtype, "out_dtype"), cache,
-                                    _row_stride(q, "q"), max_len, span, sinks,
+                                    _row_stride(q, "q"), max_len, window, sinks,
                                     cache.D ** -0.5 if scale is None else scale)
     return ctypes.byref(prob), shape, gdr_cache_attention_workspace(prob)
 
@@ -366,9 +386,9 @@ def _attention_problem(q, k, v, scale, window, sinks, out_dtype, cu_seqlens, dim
     if cu_seqlens is not None:
         if not cu_seqlens.is_contiguous():
             raise ValueError("cu_seqlens must be contiguous")
-        T = min(T, rows[1])  # no sequence is longer than the batch
+        T = min(_whole(T, "max_seqlen"), rows[1])  # no sequence is longer than the batch
     return GdrAttentionProblem(B, T, Hq, Hk, D, _dtype(q.dtype, "q"), _dtype(out_dtype, "out_dtype"),
-                               _span(window, sinks), sinks, D ** -0.5 if scale is None and D else scale or 0.0,
+                               *_span(window, sinks), D ** -0.5 if scale is None and D else scale or 0.0,
                                _row_stride(q, "q"), _row_stride(k, "k"), _row_stride(v, "v"))
 
 
@@ -387,7 +407,8 @@ def gdr_attention_forward(q, k, v, *, scale=None, window=None, sinks=0, out_dtyp
                                          cu_seqlens=cu_seqlens, max_seqlen=max_seqlen)
     dims = None if cu_seqlens is None else _ragged_dims(q, cu_seqlens, max_seqlen)
     scale = None if scale is None else float(scale)
-    key = ("forward", _meta(q), _meta(k), _meta(v), _meta(o), _meta(cu_seqlens), dims, scale, window, sinks, out_dtype)
+    key = ("forward", _meta(q), _meta(k), _meta(v), _meta(o), _meta(cu_seqlens), dims, scale, window, sinks,
+           window.__class__, sinks.__class__, max_seqlen.__class__, out_dtype)
 
     def make():
         if o is not None:
@@ -430,7 +451,7 @@ def gdr_attention_backward(q, k, v, o, lse, dout, *, scale=None, window=None, si
     dims = None if cu_seqlens is None else _ragged_dims(q, cu_seqlens, max_seqlen)
     scale = None if scale is None else float(scale)
     key = ("backward", _meta(q), _meta(k), _meta(v), _meta(o), _meta(lse), _meta(dout), _meta(cu_seqlens), dims, scale,
-           window, sinks)
+           window, sinks, window.__class__, sinks.__class__, max_seqlen.__class__)
 
     def make():
         prob = _attention_problem(q, k, v, scale, window, sinks, o.dtype, cu_seqlens, dims)
