@@ -297,13 +297,13 @@ def gdr_cache_attention_workspace(prob):
 
 
 def _span(window, sinks):
-    """The window (0: none) and the sinks, checked."""
+    """The window (0: none), both checked."""
     window, sinks = _whole(window, "window"), _whole(sinks, "sinks")
     if window is not None and window < 1:
         raise ValueError("window must be at least 1, or None for all tokens")
     if sinks is None or sinks < 0:
         raise ValueError("sinks must be at least 0")
-    return 0 if window is None else window, sinks
+    return 0 if window is None else window
 
 
 def _lse_meta(lse):
@@ -359,14 +359,13 @@ def _cache_attention_plan(q, k_cache, v_cache, table, lengths, scale, window, si
         _want(o, "o", shape, o.dtype, dev)
     if lse is not True:
         _want(lse, "lse", shape[:3], torch.float32, dev)
-    window, sinks = _span(window, sinks)
-    max_len = _whole(max_len, "max_len")
+    window, max_len = _span(window, sinks), _whole(max_len, "max_len")
     if max_len is None:
         max_len = 0
     elif max_len < 1:
         raise ValueError("max_len must be at least 1")
     prob = GdrCacheAttentionProblem(shape[0], shape[2], _dtype(out_dtype if o is None else o.dtype, "out_dtype"), cache,
-                                    _row_stride(q, "q"), max_len, window, sinks,
+                                    _row_stride(q, "q"), max_len, window, _whole(sinks, "sinks"),
                                     cache.D ** -0.5 if scale is None else scale)
     return ctypes.byref(prob), shape, gdr_cache_attention_workspace(prob)
 
@@ -388,7 +387,8 @@ def _attention_problem(q, k, v, scale, window, sinks, out_dtype, cu_seqlens, dim
             raise ValueError("cu_seqlens must be contiguous")
         T = min(_whole(T, "max_seqlen"), rows[1])  # no sequence is longer than the batch
     return GdrAttentionProblem(B, T, Hq, Hk, D, _dtype(q.dtype, "q"), _dtype(out_dtype, "out_dtype"),
-                               *_span(window, sinks), D ** -0.5 if scale is None and D else scale or 0.0,
+                               _span(window, sinks), _whole(sinks, "sinks"),
+                               D ** -0.5 if scale is None and D else scale or 0.0,
                                _row_stride(q, "q"), _row_stride(k, "k"), _row_stride(v, "v"))
 
 
