@@ -152,8 +152,9 @@ gdr_status append(const gdr_append_problem* p, const int64_t* cu, bool ragged, c
   if (st != GDR_OK) return st;
   const int64_t rows = ragged ? p->rows : p->B * p->T;
   const bool empty = rows == 0 || p->B == 0 || p->T == 0;
-  if (!empty && (!k || !v || !kc || !vc || !lengths || (!table && c.max_pages) || (p->Hq && (!q || !qo)) ||
-                 (ragged && !cu) || (p->rot.R && !freq)))
+  // a cache without pages has no buffers: nothing is stored, q is turned all the same
+  if (!empty && (!k || !v || (c.pages && (!kc || !vc)) || !lengths || (!table && c.max_pages) ||
+                 (p->Hq && (!q || !qo)) || (ragged && !cu) || (p->rot.R && !freq)))
     return GDR_ERR_NULL_ARG;
   if (p->rot.R && p->rot.axes > 1 && !pos && !empty) return GDR_ERR_NULL_ARG;
   for (const void* ptr : {q, k, v, static_cast<const void*>(qo), static_cast<const void*>(kc),

@@ -427,8 +427,9 @@ gdr_status gdr_rotary_backward(const gdr_rotary_problem* p, const void* dq_out, 
  * max_pages], rows table_row elements apart, 0: dense) holds each sequence's
  * pages in order: place j of a sequence is slot j % page_size of page
  * table[b][j / page_size].  An entry outside [0, pages) is a page that is not
- * there: nothing is stored to it, and its tokens are not visible.  lengths
- * (device, int64 [B]) are the tokens that each sequence holds. */
+ * there: nothing is stored to it, and its tokens are not visible (with pages 0 the
+ * buffers may be NULL).  lengths (device, int64 [B]) are the tokens that each
+ * sequence holds. */
 typedef struct gdr_cache {
   int64_t pages;
   int32_t page_size, Hk, D;
