@@ -1,4 +1,4 @@
-"""How far a NaN of one token reaches in the attention VJP: the tokens that it is
+"""How far a NaN of one token reaches in attention and its VJP: the tokens that it is
 visible to (or that are visible to it), and those that share a tile of 64 with
 them; no others.
 
@@ -68,3 +68,27 @@ def test_a_token_s_nan_in_the_vjp(io, out, D, window, sinks, B):
                 assert not torch.isnan(g[1:]).any(), (which, at, name)
             if which != "v":
                 assert torch.isnan(grads[0][0, at, 0]).any()
+
+
+@pytest.mark.parametrize("B", [1, 180])
+@pytest.mark.parametrize("window,sinks", [(None, 0), (40, 3)])
+@pytest.mark.parametrize("io,out,D", [(BF, F, 64), (BF, BF, 128), (F, F, 64), (F, F, 128), (BF, BF, 256), (F, BF, 256)])
+def test_a_token_s_nan_in_the_forward(io, out, D, window, sinks, B):
+    """v: by tiles.  q and k enter scores, which are masked one by one."""
+    T, Hq, Hk = 300, 4, 2
+    how = dict(window=window, sinks=sinks, out_dtype=out)
+    t = dict(zip("qkv", (dev(a, io).expand(B, *a.shape).contiguous() for a in draw(71, T, Hq, Hk, D, io)[:3])))
+    ok = ao.seen(T, window, sinks)
+    for which in t:
+        for at in (10, 100, 200, 299):
+            bad = dict(t, **{which: t[which].clone()})
+            bad[which][0, at, 0, 5] = float("nan")
+            o, lse = gdr.gdr_attention_forward(bad["q"], bad["k"], bad["v"], **how)
+            may = {"q": np.arange(T) == at, "k": ok[:, at], "v": tiles_seen(ok)[:, at]}[which]
+            must = {"q": np.arange(T) == at, "k": ok[:, at], "v": ok[:, at]}[which]
+            heads = 1 if which == "q" else 2
+            rows = torch.isnan(o[0, :, :heads]).any(-1).cpu().numpy()
+            assert not (rows.any(1) & ~may).any() and rows[must].all(), (which, at)
+            nan = torch.isnan(lse[0, :, :heads]).cpu().numpy()
+            assert (nan == ((may & (which != "v"))[:, None])).all(), (which, at)
+            assert not torch.isnan(o[0, :, heads:]).any() and not torch.isnan(o[1:]).any(), (which, at)
