@@ -30,20 +30,22 @@
 // as coarse as the output itself.  fp32 inputs use fp32 products.
 //
 // Bound.  The matrix cores and the vector instructions beside them: of S, e^S and its
-// two operands a wave issues 6.6-8.9 vector instructions for each product of 32 x 32 x
+// two operands a wave issues 5.7-8.7 vector instructions for each product of 32 x 32 x
 // 16, which takes as long as 8 of them, and a wave has no other one's to fill the gaps
-// (one on a SIMD in the VJP, two in the forward: 22-29 % of a wave's time it waits for
-// its turn to issue, 31-37 % for LDS or a barrier; no bank conflicts).  bf16, 32 query and
+// (one on a SIMD in the VJP, two in the forward: 18-29 % of a wave's time it waits for
+// its turn to issue, 31-50 % for LDS or a barrier, there also for waves whose rows a
+// tile's mask leaves; no bank conflicts).  bf16, 32 query and
 // 8 key heads of 128, us (a graph of calls): forward, 4 x 4096 tokens, all earlier ones
 // visible, 835 (658 TFLOP/s of 4 D a pair; its operands make 1.5 times that: 990); the
-// training step of 2 x 4096 tokens under a window of 1024 with 4 sinks 1250 (forward 230,
-// dQ 475, dK and dV 590, joins 24).  A library product of 8192 x 8192 x 8192 reaches 1287
-// TFLOP/s on this card.  Steps that got there: buffers in scalar registers, not lane by
-// lane (dK, dV 836 -> 698 us), shares instead of tiles (-> 639), two products in turn
-// that do not wait for each other (712 -> 578 with pairs converted together), masks in a
-// branch of their own, addresses formed once.  Set aside: two waves for dV and dK at 128
-// channels (more products, the same time), the next rows read before the products (1 %),
-// one code path for each LDS buffer (spills), the compiler's interleaving hints (2 % more).
+// training step of 2 x 4096 tokens under a window of 1024 with 4 sinks 1254 (of a trace's
+// 1346 the forward has 234, dQ 477, dK and dV 613, joins 22).  A library product of 8192
+// x 8192 x 8192 reaches 1287 TFLOP/s on this card.  Steps that got there: buffers in
+// scalar registers, not lane by lane (dK, dV 836 -> 698 us), shares instead of tiles (->
+// 639), two products in turn that do not wait for each other (712 -> 578 with pairs
+// converted together), masks in a branch of their own, addresses formed once.  Set aside:
+// two waves for dV and dK at 128 channels (more products, the same time), the next rows
+// read before the products (1 %), one code path for each LDS buffer (spills), the
+// compiler's interleaving hints (2 % more).
 
 #include <algorithm>
 #include <type_traits>
@@ -375,12 +377,17 @@ struct KeyTiles {
 };
 
 // The VJP's kernels have two sums for their held rows (dV and dK; dS K and P K).
-// One wave forms both, for each of four blocks of 32 rows; where its registers do not
-// hold them (256 channels in bf16) two waves do, one sum each, for each of two blocks.
-// That costs the scores twice, but 2 x 2048 tokens of 16 heads of 256 take 0.96 ms
-// instead of 1.90, of which spilled registers were the most.  At 128 channels two waves
+// One wave forms both, for each of four blocks of 32 rows; where its registers are far
+// from holding them (256 channels in bf16) two waves do, one sum each, for each of two
+// blocks.  That costs the scores twice, but 2 x 2048 tokens of 16 heads of 256 take 0.98
+// ms instead of 1.90, of which spilled registers were the most.  At 128 channels two waves
 // for each block, all eight on a compute unit, took the same time (1.24 ms for the
 // training step of 2 x 4096 tokens), and fp32 up to a quarter more.
+//
+// What still spills, registers of a lane.  bf16 at 256 channels: dK, dV 48-52, the narrow
+// forward 44, the narrow dQ with fp32 outputs 192.  fp32 at 128: the wide forward 30, dK,
+// dV 12, dQ with bf16 outputs 27-166.  fp32 at 256 (where one wave forms both sums): the
+// forward 114, dQ 223-341, dK, dV 494.
 template <typename T, int DP> constexpr bool kApart = sizeof(T) == 2 && DP > 128;
 template <typename T, int DP> constexpr int kBlocks = kApart<T, DP> ? 2 : 4;
 // Workgroups of these kernels on a compute unit.
@@ -1053,12 +1060,31 @@ size_t parts_of(const AttnArgs& a, int shares, Parts* p) {
 
 // Whether the kernels that hold queries give each wave 32 of its own: where 128 rows of
 // both tensors do not fit LDS, or from so many blocks of 128 query rows on; fewer leave
-// compute units idle.  us, 32 of its own : the same 32.  bf16, 64 channels forward: 192
-// blocks 40 : 25, 256 blocks 18.5 : 21.8; 96 channels, 256 blocks 70 : 87; 128 channels,
-// 128 blocks 39 : 30, 192 blocks 54 : 57.  256 channels (whose narrow tile has one
-// buffer): 64 blocks 44 : 49, 128 blocks 77 : 106, 256 blocks 143 : 360.  fp32, 64
-// channels: training step, 512 blocks 865 : 928, forward, 1024 blocks 351 : 515; 128
-// channels (whose wide kernel spills): 256 blocks 264 : 134, 512 blocks 538 : 446.
+// compute units idle.  One bound for the forward and dQ of a type and width, between what
+// short sequences and long ones want, whose rows differ more in length.  us, 32 of its
+// own : the same 32, 8 heads, all earlier tokens visible:
+//   channels    tokens  blocks  forward      dQ
+//   bf16,  64      128     256    11 : 16      14 : 20
+//                 2048     128    51 : 30      56 : 29
+//                 2048     256    51 : 38      56 : 43
+//                 2048     512    63 : 69      83 : 75
+//   bf16, 128      128     256    14 : 27      20 : 42
+//                 2048     128    68 : 47      91 : 55
+//                 1536     192    55 : 58      75 : 70
+//                 2048     256    69 : 88      97 : 105    (96 channels alike)
+//   bf16, 256      128      64    19 : 18      25 : 23
+//                  512      32    44 : 50      49 : 37
+//                 1024      64    77 : 98      81 : 59
+//                 2048     128   140 : 196    149 : 120
+//   fp32,  64      128     256    20 : 34      26 : 46
+//                 2048     256   166 : 137    227 : 165
+//                 2048     512   288 : 268    411 : 329
+//                 2048    1024   476 : 533    711 : 651
+//   fp32, 128      128    1024   153 : 183    183 : 315
+//                 2048     512   719 : 459    763 : 596
+//                 2048    1024  1160 : 936   1304 : 1240
+// At 256 channels the narrow tile has one buffer and its forward spills; so does the wide
+// forward of fp32 at 128.
 template <typename T, int DP> constexpr bool kNarrow = 256 * DP * sizeof(T) <= (128 << 10);
 template <typename T, int DP> constexpr int64_t kWideFrom = sizeof(T) == 2 ? (DP <= 128 ? 256 : 64) : DP <= 64 ? 256 : 1024;
 template <typename T, int DP>

@@ -482,9 +482,9 @@ gdr_status gdr_cache_append_varlen(const gdr_append_problem* p, const int64_t* c
  * in a visible v may come out as NaN.
  * Lengths are read on the device; they are clamped to [0, max_len], and max_len
  * (0: max_pages * page_size, which it may not exceed) sizes the workspace and
- * the launch, so a captured call serves all lengths up to it (at most 2^30).  B *
- * Hq is at most 2^22, scale > 0, window and sinks >= 0.  Outputs must not alias
- * inputs. */
+ * the launch, so a captured call serves all lengths up to it (at most 2^30).  B
+ * and Hq are at most 65535, B * Hq at most 2^22, scale > 0, window and sinks >= 0.
+ * Outputs must not alias inputs. */
 typedef struct gdr_cache_attention_problem {
   int64_t B;
   int32_t Hq;
